@@ -255,7 +255,7 @@ def _run_own(st):
         return st["dA"], st["dB"]
     if op == "lora":
         g.run_lora(h, st["X"], st["W"], st["D"], off, st["down"], st["up"], st["ws"],
-                   ids=st["ids_gpu"], scales=st["scales"], transW=st["trans"])
+                   ids=st["ids_gpu"], scales=st["scales"], transB=st["trans"])
         return st["D"]
     # the adapters' activations and gradients in the operands' type between the calls
     g.run_grouped(h, st["X"], st["down"], st["T"], off, transB="T", scales=st["scales"])
@@ -263,7 +263,7 @@ def _run_own(st):
     g.run_grouped_wgrad(h, st["U"], st["X"], st["ddown"], off)
     g.run_grouped_wgrad(h, st["dY"], st["T"], st["dup"], off)
     g.run_lora(h, st["dY"], st["W"], st["dX"], off, st["up"], st["down"], st["ws"],
-               ids=st["ids_gpu"], scales=st["scales"], transW=flip, transDown="N", transUp="N")
+               ids=st["ids_gpu"], scales=st["scales"], transB=flip, transDown="N", transUp="N")
     return st["dX"], st["ddown"], st["dup"]
 
 
