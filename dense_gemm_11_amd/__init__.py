@@ -47,7 +47,9 @@ EXPORTS = ("gemm_create", "gemm_destroy", "gemm_run", "gemm_status_string",
            "gemm_select_variant", "gemm_stream_k_workspace_bytes", "gemm_set_workspace",
            "gemm_set_stream_k", "gemm_last_stream_k", "gemm_run_epilogue",
            "gemm_variant_pipeline", "gemm_variant_occupancy", "gemm_stream_k_status",
-           "gemm_set_stream_k_poll_limit", "gemm_run_no_alloc", "gemm_set_planning_model")
+           "gemm_set_stream_k_poll_limit", "gemm_run_no_alloc", "gemm_set_planning_model",
+           "gemm_run_grouped", "gemm_run_grouped_wgrad", "gemm_run_lora",
+           "gemm_lora_workspace_bytes", "gemm_set_group_tile", "gemm_last_group_tile")
 
 
 class GemmEpilogue(ctypes.Structure):
@@ -56,6 +58,23 @@ class GemmEpilogue(ctypes.Structure):
     _fields_ = [("bias", ctypes.c_void_p), ("activation", ctypes.c_int),
                 ("clamp", ctypes.c_int), ("clamp_lo", ctypes.c_float),
                 ("clamp_hi", ctypes.c_float)]
+
+
+class GemmGroups(ctypes.Structure):
+    """gemm_groups_t: device pointers to groups + 1 int32 offsets and to one
+    fp32 factor per group (0/None for none)."""
+    _fields_ = [("groups", ctypes.c_int), ("offsets", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p)]
+
+
+class GemmLora(ctypes.Structure):
+    """gemm_lora_t: the segments of rows and their low-rank adapters."""
+    _fields_ = [("segments", ctypes.c_int), ("offsets", ctypes.c_void_p),
+                ("ids", ctypes.c_void_p), ("adapters", ctypes.c_int), ("rank", ctypes.c_int),
+                ("scales", ctypes.c_void_p), ("trans_down", ctypes.c_int),
+                ("down", ctypes.c_void_p), ("ld_down", ctypes.c_int64),
+                ("stride_down", ctypes.c_int64), ("trans_up", ctypes.c_int),
+                ("up", ctypes.c_void_p), ("ld_up", ctypes.c_int64), ("stride_up", ctypes.c_int64)]
 
 
 class GemmError(RuntimeError):
@@ -137,6 +156,21 @@ def _load():
     lib.gemm_stream_k_status.restype = i32
     lib.gemm_set_stream_k_poll_limit.argtypes = [vp, i32]
     lib.gemm_set_stream_k_poll_limit.restype = i32
+    lib.gemm_run_grouped.argtypes = [vp, i32, i64, i64, i64, f32, vp, i64, vp, i64, i64, f32, vp,
+                                     i64, vp, i64, i32, ctypes.POINTER(GemmGroups), vp]
+    lib.gemm_run_grouped.restype = i32
+    lib.gemm_run_grouped_wgrad.argtypes = [vp, i64, i64, i64, f32, vp, i64, vp, i64, f32, vp, i64,
+                                           i64, vp, i64, i64, i32, ctypes.POINTER(GemmGroups), vp]
+    lib.gemm_run_grouped_wgrad.restype = i32
+    lib.gemm_run_lora.argtypes = [vp, i32, i64, i64, i64, f32, vp, i64, vp, i64, f32, vp, i64, vp,
+                                  i64, i32, ctypes.POINTER(GemmLora), vp, ctypes.c_size_t, vp]
+    lib.gemm_run_lora.restype = i32
+    lib.gemm_lora_workspace_bytes.argtypes = [i64, i32]
+    lib.gemm_lora_workspace_bytes.restype = ctypes.c_size_t
+    lib.gemm_set_group_tile.argtypes = [vp, i32]
+    lib.gemm_set_group_tile.restype = i32
+    lib.gemm_last_group_tile.argtypes = [vp]
+    lib.gemm_last_group_tile.restype = i32
     return lib
 
 
@@ -264,6 +298,45 @@ def gemm_set_stream_k_poll_limit(h, polls: int) -> int:
     return lib.gemm_set_stream_k_poll_limit(h, polls)
 
 
+def gemm_run_grouped(h, transB, M, N, K, alpha, A, lda, B, ldb, strideB, beta, C, ldc, D, ldd,
+                     dtype, groups, stream) -> int:
+    """Raw call: pointers and the stream are integers (0/None for NULL); groups
+    is a GemmGroups or None."""
+    gr = None if groups is None else ctypes.byref(groups)
+    return lib.gemm_run_grouped(h, transB, M, N, K, alpha, A, lda, B, ldb, strideB, beta, C, ldc,
+                                D, ldd, dtype, gr, stream)
+
+
+def gemm_run_grouped_wgrad(h, M, N, rows, alpha, A, lda, B, ldb, beta, C, ldc, strideC, D, ldd,
+                           strideD, dtype, groups, stream) -> int:
+    """Raw call: pointers and the stream are integers (0/None for NULL); groups
+    is a GemmGroups or None."""
+    gr = None if groups is None else ctypes.byref(groups)
+    return lib.gemm_run_grouped_wgrad(h, M, N, rows, alpha, A, lda, B, ldb, beta, C, ldc, strideC,
+                                      D, ldd, strideD, dtype, gr, stream)
+
+
+def gemm_run_lora(h, transB, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, D, ldd, dtype, lora,
+                  workspace, workspace_bytes, stream) -> int:
+    """Raw call: pointers and the stream are integers (0/None for NULL); lora
+    is a GemmLora or None."""
+    lo = None if lora is None else ctypes.byref(lora)
+    return lib.gemm_run_lora(h, transB, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, D, ldd, dtype,
+                             lo, workspace, workspace_bytes, stream)
+
+
+def gemm_lora_workspace_bytes(M: int, rank: int) -> int:
+    return lib.gemm_lora_workspace_bytes(M, rank)
+
+
+def gemm_set_group_tile(h, rows: int) -> int:
+    return lib.gemm_set_group_tile(h, rows)
+
+
+def gemm_last_group_tile(h) -> int:
+    return lib.gemm_last_group_tile(h)
+
+
 def attach_workspace(h, nbytes=None, device=None):
     """Allocate a stream-K workspace as a torch uint8 tensor on `device` (the
     current device by default), hand it to h and return it; the caller keeps
@@ -360,3 +433,169 @@ def bind_tensors(h, A, B, D, C=None, transA="N", transB="N", alpha=1.0, beta=0.0
     fn, args = _marshal(h, A, B, D, C, transA, transB, alpha, beta, stream, bias, activation,
                         clamp, no_alloc)
     return lambda: fn(*args)
+
+
+def _ld(t, dims=2):
+    """Leading dimension of a tensor whose last axis is contiguous."""
+    if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"expected a {dims}-D tensor with unit stride in its last axis")
+    # a single row has no stride of its own; too small a stride (an expanded
+    # tensor) is refused by the library
+    return t.stride(-2) if t.shape[-2] > 1 else max(t.shape[-1], 1)
+
+
+def _ragged_dtype(A, B, D, C):
+    """gemm_dtype_t of a ragged product's tensors."""
+    import torch
+
+    if A.dtype == torch.float32 and B.dtype == torch.float32:
+        dtype, outs = GEMM_DTYPE_F32, (torch.float32,)
+    elif A.dtype == torch.bfloat16 and B.dtype == torch.bfloat16:
+        dtype = GEMM_DTYPE_BF16_BF16 if D.dtype == torch.bfloat16 else GEMM_DTYPE_BF16_F32
+        outs = (torch.float32, torch.bfloat16)
+    else:
+        raise TypeError("A and B must both be float32 or both bfloat16")
+    if D.dtype not in outs or (C is not None and C.dtype != D.dtype):
+        raise TypeError("C and D must be float32, or both bfloat16 with bfloat16 operands")
+    return dtype
+
+
+def _device_vector(t, dtype, length, device, what):
+    """Data pointer of a contiguous 1-D device tensor (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != length or t.device != device or (
+            length > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what} must be a contiguous length-{length} {dtype} tensor on {device}")
+    return t.data_ptr()
+
+
+def _same_device(D, *tensors):
+    if any(t is not None and t.device != D.device for t in tensors):
+        raise ValueError("every tensor must be on D's device")
+
+
+def _finish(status, check, what):
+    if check and status != GEMM_OK:
+        raise GemmError(status, what)
+    return status
+
+
+def run_grouped(h, A, B, D, offsets, C=None, transB="N", scales=None, alpha=1.0, beta=0.0,
+                stream=None, check=True) -> int:
+    """gemm_run_grouped on torch tensors: for each group g, with its rows
+    offsets[g] .. offsets[g+1]-1,
+    D[rows] = alpha * scales[g] * A[rows] @ op(B[g]) + beta * C[rows].
+
+    A: M x K; B: groups x K x N ("N") or groups x N x K ("T"); C, D: M x N;
+    offsets: int32, groups + 1, on the device; scales: float32, groups, or
+    None.  Types as for run_tensors.  Rows in no group keep their values.
+    """
+    import torch
+
+    dtype = _ragged_dtype(A, B, D, C)
+    lda, ldb, ldd = _ld(A), _ld(B, 3), _ld(D)
+    M, K = A.shape
+    groups = B.shape[0]
+    Kb, N = (B.shape[1], B.shape[2]) if transB == "N" else (B.shape[2], B.shape[1])
+    if Kb != K or tuple(D.shape) != (M, N) or (C is not None and tuple(C.shape) != (M, N)):
+        raise ValueError("inconsistent grouped GEMM shapes")
+    _same_device(D, A, B, C)
+    gr = GemmGroups(groups, _device_vector(offsets, torch.int32, groups + 1, D.device, "offsets"),
+                    _device_vector(scales, torch.float32, groups, D.device, "scales"))
+    if stream is None:
+        stream = torch.cuda.current_stream(D.device).cuda_stream
+    s = lib.gemm_run_grouped(
+        h, GEMM_OP_N if transB == "N" else GEMM_OP_T, M, N, K, float(alpha), A.data_ptr(), lda,
+        B.data_ptr(), ldb, B.stride(0), float(beta), None if C is None else C.data_ptr(),
+        N if C is None else _ld(C), D.data_ptr(), ldd, dtype, ctypes.byref(gr), stream)
+    return _finish(s, check, "gemm_run_grouped")
+
+
+def run_grouped_wgrad(h, A, B, D, offsets, C=None, scales=None, alpha=1.0, beta=0.0, stream=None,
+                      check=True) -> int:
+    """gemm_run_grouped_wgrad on torch tensors: for each group g, with its rows
+    offsets[g] .. offsets[g+1]-1,
+    D[g] = alpha * scales[g] * A[rows].T @ B[rows] + beta * C[g].
+
+    A: rows x M; B: rows x N; C, D: groups x M x N; offsets and scales as for
+    run_grouped.  D[g] of an empty group is beta * C[g].
+    """
+    import torch
+
+    dtype = _ragged_dtype(A, B, D, C)
+    lda, ldb, ldd = _ld(A), _ld(B), _ld(D, 3)
+    rows, M = A.shape
+    groups, N = D.shape[0], B.shape[1]
+    if B.shape[0] != rows or tuple(D.shape) != (groups, M, N) or (
+            C is not None and C.shape != D.shape):
+        raise ValueError("inconsistent grouped GEMM shapes")
+    _same_device(D, A, B, C)
+    gr = GemmGroups(groups, _device_vector(offsets, torch.int32, groups + 1, D.device, "offsets"),
+                    _device_vector(scales, torch.float32, groups, D.device, "scales"))
+    if stream is None:
+        stream = torch.cuda.current_stream(D.device).cuda_stream
+    s = lib.gemm_run_grouped_wgrad(
+        h, M, N, rows, float(alpha), A.data_ptr(), lda, B.data_ptr(), ldb, float(beta),
+        None if C is None else C.data_ptr(), N if C is None else _ld(C, 3),
+        0 if C is None else C.stride(0), D.data_ptr(), ldd, D.stride(0), dtype, ctypes.byref(gr),
+        stream)
+    return _finish(s, check, "gemm_run_grouped_wgrad")
+
+
+def lora_workspace(rows: int, rank: int, device=None):
+    """A workspace for run_lora on up to `rows` rows and rank `rank`, as a torch
+    uint8 tensor on `device` (the current device by default); one per
+    concurrently used stream."""
+    import torch
+
+    need = gemm_lora_workspace_bytes(rows, rank)
+    return torch.empty(max(need, 256), dtype=torch.uint8, device=device or "cuda")
+
+
+def run_lora(h, A, B, D, offsets, down, up, workspace, ids=None, scales=None, C=None, transB="N",
+             transDown="T", transUp="T", alpha=1.0, beta=0.0, stream=None, check=True) -> int:
+    """gemm_run_lora on torch tensors: a shared product with one low-rank
+    adapter per segment of rows,
+    D[rows] = alpha * (A[rows] @ op(B) + scales[a] * (A[rows] @ op(down[a])) @ op(up[a]))
+              + beta * C[rows], with a = ids[segment].
+
+    A: M x K; B: K x N ("N") or N x K ("T"); C, D: M x N; down: adapters x R x K
+    ("T") or adapters x K x R ("N"); up: adapters x N x R ("T") or adapters x R
+    x N ("N"); offsets: int32, segments + 1, on the device; ids: int32,
+    segments (negative: no adapter), or None for adapter s in segment s;
+    scales: float32, adapters, or None; workspace: from lora_workspace.
+    """
+    import torch
+
+    dtype = _ragged_dtype(A, B, D, C)
+    if down.dtype != A.dtype or up.dtype != A.dtype:
+        raise TypeError("down and up must have A's dtype")
+    lda, ldb, ldd = _ld(A), _ld(B), _ld(D)
+    M, K = A.shape
+    Kb, N = (B.shape[0], B.shape[1]) if transB == "N" else (B.shape[1], B.shape[0])
+    ld_down, ld_up = _ld(down, 3), _ld(up, 3)
+    adapters, R = down.shape[0], down.shape[1] if transDown == "T" else down.shape[2]
+    if Kb != K or tuple(D.shape) != (M, N) or (C is not None and tuple(C.shape) != (M, N)) or (
+            tuple(down.shape) != ((adapters, R, K) if transDown == "T" else (adapters, K, R))) or (
+            tuple(up.shape) != ((adapters, N, R) if transUp == "T" else (adapters, R, N))):
+        raise ValueError("inconsistent low-rank adapter shapes")
+    _same_device(D, A, B, C, down, up, workspace)
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("offsets must hold segments + 1 entries")
+    segments = offsets.shape[0] - 1
+    lo = GemmLora(segments,
+                  _device_vector(offsets, torch.int32, segments + 1, D.device, "offsets"),
+                  _device_vector(ids, torch.int32, segments, D.device, "ids"), adapters, R,
+                  _device_vector(scales, torch.float32, adapters, D.device, "scales"),
+                  GEMM_OP_N if transDown == "N" else GEMM_OP_T, down.data_ptr(), ld_down,
+                  down.stride(0), GEMM_OP_N if transUp == "N" else GEMM_OP_T, up.data_ptr(), ld_up,
+                  up.stride(0))
+    if stream is None:
+        stream = torch.cuda.current_stream(D.device).cuda_stream
+    s = lib.gemm_run_lora(
+        h, GEMM_OP_N if transB == "N" else GEMM_OP_T, M, N, K, float(alpha), A.data_ptr(), lda,
+        B.data_ptr(), ldb, float(beta), None if C is None else C.data_ptr(),
+        N if C is None else _ld(C), D.data_ptr(), ldd, dtype, ctypes.byref(lo),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream)
+    return _finish(s, check, "gemm_run_lora")

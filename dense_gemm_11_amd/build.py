@@ -28,7 +28,9 @@ SOURCES = ["api.hip", "inst_bf16.hip", "inst_bf16_dma.hip", "inst_bf16_dma_out.h
            "inst_epi_bf16_out.hip", "inst_sk_bf16_256.hip", "inst_sk_bf16_128.hip",
            "inst_sk_f32.hip", "inst_bf16_dma_tiles.hip", "inst_bf16_dma_192.hip",
            "inst_bf16_dma_out_tiles.hip", "inst_epi_tiles.hip",
-           "inst_epi_tiles_bf16_out.hip", "inst_small.hip"]
+           "inst_epi_tiles_bf16_out.hip", "inst_small.hip", "ragged_api.hip",
+           "inst_rag_rows_bf16.hip", "inst_rag_lora_bf16.hip", "inst_rag_k_bf16.hip",
+           "inst_rag_f32.hip", "inst_lora_shrink.hip"]
 
 
 def hipcc() -> str:

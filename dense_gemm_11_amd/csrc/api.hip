@@ -12,20 +12,9 @@
 
 #include "dense_gemm.h"
 #include "common.hpp"
+#include "handle.hpp"
 #include "variants.hpp"
 #include "sk_ranges.hpp"
-
-struct gemm_handle_s {
-    int forced_variant;  // -1: automatic selection
-    int last_variant;
-    int stream_k_mode;   // -1: automatic, 0: never, 1: whenever the variant and workspace allow
-    int last_stream_k;   // stream-K workgroups of the last call (0: data-parallel)
-    void* ws;            // caller-owned device workspace for stream-K, or null
-    size_t ws_bytes;
-    int sk_spin;         // polls a stream-K finisher spends on each contributor
-    int log;             // GEMM_LOG: one line per call on stderr
-    int fail_launch;     // GEMM_DEBUG_FAIL_LAUNCH: report GEMM_ERR_HIP instead of launching
-};
 
 namespace dg {
 
@@ -101,8 +90,6 @@ int find_variant(const char* name)
     return -1;
 }
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 // Per-device caches are indexed by device ordinal; devices beyond this many
 // are answered without caching.
 constexpr int MAX_DEVICES = 64;
@@ -121,6 +108,8 @@ int current_device()
     if (hipGetDevice(&dev) != hipSuccess) return -1;
     return dev;
 }
+
+}  // namespace
 
 // Compute units of the current device (cached per device; entry points may
 // be called from several threads at once, so the cache is atomic and a
@@ -141,6 +130,8 @@ int device_cus()
     }
     return n;
 }
+
+namespace {
 
 // Per-shape selection.  Large tiles give the most reuse per LDS byte
 // (the tile's input intensity grows with BM*BN/(BM+BN), "GEMM on NVIDIA
@@ -305,11 +296,6 @@ int stream_k_grid(const Variant& v, int64_t M, int64_t N, int64_t K, int mode, s
     return (int)best_g;
 }
 
-bool aligned_to(const void* p, int64_t bytes)
-{
-    return (reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes) == 0;
-}
-
 // The direct-to-LDS kernels address a workgroup's operand panel with 32-bit
 // byte offsets from the panel start: a k-contiguous panel spans (rows-1) rows
 // of ld plus K elements (plus one step of overhang), an mn-contiguous one K-1
@@ -322,12 +308,6 @@ bool dma_offsets_fit(const Variant& v, bool a_kc, bool b_kc, int64_t K, int64_t 
     const int64_t span_b = b_kc ? (v.bn - 1) * ldb + kk : kk * ldb + v.bn;
     const int64_t lim = ((int64_t)1 << 32) - 64;
     return span_a * es < lim && span_b * es < lim;
-}
-
-bool ranges_overlap(const void* a, int64_t abytes, const void* b, int64_t bbytes)
-{
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return a0 < b0 + (uintptr_t)bbytes && b0 < a0 + (uintptr_t)abytes;
 }
 
 // Device address of each device's copy of `scratch` (null until set up).
@@ -944,7 +924,7 @@ gemm_status_t gemm_create(gemm_handle_t* out)
     };
     gemm_handle_t h = new (std::nothrow) gemm_handle_s{
         -1, -1, -1, 0, nullptr, 0, dg::SK_SPIN_DEFAULT, env_on("GEMM_LOG"),
-        env_on("GEMM_DEBUG_FAIL_LAUNCH")};
+        env_on("GEMM_DEBUG_FAIL_LAUNCH"), 0, 0};
     if (!h) return GEMM_ERR_ALLOC;
     *out = h;
     return GEMM_OK;

@@ -53,6 +53,8 @@
 
 #include "common.hpp"
 #include "mfma_gemm.hpp"
+#include "lora.hpp"
+#include "ragged.hpp"
 #include "sk_ranges.hpp"
 
 namespace dg {
@@ -552,10 +554,13 @@ __device__ __forceinline__ void barrier_only() { asm volatile("s_barrier" ::: "m
 // after alpha*acc + beta*C, add the bias of the D column, apply the
 // activation and the clamp, then convert and store -- all in registers, so
 // no second kernel reads D back.
-template <class Cfg, bool A_KC, bool B_KC, bool ALIGNED, bool SK = false, bool OUT_T = false,
-          bool OUT_BF16 = false, bool EPI = false>
-__global__ __launch_bounds__(Cfg::THREADS) __attribute__((amdgpu_waves_per_eu(Cfg::WPE)))
-void dma_gemm_kernel(GemmArgs p)
+//
+// RAG (ragged.hpp): the workgroup first narrows p to its group of rows, or
+// (RAG_LORA) adds its rows' low-rank products to the accumulators between
+// the mainloop and the epilogue.
+template <class Cfg, bool A_KC, bool B_KC, bool ALIGNED, bool SK, bool OUT_T, bool OUT_BF16, bool EPI,
+          int RAG, class Args>
+__device__ __forceinline__ void dma_gemm_body(Args p)
 {
     constexpr int BM = Cfg::BM, BN = Cfg::BN, BK = Cfg::BK, FM = Cfg::FM, S = Cfg::S;
     constexpr int MF = Cfg::MF, NF = Cfg::NF, NKS = Cfg::NKS;
@@ -614,6 +619,11 @@ void dma_gemm_kernel(GemmArgs p)
     const int wave_m0 = (wave / Cfg::WN) * Cfg::WTM;
     const int wave_n0 = (wave % Cfg::WN) * Cfg::WTN;
     using T = typename Cfg::T;
+    // the tile of a group's product (RAG_ROWS, RAG_K)
+    int tm_g = 0, tn_g = 0;
+    if constexpr (RAG == RAG_ROWS || RAG == RAG_K)
+        if (!narrow_to_group<RAG, BM, T, std::conditional_t<OUT_BF16, bf16_t, float>>(p, tm_g, tn_g))
+            return;
     const T* A = static_cast<const T*>(p.A);
     const T* B = static_cast<const T*>(p.B);
 
@@ -630,6 +640,12 @@ void dma_gemm_kernel(GemmArgs p)
         B + (B_KC ? (int64_t)(p.N - 1) * p.ldb + p.K : (int64_t)(p.K - 1) * p.ldb + p.N));
     const int nk_all = (p.K + BK - 1) / BK;  // K-steps of a whole tile
     const bool k_ragged = (p.K % BK) != 0;
+    // RAG_K: the rows of a group are the product's K, and only the device
+    // knows how many there are.  The buffer resources are based anew at each
+    // K-step (scalar work beside the matrix instructions), so no offset grows
+    // with the group and a group may pass 4 GiB.
+    constexpr bool REBASE = RAG == RAG_K;
+    static_assert(!REBASE || (!A_KC && !B_KC && !PAIRED), "RAG_K operands are stored by rows");
 
     Acc acc[MF][NF];
     u32x4 fa[2][MF], fb[2][NF];
@@ -689,6 +705,11 @@ void dma_gemm_kernel(GemmArgs p)
     auto load = [&](int kt, char* base) __attribute__((always_inline)) {
         const int k0 = (k_lo + kt) * BK;
         if (kt < nk_dma) {
+            if constexpr (REBASE) {
+                oa.dma(OpA::panel_rsrc(panel_a + (int64_t)k0 * p.lda, end_a), 0, base, wave);
+                ob.dma(OpB::panel_rsrc(panel_b + (int64_t)k0 * p.ldb, end_b), 0, base + A_ST, wave);
+                return;
+            }
             if constexpr (!PA) oa.dma(rsrc_a, OpA::step_bytes(k0, p.lda), base, wave);
             if constexpr (!PB) ob.dma(rsrc_b, OpB::step_bytes(k0, p.ldb), base + A_ST, wave);
         } else {
@@ -857,8 +878,10 @@ void dma_gemm_kernel(GemmArgs p)
         constexpr int NA_PR = PA ? OpA::ND : 0;
         constexpr int NDMA = NST + ((PAIRED && (CUR & 1) != 0) ? NPR : 0);
         const int kst = (k_lo + kt + AHEAD) * BK, kpr = (k_lo + kt + 2 * NP - 1) * BK;
-        const uint32_t ka = OpA::step_bytes(PA ? kpr : kst, p.lda);
-        const uint32_t kb = OpB::step_bytes(PB ? kpr : kst, p.ldb);
+        const uint32_t ka = REBASE ? 0 : OpA::step_bytes(PA ? kpr : kst, p.lda);
+        const uint32_t kb = REBASE ? 0 : OpB::step_bytes(PB ? kpr : kst, p.ldb);
+        const i32x4 ra = REBASE ? OpA::panel_rsrc(panel_a + (int64_t)kst * p.lda, end_a) : rsrc_a;
+        const i32x4 rb = REBASE ? OpB::panel_rsrc(panel_b + (int64_t)kst * p.ldb, end_b) : rsrc_b;
         oa.refresh();
         ob.refresh();
         static_for<NKS>([&](auto ks_c) __attribute__((always_inline)) {
@@ -896,13 +919,13 @@ void dma_gemm_kernel(GemmArgs p)
                                 std::integral_constant<int, rks>{},
                                 std::integral_constant<int, cb ^ 1>{});
                     else if constexpr (d < NA_ST)
-                        oa.dma_one(d, rsrc_a, ka, stage(FAR), wave);
+                        oa.dma_one(d, ra, ka, stage(FAR), wave);
                     else if constexpr (d < NA_ST + NB_ST)
-                        ob.dma_one(d - NA_ST, rsrc_b, kb, stage(FAR) + A_ST, wave);
+                        ob.dma_one(d - NA_ST, rb, kb, stage(FAR) + A_ST, wave);
                     else if constexpr (d < NA_ST + NB_ST + NA_PR)
-                        oa.dma_one(d - NA_ST - NB_ST, rsrc_a, ka, pr((CUR >> 1) % NP), wave);
+                        oa.dma_one(d - NA_ST - NB_ST, ra, ka, pr((CUR >> 1) % NP), wave);
                     else
-                        ob.dma_one(d - NA_ST - NB_ST - NA_PR, rsrc_b, kb, pr((CUR >> 1) % NP) + A_PR,
+                        ob.dma_one(d - NA_ST - NB_ST - NA_PR, rb, kb, pr((CUR >> 1) % NP) + A_PR,
                                    wave);
                 });
                 __builtin_amdgcn_sched_barrier(0);
@@ -1191,10 +1214,15 @@ void dma_gemm_kernel(GemmArgs p)
     });
     };  // epilogue
 
-    if constexpr (!SK) {
+    if constexpr (RAG == RAG_ROWS || RAG == RAG_K) {
+        tile_work(tm_g, tn_g, 0, nk_all);  // an empty K leaves zero accumulators
+        epilogue(tm_g, tn_g, 0, 0);
+    } else if constexpr (!SK) {
         int tm, tn;
         tile_coords(p, tm, tn);
         tile_work(tm, tn, 0, nk_all);
+        if constexpr (RAG == RAG_LORA)
+            lora_expand<Cfg::KIND>(p, tm * BM + wave_m0, tn * BN + wave_n0, lane, acc);
         epilogue(tm, tn, 0, 0);
     } else {
         // Stream-K ("GEMM on NVIDIA GPUs", section 5: split-K partial sums
@@ -1295,6 +1323,22 @@ void dma_gemm_kernel(GemmArgs p)
         if (rg.mid) segment((rg.t_first + 1) * nk_all);
         segment(rg.w0);
     }
+}
+
+template <class Cfg, bool A_KC, bool B_KC, bool ALIGNED, bool SK = false, bool OUT_T = false,
+          bool OUT_BF16 = false, bool EPI = false>
+__global__ __launch_bounds__(Cfg::THREADS) __attribute__((amdgpu_waves_per_eu(Cfg::WPE)))
+void dma_gemm_kernel(GemmArgs p)
+{
+    dma_gemm_body<Cfg, A_KC, B_KC, ALIGNED, SK, OUT_T, OUT_BF16, EPI, RAG_NONE>(p);
+}
+
+// The ragged launches (whole tiles, element-aligned operands).
+template <class Cfg, bool A_KC, bool B_KC, bool OUT_BF16, int RAG>
+__global__ __launch_bounds__(Cfg::THREADS) __attribute__((amdgpu_waves_per_eu(Cfg::WPE)))
+void dma_ragged_kernel(RaggedArgs p)
+{
+    dma_gemm_body<Cfg, A_KC, B_KC, true, false, false, OUT_BF16, false, RAG>(p);
 }
 
 }  // namespace dg

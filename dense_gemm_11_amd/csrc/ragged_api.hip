@@ -1,0 +1,352 @@
+// C ABI of the products over ragged groups of rows: argument validation, tile
+// choice and launches.  Declared in include/dense_gemm.h.
+#include <algorithm>
+#include <climits>
+#include <cstdio>
+
+#include "handle.hpp"
+#include "ragged_variants.hpp"
+#include "lora.hpp"
+
+namespace dg {
+namespace {
+
+constexpr int MAX_GROUPS = 1 << 16;
+
+// The layout, type and size checks that the three calls share.
+gemm_status_t check_common(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_t N, int64_t K,
+                           gemm_dtype_t dtype)
+{
+    if (!h) return GEMM_ERR_INVALID_VALUE;
+    if (transB != GEMM_OP_N && transB != GEMM_OP_T) return GEMM_ERR_INVALID_VALUE;
+    if (dtype != GEMM_DTYPE_F32 && dtype != GEMM_DTYPE_BF16_F32 && dtype != GEMM_DTYPE_BF16_BF16)
+        return GEMM_ERR_INVALID_VALUE;
+    if (M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_VALUE;
+    return GEMM_OK;
+}
+
+// Byte offsets inside a panel of `rows` rows of `ld` elements and `cols` more
+// stay below 2^32.
+bool panel_fits(int64_t rows, int64_t ld, int64_t cols, int64_t es)
+{
+    return (rows * ld + cols) * es < ((int64_t)1 << 32) - 64;
+}
+
+// C against D: the same matrix with the same strides, or disjoint.
+bool c_d_ok(const void* C, int64_t span_c, const void* D, int64_t span_d, bool same_strides)
+{
+    return C == D ? same_strides : !ranges_overlap(C, span_c, D, span_d);
+}
+
+// The tile whose height is nearest to the forced one, else the first (the
+// tallest) that `wants` accepts, else the last.
+template <class F>
+const RaggedTile& pick_tile(const RaggedTile* t, int n, int forced, F wants)
+{
+    if (forced > 0) {
+        for (int i = 0; i < n; ++i)
+            if (t[i].bm <= forced) return t[i];
+        return t[n - 1];
+    }
+    for (int i = 0; i + 1 < n; ++i)
+        if (wants(t[i])) return t[i];
+    return t[n - 1];
+}
+
+void log_call(gemm_handle_t h, const char* what, const RaggedArgs& a, int bm, int bn, int64_t grid)
+{
+    if (h->log)
+        std::fprintf(stderr, "gemm: %s %dx%d rows=%d groups=%d M=%d N=%d K=%d grid=%lld\n", what, bm,
+                     bn, a.rows, a.groups, a.M, a.N, a.K, (long long)grid);
+}
+
+}  // namespace
+}  // namespace dg
+
+extern "C" {
+
+gemm_status_t gemm_set_group_tile(gemm_handle_t h, int rows)
+{
+    if (!h || rows < 0) return GEMM_ERR_INVALID_VALUE;
+    h->forced_rows = rows;
+    return GEMM_OK;
+}
+
+int gemm_last_group_tile(gemm_handle_t h) { return h ? h->last_rows : -1; }
+
+gemm_status_t gemm_run_grouped(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_t N, int64_t K,
+                               float alpha, const void* A, int64_t lda, const void* B, int64_t ldb,
+                               int64_t strideB, float beta, const void* C, int64_t ldc, void* D,
+                               int64_t ldd, gemm_dtype_t dtype, const gemm_groups_t* groups,
+                               hipStream_t stream)
+{
+    using namespace dg;
+    const gemm_status_t st = check_common(h, transB, M, N, K, dtype);
+    if (st != GEMM_OK) return st;
+    if (!groups || groups->groups < 0 || strideB < 0) return GEMM_ERR_INVALID_VALUE;
+    const int64_t one = 1;
+    const int64_t es = dtype == GEMM_DTYPE_F32 ? 4 : 2, eo = dtype == GEMM_DTYPE_BF16_BF16 ? 2 : 4;
+    const bool b_kc = transB == GEMM_OP_T;
+    if (lda < std::max(one, K) || ldb < std::max(one, b_kc ? K : N) || ldd < std::max(one, N) ||
+        (beta != 0.0f && ldc < std::max(one, N)))
+        return GEMM_ERR_INVALID_VALUE;
+    h->last_rows = 0;
+    if (M == 0 || N == 0 || groups->groups == 0) return GEMM_OK;
+    const bool reads_ab = K > 0 && alpha != 0.0f;
+    if (!groups->offsets || !D || (beta != 0.0f && !C) || (reads_ab && (!A || !B)))
+        return GEMM_ERR_INVALID_VALUE;
+    if (M > INT_MAX || N > INT_MAX || K > INT_MAX || lda > INT_MAX || ldb > INT_MAX ||
+        ldd > INT_MAX || (beta != 0.0f && ldc > INT_MAX) || groups->groups > MAX_GROUPS)
+        return GEMM_ERR_NOT_SUPPORTED;
+    if (beta != 0.0f &&
+        !c_d_ok(C, ((M - 1) * ldc + N) * eo, D, ((M - 1) * ldd + N) * eo, ldc == ldd))
+        return GEMM_ERR_INVALID_VALUE;
+    if (reads_ab && (!aligned_to(A, es) || !aligned_to(B, es))) return GEMM_ERR_NOT_SUPPORTED;
+
+    RaggedArgs a{};
+    a.A = A;
+    a.B = B;
+    a.C = beta != 0.0f ? static_cast<const float*>(C) : nullptr;
+    a.D = static_cast<float*>(D);
+    a.lda = lda;
+    a.ldb = ldb;
+    a.ldc = beta != 0.0f ? ldc : 0;
+    a.ldd = ldd;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.K = reads_ab ? (int)K : 0;  // no K-steps: D = beta * C
+    a.alpha = alpha;
+    a.beta = beta;
+    a.c_vec = beta != 0.0f && aligned_to(C, eo);
+    a.d_vec = aligned_to(D, eo);
+    a.offsets = groups->offsets;
+    a.scales = groups->scales;
+    a.groups = groups->groups;
+    a.rows = (int)M;
+    a.stride_b = strideB;
+    // a group holds M / groups rows on average, and the host knows no more
+    const int64_t busy = std::min<int64_t>(groups->groups, M);
+    int n = 0;
+    const RaggedTile* tiles = dtype == GEMM_DTYPE_F32 ? ragged_rows_f32(&n) : ragged_rows_bf16(&n);
+    const RaggedTile& t = pick_tile(tiles, n, h->forced_rows, [&](const RaggedTile& x) {
+        return M >= busy * 3 * x.bm / 4 &&
+               4 * (M / x.bm) * ceil_div(N, x.bn) >= 3 * (int64_t)device_cus();
+    });
+    const int64_t kk = K + t.bk;
+    if (!panel_fits(t.bm - 1, lda, kk, es) ||
+        !(b_kc ? panel_fits(t.bn - 1, ldb, kk, es) : panel_fits(kk, ldb, t.bn, es)))
+        return GEMM_ERR_NOT_SUPPORTED;
+    a.tiles_n = (int)ceil_div(N, t.bn);
+    a.group_m = 4;
+    // the most tile-rows any split into groups needs
+    const int64_t grid = (M + busy * (t.bm - 1)) / t.bm * a.tiles_n;
+    if (grid > INT_MAX) return GEMM_ERR_NOT_SUPPORTED;
+    if (h->fail_launch) return GEMM_ERR_HIP;
+    if (t.fn[b_kc][dtype == GEMM_DTYPE_BF16_BF16](a, (int)grid, stream) != hipSuccess)
+        return GEMM_ERR_HIP;
+    h->last_rows = t.bm;
+    log_call(h, "grouped", a, t.bm, t.bn, grid);
+    return GEMM_OK;
+}
+
+gemm_status_t gemm_run_grouped_wgrad(gemm_handle_t h, int64_t M, int64_t N, int64_t rows, float alpha,
+                                     const void* A, int64_t lda, const void* B, int64_t ldb,
+                                     float beta, const void* C, int64_t ldc, int64_t strideC, void* D,
+                                     int64_t ldd, int64_t strideD, gemm_dtype_t dtype,
+                                     const gemm_groups_t* groups, hipStream_t stream)
+{
+    using namespace dg;
+    const gemm_status_t st = check_common(h, GEMM_OP_N, M, N, rows, dtype);
+    if (st != GEMM_OK) return st;
+    if (!groups || groups->groups < 0) return GEMM_ERR_INVALID_VALUE;
+    const int64_t one = 1, G = groups->groups;
+    const int64_t es = dtype == GEMM_DTYPE_F32 ? 4 : 2, eo = dtype == GEMM_DTYPE_BF16_BF16 ? 2 : 4;
+    if (lda < std::max(one, M) || ldb < std::max(one, N) || ldd < std::max(one, N) ||
+        (beta != 0.0f && ldc < std::max(one, N)))
+        return GEMM_ERR_INVALID_VALUE;
+    h->last_rows = 0;
+    if (M == 0 || N == 0 || G == 0) return GEMM_OK;
+    const bool reads_ab = rows > 0 && alpha != 0.0f;
+    if (!groups->offsets || !D || (beta != 0.0f && !C) || (reads_ab && (!A || !B)))
+        return GEMM_ERR_INVALID_VALUE;
+    if (M > INT_MAX || N > INT_MAX || rows > INT_MAX || lda > INT_MAX || ldb > INT_MAX ||
+        ldd > INT_MAX || (beta != 0.0f && ldc > INT_MAX) || G > MAX_GROUPS)
+        return GEMM_ERR_NOT_SUPPORTED;
+    // the groups' outputs apart from each other: one after another, or
+    // beside each other within the rows
+    const int64_t span_d = (M - 1) * ldd + N;
+    if (G > 1 && strideD < span_d && !(strideD >= N && ldd >= (G - 1) * strideD + N))
+        return GEMM_ERR_INVALID_VALUE;
+    if (beta != 0.0f) {
+        if (G > 1 && strideC < 0) return GEMM_ERR_INVALID_VALUE;
+        const int64_t gap_c = G > 1 ? (G - 1) * strideC : 0, gap_d = G > 1 ? (G - 1) * strideD : 0;
+        if (!c_d_ok(C, (gap_c + (M - 1) * ldc + N) * eo, D, (gap_d + span_d) * eo,
+                    ldc == ldd && (G == 1 || strideC == strideD)))
+            return GEMM_ERR_INVALID_VALUE;
+    }
+    if (reads_ab && (!aligned_to(A, es) || !aligned_to(B, es))) return GEMM_ERR_NOT_SUPPORTED;
+
+    RaggedArgs a{};
+    a.A = A;
+    a.B = B;
+    a.C = beta != 0.0f ? static_cast<const float*>(C) : nullptr;
+    a.D = static_cast<float*>(D);
+    a.lda = lda;
+    a.ldb = ldb;
+    a.ldc = beta != 0.0f ? ldc : 0;
+    a.ldd = ldd;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.alpha = alpha;
+    a.beta = beta;
+    a.c_vec = beta != 0.0f && aligned_to(C, eo);
+    a.d_vec = aligned_to(D, eo);
+    a.offsets = groups->offsets;
+    a.scales = groups->scales;
+    a.groups = (int)G;
+    a.rows = reads_ab ? (int)rows : 0;  // no rows: D_g = beta * C_g
+    a.stride_c = strideC;
+    a.stride_d = strideD;
+    int n = 0;
+    const RaggedTile* tiles = dtype == GEMM_DTYPE_F32 ? ragged_k_f32(&n) : ragged_k_bf16(&n);
+    const RaggedTile& t = pick_tile(tiles, n, h->forced_rows, [&](const RaggedTile& x) {
+        return 4 * G * ceil_div(M, x.bm) * ceil_div(N, x.bn) >= 3 * (int64_t)device_cus();
+    });
+    // one K-step's offsets (the kernel bases each step anew)
+    if (!panel_fits(t.bk, 2 * lda, t.bm, es) || !panel_fits(t.bk, 2 * ldb, t.bn, es))
+        return GEMM_ERR_NOT_SUPPORTED;
+    a.tiles_m = (int)ceil_div(M, t.bm);
+    a.tiles_n = (int)ceil_div(N, t.bn);
+    a.group_m = std::min(a.tiles_m, 4);
+    const int64_t grid = G * a.tiles_m * a.tiles_n;
+    if (grid > INT_MAX) return GEMM_ERR_NOT_SUPPORTED;
+    if (h->fail_launch) return GEMM_ERR_HIP;
+    if (t.fn[0][dtype == GEMM_DTYPE_BF16_BF16](a, (int)grid, stream) != hipSuccess)
+        return GEMM_ERR_HIP;
+    h->last_rows = t.bm;
+    log_call(h, "grouped wgrad", a, t.bm, t.bn, grid);
+    return GEMM_OK;
+}
+
+size_t gemm_lora_workspace_bytes(int64_t M, int rank)
+{
+    using namespace dg;
+    if (M <= 0 || rank <= 0) return 0;
+    // rows of T's partial sums: at most 16 slices, and at most
+    // ceil(8192 / M) of them (gemm_run_lora); does not decrease with M
+    const int64_t pad = ceil_div(rank, LORA_PAD) * LORA_PAD;
+    return (size_t)(std::min<int64_t>(16 * M, 8192 + M) * pad) * sizeof(float);
+}
+
+gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_t N, int64_t K,
+                            float alpha, const void* A, int64_t lda, const void* B, int64_t ldb,
+                            float beta, const void* C, int64_t ldc, void* D, int64_t ldd,
+                            gemm_dtype_t dtype, const gemm_lora_t* lora, void* ws, size_t ws_bytes,
+                            hipStream_t stream)
+{
+    using namespace dg;
+    const gemm_status_t st = check_common(h, transB, M, N, K, dtype);
+    if (st != GEMM_OK) return st;
+    if (!lora || lora->segments < 0 || lora->adapters < 0 || lora->rank < 0 ||
+        lora->stride_down < 0 || lora->stride_up < 0 ||
+        (lora->trans_down != GEMM_OP_N && lora->trans_down != GEMM_OP_T) ||
+        (lora->trans_up != GEMM_OP_N && lora->trans_up != GEMM_OP_T))
+        return GEMM_ERR_INVALID_VALUE;
+    const int64_t one = 1, R = lora->rank;
+    const int64_t es = dtype == GEMM_DTYPE_F32 ? 4 : 2, eo = dtype == GEMM_DTYPE_BF16_BF16 ? 2 : 4;
+    const bool b_kc = transB == GEMM_OP_T;
+    const bool down_kc = lora->trans_down == GEMM_OP_T, up_kc = lora->trans_up == GEMM_OP_T;
+    h->last_rows = 0;
+    // without an adapter, or with nothing to multiply, the call is gemm_run
+    if (M == 0 || N == 0 || K == 0 || alpha == 0.0f || R == 0 || lora->segments == 0 ||
+        lora->adapters == 0)
+        return gemm_run(h, GEMM_OP_N, transB, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, D, ldd,
+                        dtype, stream);
+    if (lda < K || ldb < (b_kc ? K : N) || ldd < N || (beta != 0.0f && ldc < N) ||
+        lora->ld_down < (down_kc ? K : R) || lora->ld_up < (up_kc ? R : N))
+        return GEMM_ERR_INVALID_VALUE;
+    if (!A || !B || !D || (beta != 0.0f && !C) || !lora->offsets || !lora->down || !lora->up)
+        return GEMM_ERR_INVALID_VALUE;
+    if (M > INT_MAX || N > INT_MAX || K > INT_MAX || lda > INT_MAX || ldb > INT_MAX ||
+        ldd > INT_MAX || (beta != 0.0f && ldc > INT_MAX) || lora->segments > MAX_GROUPS ||
+        lora->ld_down > INT_MAX || lora->ld_up > INT_MAX)
+        return GEMM_ERR_NOT_SUPPORTED;
+    if (beta != 0.0f &&
+        !c_d_ok(C, ((M - 1) * ldc + N) * eo, D, ((M - 1) * ldd + N) * eo, ldc == ldd))
+        return GEMM_ERR_INVALID_VALUE;
+    if (!ws || !aligned_to(ws, 256) || ws_bytes < gemm_lora_workspace_bytes(M, lora->rank))
+        return GEMM_ERR_INVALID_VALUE;
+    if (!aligned_to(A, es) || !aligned_to(B, es) || !aligned_to(lora->down, es) ||
+        !aligned_to(lora->up, es))
+        return GEMM_ERR_NOT_SUPPORTED;
+
+    RaggedArgs a{};
+    a.A = A;
+    a.B = B;
+    a.C = beta != 0.0f ? static_cast<const float*>(C) : nullptr;
+    a.D = static_cast<float*>(D);
+    a.lda = lda;
+    a.ldb = ldb;
+    a.ldc = beta != 0.0f ? ldc : 0;
+    a.ldd = ldd;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.K = (int)K;
+    a.alpha = alpha;
+    a.beta = beta;
+    a.c_vec = beta != 0.0f && aligned_to(C, eo);
+    a.d_vec = aligned_to(D, eo);
+    a.offsets = lora->offsets;
+    a.scales = lora->scales;
+    a.groups = lora->segments;
+    a.rows = (int)M;
+    a.ids = lora->ids;
+    a.adapters = lora->adapters;
+    a.rank = lora->rank;
+    a.rank_pad = (int)(ceil_div(R, LORA_PAD) * LORA_PAD);
+    a.t = static_cast<const float*>(ws);
+    a.up = lora->up;
+    a.ld_up = lora->ld_up;
+    a.stride_up = lora->stride_up;
+    a.up_kc = up_kc;
+    int n = 0;
+    const RaggedTile* tiles = dtype == GEMM_DTYPE_F32 ? ragged_lora_f32(&n) : ragged_lora_bf16(&n);
+    const RaggedTile& t = pick_tile(tiles, n, h->forced_rows, [&](const RaggedTile& x) {
+        return 4 * ceil_div(M, x.bm) * ceil_div(N, x.bn) >= 3 * (int64_t)device_cus();
+    });
+    const int64_t kk = K + t.bk;
+    if (!panel_fits(t.bm - 1, lda, kk, es) ||
+        !(b_kc ? panel_fits(t.bn - 1, ldb, kk, es) : panel_fits(kk, ldb, t.bn, es)))
+        return GEMM_ERR_NOT_SUPPORTED;
+    a.tiles_m = (int)ceil_div(M, t.bm);
+    a.tiles_n = (int)ceil_div(N, t.bn);
+    a.group_m = std::min(a.tiles_m, 4);
+    const int64_t grid = (int64_t)a.tiles_m * a.tiles_n;
+    if (grid > INT_MAX) return GEMM_ERR_NOT_SUPPORTED;
+    ShrinkCall sc{};
+    sc.down = lora->down;
+    sc.ld_down = lora->ld_down;
+    sc.stride_down = lora->stride_down;
+    sc.down_kc = down_kc;
+    sc.t = static_cast<float*>(ws);
+    const int64_t segs = std::min<int64_t>(lora->segments, M);
+    sc.tall = M >= 32 * segs;
+    // slices of K until about 512 workgroups share the first product, each
+    // slice at least one round of the eight waves (8 runs of 4 chunk rows)
+    const int64_t bm = sc.tall ? 32 : 16, round = 8 * 4 * (64 / es);
+    const int64_t blocks = std::max<int64_t>(1, (M + segs * (bm - 1)) / bm);
+    int64_t splits = std::min<int64_t>({16, ceil_div(512, blocks), ceil_div(K, round)});
+    splits = std::max<int64_t>(1, std::min<int64_t>(splits, ceil_div(8192, M)));
+    sc.k_slice = (int)(ceil_div(ceil_div(K, splits), 4 * (64 / es)) * 4 * (64 / es));
+    sc.splits = (int)ceil_div(K, sc.k_slice);
+    a.splits = sc.splits;
+    if (h->fail_launch) return GEMM_ERR_HIP;
+    if (launch_shrink(a, sc, dtype != GEMM_DTYPE_F32, stream) != hipSuccess ||
+        t.fn[b_kc][dtype == GEMM_DTYPE_BF16_BF16](a, (int)grid, stream) != hipSuccess)
+        return GEMM_ERR_HIP;
+    h->last_rows = t.bm;
+    log_call(h, "lora", a, t.bm, t.bn, grid);
+    return GEMM_OK;
+}
+
+}  // extern "C"

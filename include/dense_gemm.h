@@ -337,6 +337,109 @@ gemm_status_t gemm_run_no_alloc(gemm_handle_t h, gemm_op_t transA, gemm_op_t tra
  * or a value below -1. */
 gemm_status_t gemm_set_stream_k_poll_limit(gemm_handle_t h, int polls);
 
+/* ---- products over ragged groups of rows ----------------------------------
+ * The rows of A (and D) divided into consecutive groups, each with a matrix
+ * of its own: the experts of a mixture over the rows routed to them, or the
+ * adapters of a batch of requests.  Group g holds rows offsets[g] ..
+ * offsets[g+1]-1, where offsets is an int32 array of groups+1 entries on the
+ * device that do not decrease: a router's running sum is used as it is, the
+ * call neither waits for it nor copies it, and a captured call follows its
+ * later values.  Groups may be empty, and rows before offsets[0] or from
+ * offsets[groups] on belong to no group.  Entries outside [0, M] are taken as
+ * the nearest bound and a negative length as an empty group: no value leads
+ * outside the operands (rows that overlapping groups share then hold one
+ * group's result).  At most 65536 groups (GEMM_ERR_NOT_SUPPORTED beyond).
+ * scales, when not NULL, holds one fp32 factor per group on the device, and
+ * alpha is multiplied by it.
+ *
+ * Types, storage and leading dimensions, alpha and beta, in-place C == D and
+ * errors are as for gemm_run; A and B must be element-aligned and a tile's
+ * panel below 4 GiB, as for gemm_run_epilogue (GEMM_ERR_NOT_SUPPORTED
+ * otherwise).  Accumulation is fp32 with one rounding to D's type, and the
+ * results are bitwise reproducible for the same call, sizes and GPU.  None of
+ * these calls allocates or waits; a handle's workspace and forced variant do
+ * not bear on them. */
+typedef struct {
+    int groups;
+    const int32_t* offsets; /* device, groups + 1 */
+    const float* scales;    /* device, groups; or NULL */
+} gemm_groups_t;
+
+/* D[rows of g] = alpha s_g A[rows of g] op(B_g) + beta C[rows of g], with A of
+ * M x K, C and D of M x N and op(B_g) of K x N at B + g*strideB elements
+ * (strideB >= 0; 0 shares one matrix).  Rows in no group are not written.
+ * The gradient with respect to A is the same call on D's gradient with the
+ * other transB. */
+gemm_status_t gemm_run_grouped(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_t N, int64_t K,
+                               float alpha, const void* A, int64_t lda, const void* B, int64_t ldb,
+                               int64_t strideB, float beta, const void* C, int64_t ldc, void* D,
+                               int64_t ldd, gemm_dtype_t dtype, const gemm_groups_t* groups,
+                               hipStream_t stream);
+
+/* The gradient with respect to the groups' matrices:
+ *     D_g = alpha s_g A[rows of g]^T B[rows of g] + beta C_g
+ * with A of rows x M, B of rows x N, and C_g, D_g of M x N at C + g*strideC,
+ * D + g*strideD.  An empty group's D_g is beta C_g (0 when beta == 0).  beta
+ * = 1 with C == D adds to gradients already there.  The D_g must lie apart:
+ * strideD >= (M-1)*ldd + N, or side by side in each row
+ * (GEMM_ERR_INVALID_VALUE otherwise). */
+gemm_status_t gemm_run_grouped_wgrad(gemm_handle_t h, int64_t M, int64_t N, int64_t rows, float alpha,
+                                     const void* A, int64_t lda, const void* B, int64_t ldb,
+                                     float beta, const void* C, int64_t ldc, int64_t strideC, void* D,
+                                     int64_t ldd, int64_t strideD, gemm_dtype_t dtype,
+                                     const gemm_groups_t* groups, hipStream_t stream);
+
+/* Low-rank adapters of many requests beside a shared product:
+ *     D = alpha (A op(B) + s_a (A op(down_a)) op(up_a)) + beta C
+ * where a is the adapter of the row's segment.  Segment s holds rows
+ * offsets[s] .. offsets[s+1]-1 (device, as for gemm_groups_t) and uses adapter
+ * ids[s] (device; NULL: adapter s).  A row in no segment, or in one whose id
+ * is negative or >= adapters, gets the shared product alone, whatever the
+ * adapters hold.  op(down_a) is K x rank: stored rank x K with trans_down ==
+ * GEMM_OP_T, K x rank with GEMM_OP_N; op(up_a) is rank x N: stored N x rank
+ * with trans_up == GEMM_OP_T, rank x N with GEMM_OP_N.  Both have A's element
+ * type, element alignment, and adapter a's at a*stride elements (>= 0).
+ * scales: one fp32 factor per adapter on the device, or NULL.
+ * The gradient with respect to A is the same call on D's gradient with the
+ * other transB, up and down in each other's place and both GEMM_OP_N.
+ *
+ * The rows' products with down are formed in fp32 in `workspace`, device
+ * memory of at least gemm_lora_workspace_bytes(M, rank) bytes that is 256-byte
+ * aligned (GEMM_ERR_INVALID_VALUE otherwise); it needs no clearing, and calls
+ * that may overlap in time need one each. */
+typedef struct {
+    int segments;
+    const int32_t* offsets; /* device, segments + 1 */
+    const int32_t* ids;     /* device, segments; or NULL */
+    int adapters;
+    int rank;
+    const float* scales;    /* device, adapters; or NULL */
+    gemm_op_t trans_down;
+    const void* down;
+    int64_t ld_down, stride_down;
+    gemm_op_t trans_up;
+    const void* up;
+    int64_t ld_up, stride_up;
+} gemm_lora_t;
+
+size_t gemm_lora_workspace_bytes(int64_t M, int rank);
+
+gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_t N, int64_t K,
+                            float alpha, const void* A, int64_t lda, const void* B, int64_t ldb,
+                            float beta, const void* C, int64_t ldc, void* D, int64_t ldd,
+                            gemm_dtype_t dtype, const gemm_lora_t* lora, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream);
+
+/* Rows of the output tile that h's later calls of the three functions above
+ * take: the tallest there is up to `rows`, else the smallest (0, the default:
+ * chosen from the call's sizes).  Tests use this to run every tile.
+ * GEMM_ERR_INVALID_VALUE for a negative value or a NULL handle. */
+gemm_status_t gemm_set_group_tile(gemm_handle_t h, int rows);
+
+/* Rows of the output tile of h's last such call (0: none launched; -1 for a
+ * NULL handle). */
+int gemm_last_group_tile(gemm_handle_t h);
+
 #ifdef __cplusplus
 }
 #endif
