@@ -1,0 +1,16 @@
+// Row-ragged products of few rows per group (gemm_run_grouped): streaming tiles.
+#include "stream_variants.hpp"
+
+namespace dg {
+
+const RaggedTile* stream_rows_bf16(int* count)
+{
+    return stream_tiles_bf16<RAG_ROWS>(count);
+}
+
+const RaggedTile* stream_rows_f32(int* count)
+{
+    return stream_tiles_f32<RAG_ROWS>(count);
+}
+
+}  // namespace dg

@@ -38,19 +38,42 @@ bool c_d_ok(const void* C, int64_t span_c, const void* D, int64_t span_d, bool s
     return C == D ? same_strides : !ranges_overlap(C, span_c, D, span_d);
 }
 
-// The tile whose height is nearest to the forced one, else the first (the
-// tallest) that `wants` accepts, else the last.
-template <class F>
-const RaggedTile& pick_tile(const RaggedTile* t, int n, int forced, F wants)
+// A call's tiles, tallest first: the direct-to-LDS ones, then the streaming
+// ones (if it has any).
+struct TileList {
+    const RaggedTile* dma;
+    const RaggedTile* stream;
+    int n_dma, n;
+    const RaggedTile& operator[](int i) const { return i < n_dma ? dma[i] : stream[i - n_dma]; }
+};
+typedef const RaggedTile* (*TileTable)(int* count);
+TileList tile_list(TileTable dma, TileTable stream)
 {
-    if (forced > 0) {
-        for (int i = 0; i < n; ++i)
-            if (t[i].bm <= forced) return t[i];
-        return t[n - 1];
-    }
-    for (int i = 0; i + 1 < n; ++i)
-        if (wants(t[i])) return t[i];
-    return t[n - 1];
+    TileList l{};
+    int n_stream = 0;
+    l.dma = dma(&l.n_dma);
+    if (stream) l.stream = stream(&n_stream);
+    l.n = l.n_dma + n_stream;
+    return l;
+}
+
+// The tallest tile up to the forced height, else the first that `wants(tile,
+// streaming)` accepts, else the last.
+template <class F>
+const RaggedTile& pick_tile(const TileList& t, int forced, F wants)
+{
+    for (int i = 0; i + 1 < t.n; ++i)
+        if (forced > 0 ? t[i].bm <= forced : wants(t[i], i >= t.n_dma)) return t[i];
+    return t[t.n - 1];
+}
+
+// A streaming tile holds the rows there are on average, and the wide ones
+// have at least half a workgroup per compute unit (narrower ones read A more
+// often).
+bool wants_stream(const RaggedTile& t, int bn, int64_t busy, int64_t avg, int64_t N)
+{
+    if (t.bm > 16) return avg > t.bm / 2;
+    return 2 * busy * ceil_div(avg, t.bm) * ceil_div(N, bn) >= device_cus();
 }
 
 void log_call(gemm_handle_t h, const char* what, const RaggedArgs& a, int bm, int bn, int64_t grid)
@@ -126,17 +149,21 @@ gemm_status_t gemm_run_grouped(gemm_handle_t h, gemm_op_t transB, int64_t M, int
     a.stride_b = strideB;
     // a group holds M / groups rows on average, and the host knows no more
     const int64_t busy = std::min<int64_t>(groups->groups, M);
-    int n = 0;
-    const RaggedTile* tiles = dtype == GEMM_DTYPE_F32 ? ragged_rows_f32(&n) : ragged_rows_bf16(&n);
-    const RaggedTile& t = pick_tile(tiles, n, h->forced_rows, [&](const RaggedTile& x) {
+    const int64_t avg = ceil_div(M, busy);
+    const TileList tiles = dtype == GEMM_DTYPE_F32 ? tile_list(ragged_rows_f32, stream_rows_f32)
+                                                   : tile_list(ragged_rows_bf16, stream_rows_bf16);
+    const RaggedTile& t = pick_tile(tiles, h->forced_rows, [&](const RaggedTile& x, bool stream) {
+        if (stream) return wants_stream(x, x.bn[b_kc], busy, avg, N);
+        if (x.bm == 128) return avg > 64;
         return M >= busy * 3 * x.bm / 4 &&
-               4 * (M / x.bm) * ceil_div(N, x.bn) >= 3 * (int64_t)device_cus();
+               4 * (M / x.bm) * ceil_div(N, x.bn[b_kc]) >= 3 * (int64_t)device_cus();
     });
+    const int bn = t.bn[b_kc];
     const int64_t kk = K + t.bk;
     if (!panel_fits(t.bm - 1, lda, kk, es) ||
-        !(b_kc ? panel_fits(t.bn - 1, ldb, kk, es) : panel_fits(kk, ldb, t.bn, es)))
+        !(b_kc ? panel_fits(bn - 1, ldb, kk, es) : panel_fits(kk, ldb, bn, es)))
         return GEMM_ERR_NOT_SUPPORTED;
-    a.tiles_n = (int)ceil_div(N, t.bn);
+    a.tiles_n = (int)ceil_div(N, bn);
     a.group_m = 4;
     // the most tile-rows any split into groups needs
     const int64_t grid = (M + busy * (t.bm - 1)) / t.bm * a.tiles_n;
@@ -145,7 +172,7 @@ gemm_status_t gemm_run_grouped(gemm_handle_t h, gemm_op_t transB, int64_t M, int
     if (t.fn[b_kc][dtype == GEMM_DTYPE_BF16_BF16](a, (int)grid, stream) != hipSuccess)
         return GEMM_ERR_HIP;
     h->last_rows = t.bm;
-    log_call(h, "grouped", a, t.bm, t.bn, grid);
+    log_call(h, "grouped", a, t.bm, bn, grid);
     return GEMM_OK;
 }
 
@@ -207,16 +234,17 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_handle_t h, int64_t M, int64_t N, int6
     a.rows = reads_ab ? (int)rows : 0;  // no rows: D_g = beta * C_g
     a.stride_c = strideC;
     a.stride_d = strideD;
-    int n = 0;
-    const RaggedTile* tiles = dtype == GEMM_DTYPE_F32 ? ragged_k_f32(&n) : ragged_k_bf16(&n);
-    const RaggedTile& t = pick_tile(tiles, n, h->forced_rows, [&](const RaggedTile& x) {
-        return 4 * G * ceil_div(M, x.bm) * ceil_div(N, x.bn) >= 3 * (int64_t)device_cus();
+    const TileList tiles =
+        tile_list(dtype == GEMM_DTYPE_F32 ? ragged_k_f32 : ragged_k_bf16, nullptr);
+    const RaggedTile& t = pick_tile(tiles, h->forced_rows, [&](const RaggedTile& x, bool) {
+        return 4 * G * ceil_div(M, x.bm) * ceil_div(N, x.bn[0]) >= 3 * (int64_t)device_cus();
     });
+    const int bn = t.bn[0];
     // one K-step's offsets (the kernel bases each step anew)
-    if (!panel_fits(t.bk, 2 * lda, t.bm, es) || !panel_fits(t.bk, 2 * ldb, t.bn, es))
+    if (!panel_fits(t.bk, 2 * lda, t.bm, es) || !panel_fits(t.bk, 2 * ldb, bn, es))
         return GEMM_ERR_NOT_SUPPORTED;
     a.tiles_m = (int)ceil_div(M, t.bm);
-    a.tiles_n = (int)ceil_div(N, t.bn);
+    a.tiles_n = (int)ceil_div(N, bn);
     a.group_m = std::min(a.tiles_m, 4);
     const int64_t grid = G * a.tiles_m * a.tiles_n;
     if (grid > INT_MAX) return GEMM_ERR_NOT_SUPPORTED;
@@ -224,7 +252,7 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_handle_t h, int64_t M, int64_t N, int6
     if (t.fn[0][dtype == GEMM_DTYPE_BF16_BF16](a, (int)grid, stream) != hipSuccess)
         return GEMM_ERR_HIP;
     h->last_rows = t.bm;
-    log_call(h, "grouped wgrad", a, t.bm, t.bn, grid);
+    log_call(h, "grouped wgrad", a, t.bm, bn, grid);
     return GEMM_OK;
 }
 
@@ -309,17 +337,20 @@ gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_
     a.ld_up = lora->ld_up;
     a.stride_up = lora->stride_up;
     a.up_kc = up_kc;
-    int n = 0;
-    const RaggedTile* tiles = dtype == GEMM_DTYPE_F32 ? ragged_lora_f32(&n) : ragged_lora_bf16(&n);
-    const RaggedTile& t = pick_tile(tiles, n, h->forced_rows, [&](const RaggedTile& x) {
-        return 4 * ceil_div(M, x.bm) * ceil_div(N, x.bn) >= 3 * (int64_t)device_cus();
+    const TileList tiles = dtype == GEMM_DTYPE_F32 ? tile_list(ragged_lora_f32, stream_lora_f32)
+                                                   : tile_list(ragged_lora_bf16, stream_lora_bf16);
+    const RaggedTile& t = pick_tile(tiles, h->forced_rows, [&](const RaggedTile& x, bool stream) {
+        if (stream) return wants_stream(x, x.bn[b_kc], 1, M, N);
+        if (x.bm == 128) return M > 64;
+        return 4 * ceil_div(M, x.bm) * ceil_div(N, x.bn[b_kc]) >= 3 * (int64_t)device_cus();
     });
+    const int bn = t.bn[b_kc];
     const int64_t kk = K + t.bk;
     if (!panel_fits(t.bm - 1, lda, kk, es) ||
-        !(b_kc ? panel_fits(t.bn - 1, ldb, kk, es) : panel_fits(kk, ldb, t.bn, es)))
+        !(b_kc ? panel_fits(bn - 1, ldb, kk, es) : panel_fits(kk, ldb, bn, es)))
         return GEMM_ERR_NOT_SUPPORTED;
     a.tiles_m = (int)ceil_div(M, t.bm);
-    a.tiles_n = (int)ceil_div(N, t.bn);
+    a.tiles_n = (int)ceil_div(N, bn);
     a.group_m = std::min(a.tiles_m, 4);
     const int64_t grid = (int64_t)a.tiles_m * a.tiles_n;
     if (grid > INT_MAX) return GEMM_ERR_NOT_SUPPORTED;
@@ -345,7 +376,7 @@ gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_
         t.fn[b_kc][dtype == GEMM_DTYPE_BF16_BF16](a, (int)grid, stream) != hipSuccess)
         return GEMM_ERR_HIP;
     h->last_rows = t.bm;
-    log_call(h, "lora", a, t.bm, t.bn, grid);
+    log_call(h, "lora", a, t.bm, bn, grid);
     return GEMM_OK;
 }
 

@@ -9,9 +9,16 @@ namespace dg {
 typedef hipError_t (*RaggedFn)(const RaggedArgs&, int grid, hipStream_t);
 
 struct RaggedTile {
-    int bm, bn, bk;
+    int bm, bn[2], bk;  // bn of either layout of B
     RaggedFn fn[2][2];  // [B k-contiguous][bf16 output] (RAG_K: [0] only)
 };
+
+// Streaming tiles (stream.hpp), tallest first, the narrowest last; *count of
+// them.
+const RaggedTile* stream_rows_bf16(int* count);
+const RaggedTile* stream_rows_f32(int* count);
+const RaggedTile* stream_lora_bf16(int* count);
+const RaggedTile* stream_lora_f32(int* count);
 
 // Direct-to-LDS tiles, tallest first; *count of them.
 const RaggedTile* ragged_rows_bf16(int* count);
@@ -46,25 +53,25 @@ hipError_t launch_ragged(const RaggedArgs& a, int grid, hipStream_t s)
 // RaggedTile entry of configuration CFG for launch kind RAG with A stored by
 // rows: both layouts of B, both output types (fp32 operands: fp32 only).
 #define DG_RAGGED_BF16(CFG, RAG)                                                             \
-    {CFG::BM, CFG::BN, CFG::BK,                                                              \
+    {CFG::BM, {CFG::BN, CFG::BN}, CFG::BK,                                                   \
      {{dg::launch_ragged<dg::dma_ragged_kernel<CFG, true, false, false, RAG>, CFG::THREADS>, \
        dg::launch_ragged<dg::dma_ragged_kernel<CFG, true, false, true, RAG>, CFG::THREADS>}, \
       {dg::launch_ragged<dg::dma_ragged_kernel<CFG, true, true, false, RAG>, CFG::THREADS>,  \
        dg::launch_ragged<dg::dma_ragged_kernel<CFG, true, true, true, RAG>, CFG::THREADS>}}}
 #define DG_RAGGED_F32(CFG, RAG)                                                              \
-    {CFG::BM, CFG::BN, CFG::BK,                                                              \
+    {CFG::BM, {CFG::BN, CFG::BN}, CFG::BK,                                                   \
      {{dg::launch_ragged<dg::dma_ragged_kernel<CFG, true, false, false, RAG>, CFG::THREADS>, \
        nullptr},                                                                             \
       {dg::launch_ragged<dg::dma_ragged_kernel<CFG, true, true, false, RAG>, CFG::THREADS>,  \
        nullptr}}}
 // ... and for RAG_K (both operands stored by rows).
 #define DG_RAGGED_K_BF16(CFG)                                                                      \
-    {CFG::BM, CFG::BN, CFG::BK,                                                                    \
+    {CFG::BM, {CFG::BN, CFG::BN}, CFG::BK,                                                         \
      {{dg::launch_ragged<dg::dma_ragged_kernel<CFG, false, false, false, RAG_K>, CFG::THREADS>,    \
        dg::launch_ragged<dg::dma_ragged_kernel<CFG, false, false, true, RAG_K>, CFG::THREADS>},    \
       {nullptr, nullptr}}}
 #define DG_RAGGED_K_F32(CFG)                                                                       \
-    {CFG::BM, CFG::BN, CFG::BK,                                                                    \
+    {CFG::BM, {CFG::BN, CFG::BN}, CFG::BK,                                                         \
      {{dg::launch_ragged<dg::dma_ragged_kernel<CFG, false, false, false, RAG_K>, CFG::THREADS>,    \
        nullptr},                                                                                   \
       {nullptr, nullptr}}}
