@@ -1,30 +1,34 @@
 // Ragged products of fp32 operands: by rows (gemm_run_grouped), along K
 // (gemm_run_grouped_wgrad) and with low-rank adapters (gemm_run_lora).
 #include "mfma_dma_gemm.hpp"
-#include "selected_configs.hpp"
+#include "ragged_configs.hpp"
 #include "ragged_variants.hpp"
 
 namespace dg {
 
 const RaggedTile* ragged_rows_f32(int* count)
 {
-    static const RaggedTile tiles[] = {DG_RAGGED_F32(SelF32Big, RAG_ROWS),
-                                       DG_RAGGED_F32(SelF32Mid, RAG_ROWS)};
+    static const RaggedTile tiles[] = {
+        DG_RAGGED_F32(SelF32Mid, RAG_ROWS, {7.8f, 60.6f, 4.9f, 61.1f}),
+        DG_RAGGED_F32(RagF32Low, RAG_ROWS, {6.2f, 31.5f, 2.5f, 31.8f})};
     *count = (int)(sizeof(tiles) / sizeof(tiles[0]));
     return tiles;
 }
 
 const RaggedTile* ragged_lora_f32(int* count)
 {
-    static const RaggedTile tiles[] = {DG_RAGGED_F32(SelF32Big, RAG_LORA),
-                                       DG_RAGGED_F32(SelF32Mid, RAG_LORA)};
+    static const RaggedTile tiles[] = {
+        DG_RAGGED_F32(SelF32Mid, RAG_LORA, {5.0f, 37.4f, 21.3f, 62.6f}),
+        DG_RAGGED_F32(RagF32Low, RAG_LORA, {17.2f, 37.3f, 15.5f, 26.6f})};
     *count = (int)(sizeof(tiles) / sizeof(tiles[0]));
     return tiles;
 }
 
 const RaggedTile* ragged_k_f32(int* count)
 {
-    static const RaggedTile tiles[] = {DG_RAGGED_K_F32(SelF32Big), DG_RAGGED_K_F32(SelF32Mid)};
+    static const RaggedTile tiles[] = {
+        DG_RAGGED_K_F32(SelF32Mid, {9.0f, 0.0f, 8.1f, 89.8f}),
+        DG_RAGGED_K_F32(RagF32Low, {7.8f, 40.8f, 4.7f, 41.4f})};
     *count = (int)(sizeof(tiles) / sizeof(tiles[0]));
     return tiles;
 }

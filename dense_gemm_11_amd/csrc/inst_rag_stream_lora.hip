@@ -5,12 +5,12 @@ namespace dg {
 
 const RaggedTile* stream_lora_bf16(int* count)
 {
-    return stream_tiles_bf16<RAG_LORA>(count);
+    return stream_tiles<bf16_t, RAG_LORA>(count);
 }
 
 const RaggedTile* stream_lora_f32(int* count)
 {
-    return stream_tiles_f32<RAG_LORA>(count);
+    return stream_tiles<float, RAG_LORA>(count);
 }
 
 }  // namespace dg

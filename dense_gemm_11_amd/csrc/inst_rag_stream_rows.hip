@@ -5,12 +5,12 @@ namespace dg {
 
 const RaggedTile* stream_rows_bf16(int* count)
 {
-    return stream_tiles_bf16<RAG_ROWS>(count);
+    return stream_tiles<bf16_t, RAG_ROWS>(count);
 }
 
 const RaggedTile* stream_rows_f32(int* count)
 {
-    return stream_tiles_f32<RAG_ROWS>(count);
+    return stream_tiles<float, RAG_ROWS>(count);
 }
 
 }  // namespace dg

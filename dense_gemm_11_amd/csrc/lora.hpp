@@ -3,15 +3,17 @@
 // where a is the adapter of the row's segment (none: the shared product
 // alone), op(down_a) is K x R and op(up_a) R x N with a small rank R.
 //
-// Two launches.  lora_shrink_kernel forms T = s_a X op(down_a), rows x R, in
+// Two launches.  The streaming kernel forms T = s_a X op(down_a), rows x R, in
 // fp32 (R padded to whole fragments with zeros); the shared product then runs
-// as it does alone, and between its mainloop and its epilogue each wave adds
-// T op(up_a) for its own rows to its accumulators (lora_expand), so D is
-// written once and rounded once.  The second product costs 2 M R N operations
-// beside 2 M K N.  T stays fp32 in memory; as bf16 MFMA operands it goes in
-// as two terms, T = hi + lo with lo = bf16(T - hi), which keeps 16 of its
-// bits: as one bf16 term its rounding (2^-9 of the low-rank part) would be as
-// large as that of D itself.
+// as it does alone, and its epilogue adds T op(up_a) to the accumulators
+// (lora_fragment; the streaming kernel adds lora_row to its sums), so D is
+// written once and rounded once.  Where all rows of an output tile share an
+// adapter, T and up are more of the product's K instead: T's terms and up_a
+// go through LDS behind the last step of X and W.
+// The second product costs 2 M R N operations beside 2 M K N.  T stays fp32
+// in memory; as bf16 MFMA operands it goes in as two terms, T = hi + lo with
+// lo = bf16(T - hi), which keeps 16 of its bits: as one bf16 term its rounding
+// (2^-9 of the low-rank part) would be as large as that of D itself.
 #pragma once
 
 #include "common.hpp"
@@ -23,19 +25,17 @@ namespace dg {
 // T is padded to whole fragments of rank along k: LORA_PAD columns.
 constexpr int LORA_PAD = 16;
 
-// VEC consecutive k (from k) of column / row mn of a matrix stored with k
-// contiguous (KC: element (mn, k) at mn*ld + k) or mn contiguous (at
-// k*ld + mn); zero where k >= K or !ok.
+// VEC consecutive k of one row (or column) with every index clamped into
+// [0, K) and zero past K.  `x` points at the row; ks: elements between k.
 template <typename T>
-__device__ __forceinline__ u32x4 load_k_chunk(const T* x, int64_t ld, bool kc, int64_t mn, bool ok,
-                                              int k, int K)
+__device__ __forceinline__ u32x4 clamped_chunk(const T* x, int64_t ks, int k, int K)
 {
     constexpr int VEC = 16 / sizeof(T);
-    if (kc && ok && k + VEC <= K) return *reinterpret_cast<const u32x4_elem<T>*>(x + mn * ld + k);
     T e[VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j)
-        e[j] = ok && k + j < K ? (kc ? x[mn * ld + k + j] : x[(int64_t)(k + j) * ld + mn]) : T(0);
+    for (int v = 0; v < VEC; ++v) e[v] = x[(int64_t)(k + v < K ? k + v : K - 1) * ks];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) e[v] = k + v < K ? e[v] : T(0);
     return pack_chunk<T>(e);
 }
 
@@ -59,85 +59,244 @@ __device__ __forceinline__ void split_terms(const float (&t)[4], u32x4& hi, u32x
                __float_as_uint(t[3])};
 }
 
-// First segment that may hold row m0 or a later one: the number of segments
-// that end at or before it (offsets do not decrease).
-__device__ __forceinline__ int first_segment(const RaggedArgs& p, int m0, int lane)
+// T as bf16 operand terms in memory: row r holds hi in columns 0 .. rank_pad-1
+// and lo behind it.  Four columns of it.
+__device__ __forceinline__ void store_terms(const RaggedArgs& p, int64_t row, int col, const f32x4& t)
 {
-    int s = 0;
-    for (int g0 = 0; g0 < p.groups; g0 += 64) {
-        const uint64_t before = __ballot(g0 + lane < p.groups && p.offsets[g0 + lane + 1] <= m0);
-        s += __builtin_popcountll(before);
-        if (~before != 0) break;
-    }
-    return s;
+    float e[8] = {t[0], t[1], t[2], t[3]};
+    u32x4 hi, lo;
+    split_terms(e, hi, lo);
+    uint16_t* d = p.t_terms + row * 2 * p.rank_pad + col;
+    *reinterpret_cast<uint2*>(d) = uint2{hi[0], hi[1]};
+    *reinterpret_cast<uint2*>(d + p.rank_pad) = uint2{lo[0], lo[1]};
 }
 
-// Adds T op(up_a) to the accumulators of a wave whose block starts at row m0
-// and column n0 (MF x NF fragments of FM x FM; lane l holds row l % FM of
-// each).  Segments are taken one after another; the product of a segment's
-// adapter with the fragment's rows goes into a temporary, and only lanes whose
-// row lies in the segment add it, so nothing an adapter holds (infinities,
-// NaN) reaches another segment's rows.
-template <int KIND, int MF, int NF, typename Acc>
-__device__ __forceinline__ void lora_expand(const RaggedArgs& p, int m0, int n0, int lane,
-                                            Acc (&acc)[MF][NF])
+// adapter[r] = the adapter of row m0 + r for the BM rows of a tile, or -1;
+// ends with a barrier.  (Where segments overlap, one of theirs.)
+template <int BM, int THREADS>
+__device__ __forceinline__ void map_adapters(const RaggedArgs& p, int m0, int tid, int* adapter)
+{
+    const int lane = tid & 63;
+    for (int r = tid; r < BM; r += THREADS) adapter[r] = -1;
+    __syncthreads();
+    for (int s0 = tid - lane; s0 < p.groups; s0 += THREADS) {
+        int lo = 0, n = 0, a = -1;
+        if (s0 + lane < p.groups) {
+            group_span(p, s0 + lane, lo, n);
+            a = p.ids ? p.ids[s0 + lane] : s0 + lane;
+        }
+        const int first = lo > m0 ? lo - m0 : 0;
+        const int end = lo + n < m0 + BM ? lo + n - m0 : BM;
+        uint64_t live = __ballot(n > 0 && first < end && a >= 0 && a < p.adapters);
+        for (; live != 0; live &= live - 1) {
+            const int src = __builtin_ctzll(live);
+            const int e = __builtin_amdgcn_readlane(end, src), v = __builtin_amdgcn_readlane(a, src);
+            for (int r = __builtin_amdgcn_readlane(first, src) + lane; r < e; r += 64) adapter[r] = v;
+        }
+    }
+    __syncthreads();
+}
+
+// The adapter of every row of [m0, m_end), or TILE_NONE where no row has one,
+// or TILE_MIXED (also where `whole` is false).  Every lane of the wave takes
+// part.
+enum : int { TILE_NONE = -1, TILE_MIXED = -2 };
+__device__ __forceinline__ int tile_adapter(const RaggedArgs& p, int m0, int m_end, int lane, bool whole)
+{
+    int found = TILE_NONE;
+    for (int s0 = 0; s0 < p.groups; s0 += 64) {
+        int lo = 0, n = 0, a = -1;
+        if (s0 + lane < p.groups) {
+            group_span(p, s0 + lane, lo, n);
+            a = p.ids ? p.ids[s0 + lane] : s0 + lane;
+        }
+        const bool here = a >= 0 && a < p.adapters && n > 0 && lo < m_end && lo + n > m0;
+        const uint64_t all = __ballot(here && lo <= m0 && lo + n >= m_end);
+        if (all != 0 && whole) return __builtin_amdgcn_readlane(a, __builtin_ctzll(all));
+        if (__ballot(here) != 0) found = TILE_MIXED;
+    }
+    return found;
+}
+
+template <int BYTES>
+struct RawLoad;
+template <>
+struct RawLoad<4> {
+    typedef uint32_t T __attribute__((ext_vector_type(1), aligned(2)));
+};
+template <>
+struct RawLoad<8> {
+    typedef uint32_t T __attribute__((ext_vector_type(2), aligned(2)));
+};
+template <>
+struct RawLoad<16> {
+    typedef uint32_t T __attribute__((ext_vector_type(4), aligned(2)));
+};
+
+// Ranks k .. k + 4 V - 1 of a row's T, summed over the slices of K.  Up to four
+// slices, read at once.
+template <int V>
+__device__ __forceinline__ void load_t(const RaggedArgs& p, int row, int k, f32x4 (&t)[V])
+{
+    const float* src = p.t + (int64_t)row * p.rank_pad + k;
+    const int64_t slice = (int64_t)p.rows * p.rank_pad;
+    if (p.splits == 1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) t[v] = reinterpret_cast<const f32x4*>(src)[v];
+        return;
+    }
+    f32x4 q[4][V];
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            q[s][v] = reinterpret_cast<const f32x4*>(src + (s < p.splits ? s : 0) * slice)[v];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        t[v] = q[0][v] + q[1][v];
+#pragma unroll
+        for (int s = 2; s < 4; ++s)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[v][e] += s < p.splits ? q[s][v][e] : 0.0f;
+    }
+}
+
+// T op(up_a) of row `row`, four columns from `col` (`inside`: of a tile that
+// lies inside the matrix, the same for every lane), in fp32 (T is not rounded
+// on this path), eight ranks at a time.
+template <typename T>
+__device__ __forceinline__ f32x4 lora_row(const RaggedArgs& p, int row, int col, int a, bool inside)
+{
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    const T* up = static_cast<const T*>(p.up) + (int64_t)a * p.stride_up;
+    for (int r = 0; r < p.rank; r += 8) {
+        f32x4 t[2];
+        load_t(p, row, r, t);
+        T u[4][8];
+        if (inside && p.up_kc && r + 8 <= p.rank) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                u32x4_elem<T> c[sizeof(T) / 2];
+#pragma unroll
+                for (int h = 0; h < (int)sizeof(T) / 2; ++h)
+                    c[h] = reinterpret_cast<const u32x4_elem<T>*>(up + (col + s) * p.ld_up + r)[h];
+                __builtin_memcpy(u[s], c, sizeof(u[s]));
+            }
+        } else if (inside && !p.up_kc) {
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+                using C = typename RawLoad<4 * sizeof(T)>::T;
+                const C c = *reinterpret_cast<const C*>(
+                    up + (int64_t)(r + v < p.rank ? r + v : p.rank - 1) * p.ld_up + col);
+                T e[4];
+                __builtin_memcpy(e, &c, sizeof(e));
+#pragma unroll
+                for (int s = 0; s < 4; ++s) u[s][v] = e[s];
+            }
+        } else {
+            const int64_t kr = p.up_kc ? 1 : p.ld_up, kc = p.up_kc ? p.ld_up : 1;
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    u[s][v] = up[(r + v < p.rank ? r + v : p.rank - 1) * kr +
+                                 (col + s < p.N ? col + s : p.N - 1) * kc];
+        }
+#pragma unroll
+        for (int v = 0; v < 8; ++v)
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                sum[s] += r + v < p.rank ? t[v / 4][v % 4] * to_f32(u[s][v]) : 0.0f;
+    }
+    return sum;
+}
+
+// T op(up_a) of a fragment of 32 rows from `row0` (of a tile whose rows start
+// at m_tile and have the adapters adapter[]) and NQ fragments of 32 columns
+// from `col0`, added to the sums a lane holds of them: row l % 32, four columns
+// each in sum[q][vg] (the epilogue's copies of the accumulators: adding to the
+// accumulators themselves, in code with branches, makes the compiler copy and
+// spill them).
+//
+// The fragment takes its rows' adapters one after another, into a product of
+// its own that only the adapter's rows add: whatever an adapter holds
+// (infinities, NaN) reaches no other row.  The loads are free of branches
+// (clamped and zeroed instead), and the first adapter's are issued ahead of
+// T's, so a fragment of one adapter waits for memory once per 32 ranks.
+template <int KIND, int NQ, int VG>
+__device__ __forceinline__ void lora_fragment(const RaggedArgs& p, const int* adapter, int m_tile,
+                                              int row0, int col0, int lane, f32x4 (&sum)[NQ][VG])
 {
     using T = typename MfmaShape<KIND>::T;
-    constexpr int FM = MfmaShape<KIND>::FM, ACC = MfmaShape<KIND>::ACC;
-    constexpr int VEC = 16 / sizeof(T), KSTEP = 64 / FM * VEC;
-    constexpr int NK = 4;  // fragment steps of rank held at once
-    const int m_end = m0 + MF * FM < p.M ? m0 + MF * FM : p.M;
-    if (m0 >= m_end || n0 >= p.N) return;
+    using Acc = typename AccType<KIND>::type;
+    constexpr int FM = MfmaShape<KIND>::FM, VEC = 16 / sizeof(T), KSTEP = 64 / FM * VEC;
+    constexpr int NK = 2;  // fragment steps of rank at once
+    static_assert(FM == 32 && VG == 4, "accumulator layout");
+    int row = row0 + lane % FM;
+    const int mine = row < p.M ? adapter[row - m_tile] : -1;
+    const uint64_t some = __ballot(mine >= 0);
+    if (some == 0) return;
+    if (row >= p.M) row = p.M - 1;
     const int kl = VEC * (lane / FM);
-    for (int s = first_segment(p, m0, lane); s < p.groups; ++s) {
-        int start, size;
-        group_span(p, s, start, size);
-        if (start >= m_end) break;
-        const int end = start + size;
-        const int a = p.ids ? p.ids[s] : s;
-        if (size == 0 || end <= m0 || a < 0 || a >= p.adapters) continue;
-        const T* up = static_cast<const T*>(p.up) + (int64_t)a * p.stride_up;
-        for (int r0 = 0; r0 < p.rank; r0 += NK * KSTEP) {
+    for (int r0 = 0; r0 < p.rank; r0 += NK * KSTEP) {
+        u32x4 b[NQ][NK];
+        auto load_up = [&](int a) __attribute__((always_inline)) {
+            const T* up = static_cast<const T*>(p.up) + (int64_t)a * p.stride_up;
+            int64_t at[NQ];
 #pragma unroll
-            for (int i = 0; i < MF; ++i) {
-                const int rf = m0 + i * FM;  // the fragment's first row
-                if (rf >= end || rf + FM <= start) continue;
-                const int row = rf + lane % FM;
-                const bool mine = row >= start && row < end;
-                u32x4 hi[NK], lo[NK];
+            for (int q = 0; q < NQ; ++q) {
+                const int col = col0 + q * FM + lane % FM;
+                at[q] = (int64_t)(col < p.N ? col : p.N - 1) * (p.up_kc ? p.ld_up : 1);
+            }
+            if (p.up_kc && p.rank % VEC == 0) {
 #pragma unroll
-                for (int kk = 0; kk < NK; ++kk) {
-                    const int k = r0 + kk * KSTEP + kl;
-                    float t[VEC] = {};
-                    if (mine && k < p.rank_pad) {
-                        const float* src = p.t + (int64_t)row * p.rank_pad + k;
-                        for (int sp = 0; sp < p.splits; ++sp, src += (int64_t)p.rows * p.rank_pad)
-#pragma unroll
-                            for (int v = 0; v < VEC / 4; ++v) {
-                                const f32x4 q = reinterpret_cast<const f32x4*>(src)[v];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) t[4 * v + e] += q[e];
-                            }
-                    }
-                    split_terms(t, hi[kk], lo[kk]);
-                }
-#pragma unroll
-                for (int j = 0; j < NF; ++j) {
-                    const int col = n0 + j * FM + lane % FM;
-                    Acc tmp = {};
+                for (int q = 0; q < NQ; ++q)
 #pragma unroll
                     for (int kk = 0; kk < NK; ++kk) {
-                        if (r0 + kk * KSTEP >= p.rank) break;
-                        const u32x4 b = load_k_chunk<T>(up, p.ld_up, p.up_kc, col, col < p.N,
-                                                        r0 + kk * KSTEP + kl, p.rank);
-                        mfma_step<KIND>(b, hi[kk], tmp);
-                        if constexpr (sizeof(T) == 2) mfma_step<KIND>(b, lo[kk], tmp);
+                        const int k = r0 + kk * KSTEP + kl;
+                        const u32x4 v = *reinterpret_cast<const u32x4_elem<T>*>(
+                            up + at[q] + (k < p.rank ? k : 0));
+                        b[q][kk] = k < p.rank ? v : u32x4{0, 0, 0, 0};
                     }
-                    if (mine)
+            } else {
 #pragma unroll
-                        for (int v = 0; v < ACC; ++v) acc[i][j][v] += tmp[v];
-                }
+                for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                    for (int kk = 0; kk < NK; ++kk)
+                        b[q][kk] = clamped_chunk<T>(up + at[q], p.up_kc ? 1 : p.ld_up,
+                                                    r0 + kk * KSTEP + kl, p.rank);
             }
+        };
+        int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(some));
+        load_up(a);
+        // the rows' T as operand terms
+        u32x4 hi[NK], lo[NK];
+#pragma unroll
+        for (int kk = 0; kk < NK; ++kk) {
+            const int k = r0 + kk * KSTEP + kl;
+            f32x4 q[VEC / 4];
+            load_t(p, row, k < p.rank_pad ? k : 0, q);
+            float t[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) t[e] = k < p.rank_pad ? q[e / 4][e % 4] : 0.0f;
+            split_terms(t, hi[kk], lo[kk]);
+        }
+        for (uint64_t left = some;;) {
+            left &= ~__ballot(mine == a);
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                Acc v = {};
+#pragma unroll
+                for (int kk = 0; kk < NK; ++kk) {
+                    mfma_step<KIND>(b[q][kk], hi[kk], v);
+                    if constexpr (sizeof(T) == 2) mfma_step<KIND>(b[q][kk], lo[kk], v);
+                }
+#pragma unroll
+                for (int e = 0; e < 4 * VG; ++e) sum[q][e / 4][e % 4] += mine == a ? v[e] : 0.0f;
+            }
+            if (left == 0) break;
+            a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
+            load_up(a);
         }
     }
 }
@@ -155,72 +314,6 @@ __device__ __forceinline__ void mfma16(const u32x4& a, const u32x4& b, f32x4& ac
         for (int e = 0; e < 4; ++e)
             acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(b[e]), __uint_as_float(a[e]),
                                                        acc, 0, 0, 0);
-    }
-}
-
-// T = s_a X op(down_a): one block of 16*RF rows of one segment per workgroup
-// (blockIdx.x), a slice of K per blockIdx.y (its own partial sums of T) and
-// 16*NF columns of rank per blockIdx.z.  The eight waves split the slice's K
-// in runs of 4 chunk rows (256 contiguous bytes of each row of X and, where k
-// is contiguous, of down), load fragments straight from memory into the MFMA
-// lane layout and add their sums through LDS in wave order.
-constexpr int SHRINK_WAVES = 8;
-template <typename T, int RF, int NF, bool KC>
-__global__ __launch_bounds__(64 * SHRINK_WAVES) void lora_shrink_kernel(
-    RaggedArgs p, const void* down_v, int64_t ld_down, int64_t stride_down, int k_slice, float* t_out)
-{
-    constexpr int VEC = 16 / sizeof(T), KB = 4 * VEC, U = 4;
-    RowTile t;
-    if (!find_row_tile<16 * RF>(p, blockIdx.x, 1, t)) return;
-    const int a = p.ids ? p.ids[t.group] : t.group;
-    if (a < 0 || a >= p.adapters) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int r0 = t.in_group * 16 * RF;  // first row within the segment
-    const int c0 = blockIdx.z * 16 * NF;  // first column of rank
-    const int k_lo = blockIdx.y * k_slice;
-    const int k_hi = k_lo + k_slice < p.K ? k_lo + k_slice : p.K;
-    const T* X = static_cast<const T*>(p.A) + (int64_t)t.start * p.lda;
-    const T* down = static_cast<const T*>(down_v) + (int64_t)a * stride_down;
-    f32x4 acc[RF][NF] = {};
-    for (int kw = k_lo + wave * U * KB; kw < k_hi; kw += SHRINK_WAVES * U * KB) {
-        u32x4 xa[U][RF], xb[U][NF];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = kw + u * KB + VEC * (lane / 16);
-#pragma unroll
-            for (int i = 0; i < RF; ++i) {
-                const int row = r0 + i * 16 + lane % 16;
-                xa[u][i] = load_k_chunk<T>(X, p.lda, true, row, row < t.size, k, k_hi);
-            }
-#pragma unroll
-            for (int j = 0; j < NF; ++j) {
-                const int col = c0 + j * 16 + lane % 16;
-                xb[u][j] = load_k_chunk<T>(down, ld_down, KC, col, col < p.rank, k, k_hi);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < RF; ++i)
-#pragma unroll
-                for (int j = 0; j < NF; ++j) mfma16<T>(xa[u][i], xb[u][j], acc[i][j]);
-    }
-    __shared__ f32x4 part[SHRINK_WAVES][RF * NF][64];
-#pragma unroll
-    for (int i = 0; i < RF; ++i)
-#pragma unroll
-        for (int j = 0; j < NF; ++j) part[wave][i * NF + j][lane] = acc[i][j];
-    __syncthreads();
-    const float scale = p.scales ? p.scales[a] : 1.0f;
-    float* out = t_out + (int64_t)blockIdx.y * p.rows * p.rank_pad;
-    for (int f = wave; f < RF * NF; f += SHRINK_WAVES) {
-        const int row = r0 + f / NF * 16 + lane % 16;
-        const int col = c0 + f % NF * 16 + 4 * (lane / 16);
-        if (row >= t.size || col >= p.rank_pad) continue;
-        f32x4 sum = part[0][f][lane];
-#pragma unroll
-        for (int w = 1; w < SHRINK_WAVES; ++w) sum += part[w][f][lane];
-        *reinterpret_cast<f32x4*>(out + (int64_t)(t.start + row) * p.rank_pad + col) = scale * sum;
     }
 }
 

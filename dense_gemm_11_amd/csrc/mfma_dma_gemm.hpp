@@ -458,6 +458,50 @@ struct DmaOperand {
         }
     }
 
+    // One step of a matrix in either orientation, element (mn, k) at mn * s_mn +
+    // k * s_k, into registers and from there into LDS: the few steps of T and up
+    // (RAG_LORA), for which all loads of both operands are issued before the
+    // first is waited for.  WIDE: 16 bytes at a time, where the matrix has the
+    // operand's orientation and every chunk that starts inside ends inside;
+    // else an element at a time.  Zero outside [0, rlim) x [0, K).
+    template <bool WIDE>
+    __device__ __forceinline__ void fetch(const T* x, int64_t s_mn, int64_t s_k, int rlim, int k0,
+                                          int K, int tid, u32x4 (&v)[GL]) const
+    {
+        static_for<GL>([&](auto i_c) __attribute__((always_inline)) {
+            const int q = tid + decltype(i_c)::value * Cfg::THREADS;
+            const int row = q / SCPR, c = q % SCPR;
+            T e[VEC];
+            if constexpr (WIDE) {
+                const int mn = KC ? row : c * VEC, k = k0 + (KC ? c * VEC : row);
+                const bool in = mn < rlim && k < K;
+                v[i_c] = *reinterpret_cast<const u32x4_elem<T>*>(
+                    x + (in ? (int64_t)mn * s_mn + (int64_t)k * s_k : 0));
+                v[i_c] = in ? v[i_c] : u32x4{0, 0, 0, 0};
+            } else {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const int mn = KC ? row : c * VEC + j, k = k0 + (KC ? c * VEC + j : row);
+                    e[j] = x[(mn < rlim ? mn : rlim - 1) * s_mn + (k < K ? k : K - 1) * s_k];
+                }
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const int mn = KC ? row : c * VEC + j, k = k0 + (KC ? c * VEC + j : row);
+                    e[j] = mn < rlim && k < K ? e[j] : T(0);
+                }
+                v[i_c] = pack_chunk<T>(e);
+            }
+        });
+    }
+    __device__ __forceinline__ void put(const u32x4 (&v)[GL], char* lds, int tid, int half) const
+    {
+        static_for<GL>([&](auto i_c) __attribute__((always_inline)) {
+            const int q = tid + decltype(i_c)::value * Cfg::THREADS;
+            if (CHUNKS % Cfg::THREADS == 0 || q < CHUNKS)
+                *reinterpret_cast<u32x4*>(lds + L::off(q / SCPR, q % SCPR + half * SCPR)) = v[i_c];
+        });
+    }
+
     // ---- fragment reads (FragAddr: per-lane base registers + constants)
     using FA = FragAddr<Cfg, R, KC, KD, WT, NWP>;
     static constexpr int NREAD_PER_FRAG = FA::NPC;
@@ -556,8 +600,8 @@ __device__ __forceinline__ void barrier_only() { asm volatile("s_barrier" ::: "m
 // no second kernel reads D back.
 //
 // RAG (ragged.hpp): the workgroup first narrows p to its group of rows, or
-// (RAG_LORA) adds its rows' low-rank products to the accumulators between
-// the mainloop and the epilogue.
+// (RAG_LORA) adds its rows' low-rank products, as more of K where the tile has
+// one adapter and in the epilogue where it has several.
 template <class Cfg, bool A_KC, bool B_KC, bool ALIGNED, bool SK, bool OUT_T, bool OUT_BF16, bool EPI,
           int RAG, class Args>
 __device__ __forceinline__ void dma_gemm_body(Args p)
@@ -619,6 +663,10 @@ __device__ __forceinline__ void dma_gemm_body(Args p)
     const int wave_m0 = (wave / Cfg::WN) * Cfg::WTM;
     const int wave_n0 = (wave % Cfg::WN) * Cfg::WTN;
     using T = typename Cfg::T;
+    // RAG_LORA: the adapters of the tile's rows, and the tile's: one that its K
+    // takes in, or TILE_NONE or TILE_MIXED
+    __shared__ int adapter[RAG == RAG_LORA ? BM : 1];
+    int tile_a = TILE_NONE;
     // the tile of a group's product (RAG_ROWS, RAG_K)
     int tm_g = 0, tn_g = 0;
     if constexpr (RAG == RAG_ROWS || RAG == RAG_K)
@@ -739,6 +787,13 @@ __device__ __forceinline__ void dma_gemm_body(Args p)
 #pragma unroll
         for (int j = 0; j < NF; ++j) acc[i][j] = Acc{};
 
+    // the tile's adapter, found while the first copies are under way
+    auto find_adapter = [&]() __attribute__((always_inline)) {
+        if constexpr (RAG == RAG_LORA)
+            tile_a = tile_adapter(p, m0, m0 + BM < p.M ? m0 + BM : p.M, lane,
+                                  Cfg::ES == 4 ? p.splits == 1 : p.t_terms != nullptr);
+    };
+
     // prologue: the copies the barriers of steps -VP .. -1 would have issued
     // (steps 0 .. AHEAD-1, and when paired pairs 0 .. NP-1), then wait for
     // step 0
@@ -746,6 +801,7 @@ __device__ __forceinline__ void dma_gemm_body(Args p)
 #pragma unroll
         for (int s = 0; s < AHEAD; ++s)
             if (s < nk) load(s, stage(s));
+        find_adapter();
         if (nk >= AHEAD) wait_vm_lgkm0<WAIT_PRO>();
         else wait_vm_lgkm0<0>();
     } else {
@@ -759,6 +815,7 @@ __device__ __forceinline__ void dma_gemm_body(Args p)
                 if (2 * q < nk) load_pair(q, pr(q % NP));
             }
         });
+        find_adapter();
         if (nk > LOOK) wait_vm_lgkm0<WAIT_PRO>();
         else wait_vm_lgkm0<0>();
     }
@@ -958,6 +1015,44 @@ __device__ __forceinline__ void dma_gemm_body(Args p)
         if constexpr (P > 5)
             if (kt + 5 < nk) step(I5{}, kt + 5);
     }
+    // RAG_LORA, a tile of one adapter: BK ranks at a time of T (its terms in
+    // slots 0 and 1) and up, through LDS.  Not in the pipeline above: there the
+    // copies' registers would meet the fragments'.
+    if constexpr (RAG == RAG_LORA) {
+        constexpr int TERMS = Cfg::ES == 2 ? 2 : 1;
+        const int ldt = TERMS * p.rank_pad;
+        const T* t = (Cfg::ES == 2 ? reinterpret_cast<const T*>(p.t_terms)
+                                   : reinterpret_cast<const T*>(p.t)) + (int64_t)m0 * ldt;
+        const int64_t s_n = p.up_kc ? p.ld_up : 1, s_k = p.up_kc ? 1 : p.ld_up;
+        const T* up = static_cast<const T*>(p.up) + (int64_t)tile_a * p.stride_up + n0 * s_n;
+        const bool wide = p.up_kc == (int)B_KC && (B_KC ? p.rank % Cfg::VEC == 0 : rlim_b >= BN);
+#pragma unroll 1
+        for (int r0 = 0; tile_a >= 0 && r0 < p.rank; r0 += BK) {
+            u32x4 va[TERMS][OpA::GL], vb[OpB::GL];
+#pragma unroll
+            for (int u = 0; u < TERMS; ++u)
+                oa.template fetch<true>(t + u * p.rank_pad, ldt, 1, rlim_a, r0, p.rank_pad, tid, va[u]);
+            if (wide) ob.template fetch<true>(up, s_n, s_k, rlim_b, r0, p.rank, tid, vb);
+            else ob.template fetch<false>(up, s_n, s_k, rlim_b, r0, p.rank, tid, vb);
+            __syncthreads();  // every wave is done reading the slots
+            static_for<TERMS>([&](auto u_c) __attribute__((always_inline)) {
+                constexpr int u = decltype(u_c)::value;
+                oa.put(va[u], a_lds(u), tid, PA ? u : 0);
+                ob.put(vb, b_lds(u), tid, PB ? u : 0);
+            });
+            __syncthreads();
+            oa.refresh();
+            ob.refresh();
+            static_for<TERMS * NKS>([&](auto x_c) __attribute__((always_inline)) {
+                constexpr int u = decltype(x_c)::value / NKS, ks = decltype(x_c)::value % NKS;
+                read_frags(std::integral_constant<int, u>{}, std::integral_constant<int, ks>{}, I0{});
+#pragma unroll
+                for (int i = 0; i < MF; ++i)
+#pragma unroll
+                    for (int j = 0; j < NF; ++j) mfma_step<Cfg::KIND>(fb[0][j], fa[0][i], acc[i][j]);
+            });
+        }
+    }
     };  // tile_work
 
     // Index (in f32x4 units) of a thread's accumulator group (i, j, vg) in a
@@ -991,7 +1086,19 @@ __device__ __forceinline__ void dma_gemm_body(Args p)
             return *reinterpret_cast<const f32x4_a4*>(q);
         }
     };
-    auto store4 = [](OutT* q, f32x4 v) __attribute__((always_inline)) {
+    // (The ragged calls store in the ordinary way where rows of D do not start
+    // on 128-byte lines, so that neighbouring tiles' parts of a line meet in L2:
+    // 59 groups of 1216x4680 bf16, 0.444 -> 0.334 ms.)
+    auto store4 = [&](OutT* q, f32x4 v) __attribute__((always_inline)) {
+        if constexpr (RAG != RAG_NONE) {
+            if (!p.d_lines) {
+                if constexpr (OUT_BF16)
+                    *reinterpret_cast<bf16x4_a2*>(q) = __builtin_convertvector(v, bf16x4);
+                else
+                    *reinterpret_cast<f32x4_a4*>(q) = v;
+                return;
+            }
+        }
         if constexpr (OUT_BF16)
             __builtin_nontemporal_store(__builtin_convertvector(v, bf16x4),
                                         reinterpret_cast<bf16x4_a2*>(q));
@@ -1092,6 +1199,10 @@ __device__ __forceinline__ void dma_gemm_body(Args p)
                 sum[q][vg] = f32x4{acc[i][j][4 * vg], acc[i][j][4 * vg + 1], acc[i][j][4 * vg + 2],
                                    acc[i][j][4 * vg + 3]};
         }
+        if constexpr (RAG == RAG_LORA)
+            if (tile_a == TILE_MIXED)
+                lora_fragment<Cfg::KIND>(p, adapter, m0, m0 + wave_m0 + o * FM,
+                                         n0 + wave_n0 + qh * DC, lane, sum);
         if constexpr (SK) {
             for (int64_t c = c0; c < c1; ++c) {
                 const auto rsrc = part_rsrc(c);
@@ -1129,7 +1240,9 @@ __device__ __forceinline__ void dma_gemm_body(Args p)
         // (the compiler cannot move a C load above an earlier D store itself:
         // C and D may be the same matrix).  Every element is still read
         // before it is written, so C == D stays correct.
-        constexpr int CG = NT < 4 ? NT : 4;
+        // (RAG_K: all of a batch's: with few rows per group, the call is the
+        // reading and writing of C and D.)
+        constexpr int CG = NT < 4 || RAG == RAG_K ? NT : 4;
         auto interior_rows = [&](auto act_c, auto clamp_c) __attribute__((always_inline)) {
 #pragma unroll 1
             for (int t0 = 0; t0 < NT; t0 += CG) {
@@ -1220,9 +1333,12 @@ __device__ __forceinline__ void dma_gemm_body(Args p)
     } else if constexpr (!SK) {
         int tm, tn;
         tile_coords(p, tm, tn);
-        tile_work(tm, tn, 0, nk_all);
-        if constexpr (RAG == RAG_LORA)
-            lora_expand<Cfg::KIND>(p, tm * BM + wave_m0, tn * BN + wave_n0, lane, acc);
+        if constexpr (RAG == RAG_LORA) {
+            tile_work(tm, tn, 0, nk_all);
+            if (tile_a == TILE_MIXED) map_adapters<BM, Cfg::THREADS>(p, tm * BM, tid, adapter);
+        } else {
+            tile_work(tm, tn, 0, nk_all);
+        }
         epilogue(tm, tn, 0, 0);
     } else {
         // Stream-K ("GEMM on NVIDIA GPUs", section 5: split-K partial sums

@@ -17,14 +17,17 @@ namespace dg {
 //  RAG_K   : D_g = alpha s_g op(A)[:, rows of g] op(B)[rows of g, :] + beta C_g
 //            (the rows are the product's K);
 //  RAG_LORA: D = alpha (A op(B) + T op(up_a)) + beta C, T the rows' products
-//            with their segment's adapter, already scaled (lora.hpp).
-enum : int { RAG_NONE = 0, RAG_ROWS = 1, RAG_K = 2, RAG_LORA = 3 };
+//            with their segment's adapter, already scaled (lora.hpp);
+//  RAG_SHRINK: those products, T[rows of s] = s_a A[rows of s] op(down_a)
+//            (stream.hpp).
+enum : int { RAG_NONE = 0, RAG_ROWS = 1, RAG_K = 2, RAG_LORA = 3, RAG_SHRINK = 4 };
 
 struct RaggedArgs : GemmArgs {
     const int32_t* offsets;  // groups + 1
     const float* scales;     // one per group (RAG_LORA: per adapter), or null
     int groups;
     int rows;                // the rows that offsets divide
+    int d_lines;             // D's rows (and groups) start on 128-byte lines
     int64_t stride_b;        // elements between the groups' B (RAG_ROWS)
     int64_t stride_c, stride_d;  // ... C and D (RAG_K)
     // RAG_LORA: adapter of each segment (< 0 or >= adapters: none; null: the
@@ -36,6 +39,8 @@ struct RaggedArgs : GemmArgs {
     const void* up;
     int64_t ld_up, stride_up;
     int up_kc;               // up stored N x rank (rank contiguous)
+    int k_slice;             // RAG_SHRINK: K of each of the `splits` slices
+    uint16_t* t_terms;       // bf16 operands: T as two terms (lora.hpp), or null
 };
 
 // First row and length of group g.

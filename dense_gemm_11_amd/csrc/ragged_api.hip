@@ -57,23 +57,33 @@ TileList tile_list(TileTable dma, TileTable stream)
     return l;
 }
 
-// The tallest tile up to the forced height, else the first that `wants(tile,
-// streaming)` accepts, else the last.
+// The tallest tile up to the forced height, else the one of least expected
+// time; tiles(t) is the number of output tiles of t a call has, or expects.
 template <class F>
-const RaggedTile& pick_tile(const TileList& t, int forced, F wants)
+const RaggedTile& pick_tile(const TileList& t, int forced, int64_t K, F tiles)
 {
-    for (int i = 0; i + 1 < t.n; ++i)
-        if (forced > 0 ? t[i].bm <= forced : wants(t[i], i >= t.n_dma)) return t[i];
-    return t[t.n - 1];
+    int best = t.n - 1;
+    if (forced > 0) {
+        for (int i = 0; i < t.n; ++i)
+            if (t[i].bm <= forced) return t[i];
+        return t[best];
+    }
+    double best_us = 0.0;
+    for (int i = 0; i < t.n; ++i) {
+        const double us = expected_us(t[i], tiles(t[i]), (double)K, device_cus());
+        if (i == 0 || us < best_us) {
+            best = i;
+            best_us = us;
+        }
+    }
+    return t[best];
 }
 
-// A streaming tile holds the rows there are on average, and the wide ones
-// have at least half a workgroup per compute unit (narrower ones read A more
-// often).
-bool wants_stream(const RaggedTile& t, int bn, int64_t busy, int64_t avg, int64_t N)
+// Rows of tiles of height bm in `busy` groups of avg rows on average: the last
+// tile of a group is half full.
+double row_tiles(double busy, double avg, int bm)
 {
-    if (t.bm > 16) return avg > t.bm / 2;
-    return 2 * busy * ceil_div(avg, t.bm) * ceil_div(N, bn) >= device_cus();
+    return busy * std::max(1.0, avg / bm + 0.5);
 }
 
 void log_call(gemm_handle_t h, const char* what, const RaggedArgs& a, int bm, int bn, int64_t grid)
@@ -142,6 +152,7 @@ gemm_status_t gemm_run_grouped(gemm_handle_t h, gemm_op_t transB, int64_t M, int
     a.beta = beta;
     a.c_vec = beta != 0.0f && aligned_to(C, eo);
     a.d_vec = aligned_to(D, eo);
+    a.d_lines = aligned_to(D, 128) && ldd * eo % 128 == 0;
     a.offsets = groups->offsets;
     a.scales = groups->scales;
     a.groups = groups->groups;
@@ -149,14 +160,11 @@ gemm_status_t gemm_run_grouped(gemm_handle_t h, gemm_op_t transB, int64_t M, int
     a.stride_b = strideB;
     // a group holds M / groups rows on average, and the host knows no more
     const int64_t busy = std::min<int64_t>(groups->groups, M);
-    const int64_t avg = ceil_div(M, busy);
     const TileList tiles = dtype == GEMM_DTYPE_F32 ? tile_list(ragged_rows_f32, stream_rows_f32)
                                                    : tile_list(ragged_rows_bf16, stream_rows_bf16);
-    const RaggedTile& t = pick_tile(tiles, h->forced_rows, [&](const RaggedTile& x, bool stream) {
-        if (stream) return wants_stream(x, x.bn[b_kc], busy, avg, N);
-        if (x.bm == 128) return avg > 64;
-        return M >= busy * 3 * x.bm / 4 &&
-               4 * (M / x.bm) * ceil_div(N, x.bn[b_kc]) >= 3 * (int64_t)device_cus();
+    const RaggedTile& t = pick_tile(tiles, h->forced_rows, K, [&](const RaggedTile& x) {
+        return ceil_div(N, x.bn[b_kc]) *
+               (busy > 1 ? row_tiles((double)busy, (double)M / busy, x.bm) : (double)ceil_div(M, x.bm));
     });
     const int bn = t.bn[b_kc];
     const int64_t kk = K + t.bk;
@@ -228,6 +236,7 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_handle_t h, int64_t M, int64_t N, int6
     a.beta = beta;
     a.c_vec = beta != 0.0f && aligned_to(C, eo);
     a.d_vec = aligned_to(D, eo);
+    a.d_lines = aligned_to(D, 128) && ldd * eo % 128 == 0 && strideD * eo % 128 == 0;
     a.offsets = groups->offsets;
     a.scales = groups->scales;
     a.groups = (int)G;
@@ -236,8 +245,8 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_handle_t h, int64_t M, int64_t N, int6
     a.stride_d = strideD;
     const TileList tiles =
         tile_list(dtype == GEMM_DTYPE_F32 ? ragged_k_f32 : ragged_k_bf16, nullptr);
-    const RaggedTile& t = pick_tile(tiles, h->forced_rows, [&](const RaggedTile& x, bool) {
-        return 4 * G * ceil_div(M, x.bm) * ceil_div(N, x.bn[0]) >= 3 * (int64_t)device_cus();
+    const RaggedTile& t = pick_tile(tiles, h->forced_rows, rows / G, [&](const RaggedTile& x) {
+        return (double)(G * ceil_div(M, x.bm) * ceil_div(N, x.bn[0]));
     });
     const int bn = t.bn[0];
     // one K-step's offsets (the kernel bases each step anew)
@@ -260,10 +269,11 @@ size_t gemm_lora_workspace_bytes(int64_t M, int rank)
 {
     using namespace dg;
     if (M <= 0 || rank <= 0) return 0;
-    // rows of T's partial sums: at most 16 slices, and at most
-    // ceil(8192 / M) of them (gemm_run_lora); does not decrease with M
+    // rows of T's partial sums: at most 4 slices, and at most ceil(8192 / M)
+    // of them; or T and its bf16 terms (gemm_run_lora); does not decrease with M
     const int64_t pad = ceil_div(rank, LORA_PAD) * LORA_PAD;
-    return (size_t)(std::min<int64_t>(16 * M, 8192 + M) * pad) * sizeof(float);
+    return (size_t)(std::max<int64_t>(2 * M, std::min<int64_t>(4 * M, 8192 + M)) * pad) *
+           sizeof(float);
 }
 
 gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_t N, int64_t K,
@@ -324,6 +334,7 @@ gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_
     a.beta = beta;
     a.c_vec = beta != 0.0f && aligned_to(C, eo);
     a.d_vec = aligned_to(D, eo);
+    a.d_lines = aligned_to(D, 128) && ldd * eo % 128 == 0;
     a.offsets = lora->offsets;
     a.scales = lora->scales;
     a.groups = lora->segments;
@@ -339,10 +350,8 @@ gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_
     a.up_kc = up_kc;
     const TileList tiles = dtype == GEMM_DTYPE_F32 ? tile_list(ragged_lora_f32, stream_lora_f32)
                                                    : tile_list(ragged_lora_bf16, stream_lora_bf16);
-    const RaggedTile& t = pick_tile(tiles, h->forced_rows, [&](const RaggedTile& x, bool stream) {
-        if (stream) return wants_stream(x, x.bn[b_kc], 1, M, N);
-        if (x.bm == 128) return M > 64;
-        return 4 * ceil_div(M, x.bm) * ceil_div(N, x.bn[b_kc]) >= 3 * (int64_t)device_cus();
+    const RaggedTile& t = pick_tile(tiles, h->forced_rows, K, [&](const RaggedTile& x) {
+        return (double)(ceil_div(M, x.bm) * ceil_div(N, x.bn[b_kc]));
     });
     const int bn = t.bn[b_kc];
     const int64_t kk = K + t.bk;
@@ -354,25 +363,44 @@ gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_
     a.group_m = std::min(a.tiles_m, 4);
     const int64_t grid = (int64_t)a.tiles_m * a.tiles_n;
     if (grid > INT_MAX) return GEMM_ERR_NOT_SUPPORTED;
-    ShrinkCall sc{};
-    sc.down = lora->down;
-    sc.ld_down = lora->ld_down;
-    sc.stride_down = lora->stride_down;
-    sc.down_kc = down_kc;
-    sc.t = static_cast<float*>(ws);
-    const int64_t segs = std::min<int64_t>(lora->segments, M);
-    sc.tall = M >= 32 * segs;
-    // slices of K until about 512 workgroups share the first product, each
-    // slice at least one round of the eight waves (8 runs of 4 chunk rows)
-    const int64_t bm = sc.tall ? 32 : 16, round = 8 * 4 * (64 / es);
-    const int64_t blocks = std::max<int64_t>(1, (M + segs * (bm - 1)) / bm);
-    int64_t splits = std::min<int64_t>({16, ceil_div(512, blocks), ceil_div(K, round)});
-    splits = std::max<int64_t>(1, std::min<int64_t>(splits, ceil_div(8192, M)));
-    sc.k_slice = (int)(ceil_div(ceil_div(K, splits), 4 * (64 / es)) * 4 * (64 / es));
-    sc.splits = (int)ceil_div(K, sc.k_slice);
-    a.splits = sc.splits;
+    // the first product: blocks of as many rows as a segment has on average,
+    // as narrow as the rank allows, and slices of K until there is a
+    // workgroup per compute unit or a slice is two batches per wave
+    RaggedArgs f = a;
+    f.B = lora->down;
+    f.ldb = lora->ld_down;
+    f.stride_b = lora->stride_down;
+    f.N = (int)R;
+    f.C = nullptr;
+    f.D = static_cast<float*>(ws);
+    f.ldd = a.rank_pad;
+    f.alpha = 1.0f;
+    f.beta = 0.0f;
+    f.group_m = 4;
+    const int64_t segs = std::min<int64_t>(lora->segments, M), avg = ceil_div(M, segs);
+    int n_first = 0;
+    const RaggedTile* first = (dtype == GEMM_DTYPE_F32 ? stream_shrink_f32 : stream_shrink_bf16)(&n_first);
+    int fi = 0;
+    while (fi + 1 < n_first &&
+           ((fi + 2 < n_first && first[fi].bn[down_kc] < R) ||
+            (first[fi].bm > 16 && (avg <= first[fi].bm / 2 || 2 * M < device_cus() * first[fi].bm))))
+        ++fi;
+    const RaggedTile& ft = first[fi];
+    f.tiles_n = (int)ceil_div(R, ft.bn[down_kc]);
+    const int64_t blocks = (M + segs * (ft.bm - 1)) / ft.bm * f.tiles_n;
+    int64_t splits = std::min<int64_t>({4, ceil_div(device_cus(), blocks), ceil_div(8192, M),
+                                        K / (8 * 4 * ft.bk)});
+    // the direct-to-LDS tiles want T whole, for their K-steps
+    splits = t.stream ? std::max<int64_t>(1, splits) : 1;
+    if (!t.stream && dtype != GEMM_DTYPE_F32)
+        a.t_terms = f.t_terms = reinterpret_cast<uint16_t*>(static_cast<float*>(ws) + M * a.rank_pad);
+    f.k_slice = (int)(ceil_div(ceil_div(K, splits), ft.bk) * ft.bk);
+    f.splits = a.splits = (int)ceil_div(K, f.k_slice);
+    if (blocks > INT_MAX ||
+        !(down_kc ? panel_fits(ft.bn[1] - 1, f.ldb, kk, es) : panel_fits(kk, f.ldb, ft.bn[0], es)))
+        return GEMM_ERR_NOT_SUPPORTED;
     if (h->fail_launch) return GEMM_ERR_HIP;
-    if (launch_shrink(a, sc, dtype != GEMM_DTYPE_F32, stream) != hipSuccess ||
+    if (ft.fn[down_kc][0](f, (int)blocks, stream) != hipSuccess ||
         t.fn[b_kc][dtype == GEMM_DTYPE_BF16_BF16](a, (int)grid, stream) != hipSuccess)
         return GEMM_ERR_HIP;
     h->last_rows = t.bm;

@@ -8,10 +8,33 @@ namespace dg {
 
 typedef hipError_t (*RaggedFn)(const RaggedArgs&, int grid, hipStream_t);
 
+// Microseconds of a launch whose tiles find a compute unit each, and of each
+// tile where they share the units: a fixed part and a part per 1000 of K.
+struct TileCost {
+    float alone, alone_k, each, each_k;
+};
+
 struct RaggedTile {
     int bm, bn[2], bk;  // bn of either layout of B
     RaggedFn fn[2][2];  // [B k-contiguous][bf16 output] (RAG_K: [0] only)
+    bool stream;        // a streaming tile
+    TileCost cost;
 };
+
+// Expected time of `tiles` tiles of t.  The costs are least-squares fits of
+// this form to timings of every tile on random calls of each kind (70 to 140
+// of bf16 operands, 30 to 60 of fp32: 1 to 16384 rows, 1 to 128 groups, K 128
+// to 8192, N 8 to 14336); taking the tile of least expected time runs within 1
+// to 6 % of the best tile on average.
+inline double expected_us(const RaggedTile& t, double tiles, double K, int cus)
+{
+    const double n = tiles > cus ? tiles / cus : 1.0, k = K / 1000.0;
+    const double alone = t.cost.alone + k * t.cost.alone_k;
+    // workgroups that have a unit to themselves come in whole rounds
+    const double rounds = t.bm * t.bn[0] >= 192 * 256 ? (double)(int64_t)(n + 0.9) : n;
+    const double full = rounds * (t.cost.each + k * t.cost.each_k);
+    return alone > full ? alone : full;
+}
 
 // Streaming tiles (stream.hpp), tallest first, the narrowest last; *count of
 // them.
@@ -28,50 +51,45 @@ const RaggedTile* ragged_k_f32(int* count);
 const RaggedTile* ragged_lora_bf16(int* count);
 const RaggedTile* ragged_lora_f32(int* count);
 
-// T = s X op(down) (lora.hpp).  `tall`: blocks of 32 rows in place of 16.
-struct ShrinkCall {
-    const void* down;
-    int64_t ld_down, stride_down;
-    bool down_kc;
-    int k_slice, splits;
-    bool tall;
-    float* t;
-};
-hipError_t launch_shrink(const RaggedArgs& a, const ShrinkCall& c, bool bf16, hipStream_t s);
+// Streaming tiles of T = s_a X op(down_a) (stream.hpp), by the narrowest that
+// holds the rank and by descending height; *count of them.
+const RaggedTile* stream_shrink_bf16(int* count);
+const RaggedTile* stream_shrink_f32(int* count);
 
-template <auto KERNEL, int THREADS>
+// SPLIT: a.splits workgroups along the second axis (RAG_SHRINK).
+template <auto KERNEL, int THREADS, bool SPLIT = false>
 hipError_t launch_ragged(const RaggedArgs& a, int grid, hipStream_t s)
 {
     RaggedArgs copy = a;
     void* args[] = {&copy};
-    return hipLaunchKernel(reinterpret_cast<const void*>(KERNEL), dim3(grid), dim3(THREADS), args,
-                           0, s);
+    return hipLaunchKernel(reinterpret_cast<const void*>(KERNEL), dim3(grid, SPLIT ? a.splits : 1),
+                           dim3(THREADS), args, 0, s);
 }
 
 }  // namespace dg
 
-// RaggedTile entry of configuration CFG for launch kind RAG with A stored by
-// rows: both layouts of B, both output types (fp32 operands: fp32 only).
-#define DG_RAGGED_BF16(CFG, RAG)                                                             \
+// RaggedTile entry of configuration CFG for launch kind RAG, with its cost, A
+// stored by rows: both layouts of B, both output types (fp32 operands: fp32 only).
+#define DG_RAGGED_BF16(CFG, RAG, ...)                                                        \
     {CFG::BM, {CFG::BN, CFG::BN}, CFG::BK,                                                   \
      {{dg::launch_ragged<dg::dma_ragged_kernel<CFG, true, false, false, RAG>, CFG::THREADS>, \
        dg::launch_ragged<dg::dma_ragged_kernel<CFG, true, false, true, RAG>, CFG::THREADS>}, \
       {dg::launch_ragged<dg::dma_ragged_kernel<CFG, true, true, false, RAG>, CFG::THREADS>,  \
-       dg::launch_ragged<dg::dma_ragged_kernel<CFG, true, true, true, RAG>, CFG::THREADS>}}}
-#define DG_RAGGED_F32(CFG, RAG)                                                              \
+       dg::launch_ragged<dg::dma_ragged_kernel<CFG, true, true, true, RAG>, CFG::THREADS>}}, false, __VA_ARGS__}
+#define DG_RAGGED_F32(CFG, RAG, ...)                                                         \
     {CFG::BM, {CFG::BN, CFG::BN}, CFG::BK,                                                   \
      {{dg::launch_ragged<dg::dma_ragged_kernel<CFG, true, false, false, RAG>, CFG::THREADS>, \
        nullptr},                                                                             \
       {dg::launch_ragged<dg::dma_ragged_kernel<CFG, true, true, false, RAG>, CFG::THREADS>,  \
-       nullptr}}}
+       nullptr}}, false, __VA_ARGS__}
 // ... and for RAG_K (both operands stored by rows).
-#define DG_RAGGED_K_BF16(CFG)                                                                      \
+#define DG_RAGGED_K_BF16(CFG, ...)                                                                 \
     {CFG::BM, {CFG::BN, CFG::BN}, CFG::BK,                                                         \
      {{dg::launch_ragged<dg::dma_ragged_kernel<CFG, false, false, false, RAG_K>, CFG::THREADS>,    \
        dg::launch_ragged<dg::dma_ragged_kernel<CFG, false, false, true, RAG_K>, CFG::THREADS>},    \
-      {nullptr, nullptr}}}
-#define DG_RAGGED_K_F32(CFG)                                                                       \
+      {nullptr, nullptr}}, false, __VA_ARGS__}
+#define DG_RAGGED_K_F32(CFG, ...)                                                                  \
     {CFG::BM, {CFG::BN, CFG::BN}, CFG::BK,                                                         \
      {{dg::launch_ragged<dg::dma_ragged_kernel<CFG, false, false, false, RAG_K>, CFG::THREADS>,    \
        nullptr},                                                                                   \
-      {nullptr, nullptr}}}
+      {nullptr, nullptr}}, false, __VA_ARGS__}

@@ -6,22 +6,31 @@
 //  * one workgroup of eight waves per tile of 16*RF rows and 16*NF columns,
 //    the waves splitting K into eight runs, so even a call of a few tiles has
 //    every wave of a compute unit loading;
-//  * operands go from memory straight into the registers of the 16x16 MFMA
-//    layout, U fragment steps at a time in two batches (one loading while the
-//    other is multiplied); nothing is staged, so no barrier is met until the
-//    waves' sums are added;
-//  * a k-contiguous B gives each lane 16 consecutive bytes along k; an
-//    n-contiguous one NF consecutive columns of each of VEC rows of k, turned
-//    into fragments of every NF-th column by byte permutes (for fp32 they
-//    already are);
-//  * rows past the group's and the ragged last columns are not masked on the
-//    way in: the lane reads the group's last row again, and the last tile of
-//    a row starts at column N - BN instead, and what is read twice is not
-//    stored.  Only K's ragged end, and matrices smaller than a tile, take
-//    element-wise loads.
+//  * operands go from memory straight into registers, four fragment steps of
+//    K at a time and, where the registers hold them, two such batches in flight; nothing is staged, so no
+//    barrier is met until the waves' sums are added;
+//  * the memory pipeline looks up the lines of four consecutive lanes at a
+//    time, so a k-contiguous operand is not read in the MFMA's lane order (16
+//    rows side by side: a line per lane; 64 rows of a 4096x4096 product took
+//    24 us) but 64 bytes of one row per four lanes, 256 of each of four rows
+//    per load, and four loads are then transposed within each four lanes
+//    (quad_turn);
+//  * an n-contiguous B gives each lane NF consecutive columns of each of VEC
+//    rows of k, turned into fragments of every NF-th column by byte permutes
+//    (for fp32 they already are);
+//  * rows past the group's and columns past N are not masked on the way in:
+//    the lane reads the last row or column again (the last tile of an
+//    n-contiguous B starts at column N - BN instead), and what is read twice
+//    is not stored.  Only K's ragged end, and an n-contiguous B narrower than
+//    a tile and of no multiple of NF columns, take element-wise loads.
 //
 // The eight sums are added through LDS in wave order, so results are
 // reproducible, and rounded once.
+//
+// RAG_SHRINK forms the adapters' first product, T = s_a X op(down_a): the row
+// groups are the segments, B is their adapter's matrix and N its rank.
+// blockIdx.y takes a slice of K each, whose sums go to a part of T of their
+// own.
 #pragma once
 
 #include "lora.hpp"
@@ -29,27 +38,12 @@
 
 namespace dg {
 
-template <int BYTES>
-struct RawLoad;
-template <>
-struct RawLoad<4> {
-    typedef uint32_t T __attribute__((ext_vector_type(1), aligned(2)));
-};
-template <>
-struct RawLoad<8> {
-    typedef uint32_t T __attribute__((ext_vector_type(2), aligned(2)));
-};
-template <>
-struct RawLoad<16> {
-    typedef uint32_t T __attribute__((ext_vector_type(4), aligned(2)));
-};
-
-// RF x NF fragments of 16x16, U fragment steps of K per batch.
-template <typename T_, bool KC_, int RF_, int NF_, int U_>
+// RF x NF fragments of 16x16.
+template <typename T_, bool KC_, int RF_, int NF_>
 struct StreamConfig {
     using T = T_;
     static constexpr bool KC = KC_;
-    static constexpr int RF = RF_, NF = NF_, U = U_;
+    static constexpr int RF = RF_, NF = NF_;
     static constexpr int WAVES = 8, THREADS = 64 * WAVES;
     static constexpr int ES = sizeof(T), VEC = 16 / ES, KSTEP = 4 * VEC;
     static constexpr int BM = 16 * RF, BN = 16 * NF;
@@ -59,6 +53,8 @@ struct StreamConfig {
     static constexpr int SLOTS = PF * NF;               // 16x16 blocks per pass
     static constexpr int ITEMS = SLOTS * 64;            // 16-byte pieces of them
     static constexpr int IPT = (ITEMS + THREADS - 1) / THREADS;
+    // a second batch in flight where the registers hold it
+    static constexpr bool TWO = (RF + NF) * 36 - (KC ? 0 : 4 * NF) + 4 * RF * NF < 240;
     static_assert(RF % PF == 0 && NF <= 8, "exchange");
     static_assert(KC || NF * ES >= 4, "an n-contiguous row piece of at least 4 bytes");
     // Column within the tile of fragment j's column c.
@@ -71,139 +67,76 @@ struct StreamConfig {
     }
 };
 
-// One batch of operand registers.
+// Four fragment steps of operand registers.  Step j of lane group g = lane / 16
+// covers the VEC k from VEC * (4 g + j) of the batch's 4 KSTEP: any assignment
+// serves that is the same for both operands, and with this one the chunks of
+// four consecutive lanes are consecutive in memory.
 template <class S>
 struct StreamBatch {
-    u32x4 a[S::U][S::RF];
-    uint32_t b[S::U][S::NF * 4];
+    u32x4 a[S::RF][4];
+    u32x4 b[S::KC ? S::NF : 1][4];                       // k-contiguous B
+    uint32_t r[S::KC ? 1 : 4][S::KC ? 1 : S::NF * 4];    // rows of the other
 };
 
-// Fragment j of step u of a batch as the MFMA operand.
+// x[s] of lane 4 q + j to x[j] of lane 4 q + s, for every q: two rounds of
+// exchanges between register and lane numbers that differ in one bit.
+__device__ __forceinline__ void quad_turn(u32x4 (&x)[4], int lane)
+{
+    const bool odd = lane & 1, high = lane & 2;
+    auto swap = [](u32x4& lo, u32x4& hi, bool upper, auto perm) __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t l = lo[e], h = hi[e];
+            const uint32_t from_h = __builtin_amdgcn_mov_dpp(h, decltype(perm)::value, 0xf, 0xf, true);
+            const uint32_t from_l = __builtin_amdgcn_mov_dpp(l, decltype(perm)::value, 0xf, 0xf, true);
+            lo[e] = upper ? from_h : l;
+            hi[e] = upper ? h : from_l;
+        }
+    };
+    using X1 = std::integral_constant<int, 0xB1>;  // quad_perm 1, 0, 3, 2
+    using X2 = std::integral_constant<int, 0x4E>;  // quad_perm 2, 3, 0, 1
+    swap(x[0], x[1], odd, X1{});
+    swap(x[2], x[3], odd, X1{});
+    swap(x[0], x[2], high, X2{});
+    swap(x[1], x[3], high, X2{});
+}
+
+// Fragment j of the rows of k in r as the MFMA operand.
 template <class S>
-__device__ __forceinline__ u32x4 stream_b(const StreamBatch<S>& x, int u, int j)
+__device__ __forceinline__ u32x4 rows_fragment(const uint32_t (&x)[S::NF * 4], int j)
 {
     u32x4 r;
-    if constexpr (S::KC) {
+    if constexpr (S::ES == 4) {          // row k: words NF*k .. of the columns
 #pragma unroll
-        for (int q = 0; q < 4; ++q) r[q] = x.b[u][4 * j + q];
-    } else if constexpr (S::ES == 4) {   // row k: words NF*k .. of the columns
-#pragma unroll
-        for (int q = 0; q < 4; ++q) r[q] = x.b[u][S::NF * q + j];
+        for (int q = 0; q < 4; ++q) r[q] = x[S::NF * q + j];
     } else {                             // row k: words NF/2*k .., two columns each
         constexpr int W = S::NF / 2;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            r[q] = __builtin_amdgcn_perm(x.b[u][W * (2 * q + 1) + j / 2], x.b[u][W * (2 * q) + j / 2],
+            r[q] = __builtin_amdgcn_perm(x[W * (2 * q + 1) + j / 2], x[W * (2 * q) + j / 2],
                                          j % 2 ? 0x07060302u : 0x05040100u);
     }
     return r;
-}
-
-// VEC consecutive k of one row (or column) with every index clamped into
-// [0, K) and zero past K.  `x` points at the row; ks: elements between k.
-template <typename T>
-__device__ __forceinline__ u32x4 clamped_chunk(const T* x, int64_t ks, int k, int K)
-{
-    constexpr int VEC = 16 / sizeof(T);
-    T e[VEC];
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) e[v] = x[(int64_t)(k + v < K ? k + v : K - 1) * ks];
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) e[v] = k + v < K ? e[v] : T(0);
-    return pack_chunk<T>(e);
-}
-
-// t[0..8) . up[0..8) of four adjacent columns from `col`, added to sum: ranks
-// r .. r+7 of adapter `up` (clamped to the matrix; ranks past the last add
-// nothing).
-template <typename T>
-__device__ __forceinline__ void lora_dot8(const RaggedArgs& p, const T* up, int col, int r,
-                                          const float (&t)[8], f32x4& sum)
-{
-    T u[4][8];
-    const bool whole = r + 8 <= p.rank;
-    if (p.up_kc) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const T* row = up + (int64_t)(col + s < p.N ? col + s : p.N - 1) * p.ld_up;
-            if (whole) {
-#pragma unroll
-                for (int h = 0; h < (int)sizeof(T) / 2; ++h) {
-                    constexpr int VEC = 16 / sizeof(T);
-                    const u32x4 c = *reinterpret_cast<const u32x4_elem<T>*>(row + r + h * VEC);
-                    T e[VEC];
-                    __builtin_memcpy(e, &c, 16);
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) u[s][h * VEC + v] = e[v];
-                }
-            } else {
-#pragma unroll
-                for (int v = 0; v < 8; ++v) u[s][v] = row[r + v < p.rank ? r + v : p.rank - 1];
-            }
-        }
-    } else {
-#pragma unroll
-        for (int v = 0; v < 8; ++v) {
-            const T* row = up + (int64_t)(r + v < p.rank ? r + v : p.rank - 1) * p.ld_up;
-            if (col + 4 <= p.N) {
-                const typename RawLoad<4 * sizeof(T)>::T c =
-                    *reinterpret_cast<const typename RawLoad<4 * sizeof(T)>::T*>(row + col);
-                T e[4];
-                __builtin_memcpy(e, &c, 4 * sizeof(T));
-#pragma unroll
-                for (int s = 0; s < 4; ++s) u[s][v] = e[s];
-            } else {
-#pragma unroll
-                for (int s = 0; s < 4; ++s) u[s][v] = row[col + s < p.N ? col + s : p.N - 1];
-            }
-        }
-    }
-#pragma unroll
-    for (int v = 0; v < 8; ++v)
-        if (r + v < p.rank)
-#pragma unroll
-            for (int s = 0; s < 4; ++s) sum[s] += t[v] * to_f32(u[s][v]);
-}
-
-// T op(up_a) of row `row`, four columns from `col`, in fp32 (T is not
-// rounded on this path).
-template <typename T>
-__device__ __forceinline__ f32x4 lora_row(const RaggedArgs& p, int row, int col, int a)
-{
-    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-    const T* up = static_cast<const T*>(p.up) + (int64_t)a * p.stride_up;
-    const float* src = p.t + (int64_t)row * p.rank_pad;
-    for (int r = 0; r < p.rank; r += 8) {
-        float t[8] = {};
-        for (int sp = 0; sp < p.splits; ++sp) {
-            const f32x4* q =
-                reinterpret_cast<const f32x4*>(src + (int64_t)sp * p.rows * p.rank_pad + r);
-            const f32x4 q0 = q[0], q1 = q[1];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                t[e] += q0[e];
-                t[4 + e] += q1[e];
-            }
-        }
-        lora_dot8<T>(p, up, col, r, t, sum);
-    }
-    return sum;
 }
 
 template <class S, typename OutT, int RAG>
 __global__ __launch_bounds__(S::THREADS) void stream_kernel(RaggedArgs p)
 {
     using T = typename S::T;
-    constexpr int RF = S::RF, NF = S::NF, U = S::U, KSTEP = S::KSTEP, VEC = S::VEC, ES = S::ES;
+    constexpr int RF = S::RF, NF = S::NF, KSTEP = S::KSTEP, VEC = S::VEC, ES = S::ES;
     __shared__ f32x4 part[S::WAVES][S::SLOTS][64];
     __shared__ int adapter[RAG == RAG_LORA ? S::BM : 1];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int tm, tn, start = 0, size = p.M, g = 0;
-    if constexpr (RAG == RAG_ROWS) {
+    if constexpr (RAG == RAG_ROWS || RAG == RAG_SHRINK) {
         RowTile t;
         if (!find_row_tile<S::BM>(p, blockIdx.x, p.tiles_n, t)) return;
         g = t.group;
+        if constexpr (RAG == RAG_SHRINK) {
+            if (p.ids) g = __builtin_amdgcn_readfirstlane(p.ids[g]);
+            if (g < 0 || g >= p.adapters) return;
+        }
         start = t.start;
         size = t.size;
         p.tiles_m = t.tiles_m;
@@ -213,94 +146,175 @@ __global__ __launch_bounds__(S::THREADS) void stream_kernel(RaggedArgs p)
         tile_coords(p, tm, tn);
     }
     const int r0 = tm * S::BM, n0 = tn * S::BN;  // r0 within the group
-    // the last tile of a row moves back to end at column N
-    const int nb = n0 + S::BN <= p.N ? n0 : (p.N >= S::BN ? p.N - S::BN : 0);
+    // with an n-contiguous B the last tile of a row moves back to end at
+    // column N
+    const int nb = S::KC || n0 + S::BN <= p.N ? n0 : (p.N >= S::BN ? p.N - S::BN : 0);
     const T* A = static_cast<const T*>(p.A) + (int64_t)(start + r0) * p.lda;
     const T* B = static_cast<const T*>(p.B) + (int64_t)g * p.stride_b +
                  (S::KC ? (int64_t)nb * p.ldb : nb);
+    if constexpr (RAG == RAG_SHRINK) {
+        const int k_lo = blockIdx.y * p.k_slice;
+        A += k_lo;
+        B += S::KC ? (int64_t)k_lo : (int64_t)k_lo * p.ldb;
+        p.K = p.K - k_lo < p.k_slice ? p.K - k_lo : p.k_slice;
+        p.D += (int64_t)blockIdx.y * p.rows * p.rank_pad;
+    }
     const int rows = size - r0;  // of the group, from the tile's first
 
     f32x4 acc[RF][NF] = {};
-    auto multiply = [&](const StreamBatch<S>& x, int u) __attribute__((always_inline)) {
-#pragma unroll
-        for (int j = 0; j < NF; ++j) {
-            const u32x4 b = stream_b<S>(x, u, j);
-#pragma unroll
-            for (int i = 0; i < RF; ++i) mfma16<T>(x.a[u][i], b, acc[i][j]);
-        }
-    };
-    auto arow = [&](int i) { const int r = i * 16 + lane % 16; return r < rows ? r : rows - 1; };
-    // whole fragment steps of K, split evenly over the waves
-    const bool narrow = p.N < S::BN;
-    const int steps = narrow ? 0 : p.K / KSTEP;
-    uint32_t off_a[RF], off_b[S::KC ? NF : 1];
+    // the row (of A, or of a k-contiguous B) and chunk of 16 bytes that load t of
+    // a batch takes within a fragment of 16 rows
+    const int q_row = 4 * ((lane >> 2) & 3), q_chunk = 4 * (lane >> 4) + (lane & 3);
+    auto last = [](int r, int n) { return r < n ? r : n - 1; };
+    uint32_t off_a[RF][4], off_b[S::KC ? NF : 1][4];
 #pragma unroll
     for (int i = 0; i < RF; ++i)
-        off_a[i] = (uint32_t)(((int64_t)arow(i) * p.lda + VEC * (lane / 16)) * ES);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            off_a[i][t] = (uint32_t)(((int64_t)last(i * 16 + q_row + t, rows) * p.lda + VEC * q_chunk) * ES);
     if constexpr (S::KC) {
 #pragma unroll
         for (int j = 0; j < NF; ++j)
-            off_b[j] = (uint32_t)(((int64_t)(j * 16 + lane % 16) * p.ldb + VEC * (lane / 16)) * ES);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                off_b[j][t] = (uint32_t)(((int64_t)last(j * 16 + q_row + t, p.N - nb) * p.ldb +
+                                          VEC * q_chunk) * ES);
     } else {
-        off_b[0] = (uint32_t)(((int64_t)VEC * (lane / 16) * p.ldb + NF * (lane % 16)) * ES);
+        const int c = NF * (lane % 16);
+        off_b[0][0] = (uint32_t)(((int64_t)4 * VEC * (lane / 16) * p.ldb +
+                                  (nb + c < p.N ? c : p.N - NF - nb)) * ES);
     }
-    auto load = [&](StreamBatch<S>& x, int u, int step) __attribute__((always_inline)) {
-        const int k = step * KSTEP;
-        const char* a = reinterpret_cast<const char*>(A + k);
-#pragma unroll
-        for (int i = 0; i < RF; ++i)
-            x.a[u][i] = *reinterpret_cast<const u32x4_elem<T>*>(a + off_a[i]);
-        if constexpr (S::KC) {
-            const char* b = reinterpret_cast<const char*>(B + k);
-#pragma unroll
-            for (int j = 0; j < NF; ++j) {
-                const u32x4 v = *reinterpret_cast<const u32x4_elem<T>*>(b + off_b[j]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) x.b[u][4 * j + q] = v[q];
-            }
-        } else {
+    // VEC rows of an n-contiguous B, from the one at `row`
+    auto load_rows = [&](uint32_t (&x)[S::KC ? 1 : NF * 4], const T* row, uint32_t off)
+                         __attribute__((always_inline)) {
+        if constexpr (!S::KC) {
             constexpr int W = NF * ES / 4, PW = W > 4 ? 4 : W;  // words per row of k, per load
             using V = typename RawLoad<4 * PW>::T;
 #pragma unroll
             for (int r = 0; r < VEC; ++r) {
-                const char* b = reinterpret_cast<const char*>(B + (int64_t)(k + r) * p.ldb);
+                const char* b = reinterpret_cast<const char*>(row + (int64_t)r * p.ldb);
 #pragma unroll
                 for (int h = 0; h < W / PW; ++h) {
-                    const V v = *reinterpret_cast<const V*>(b + off_b[0] + h * 16);
+                    const V v = *reinterpret_cast<const V*>(b + off + h * 16);
 #pragma unroll
-                    for (int q = 0; q < PW; ++q) x.b[u][W * r + PW * h + q] = v[q];
+                    for (int q = 0; q < PW; ++q) x[W * r + PW * h + q] = v[q];
                 }
             }
         }
     };
-    const int s_lo = (int)((int64_t)steps * wave / S::WAVES);
-    const int s_hi = (int)((int64_t)steps * (wave + 1) / S::WAVES);
-    const int batches = (s_hi - s_lo) / U, rest = (s_hi - s_lo) % U;
-    StreamBatch<S> x0, x1;
-    // the steps that fill no batch first, with the first batch behind them
-    int s = s_lo + rest;
-    static_for<U - 1>([&](auto u) __attribute__((always_inline)) {
-        if (decltype(u)::value < rest) load(x1, decltype(u)::value, s_lo + decltype(u)::value);
-    });
-    if (batches > 0)
-        static_for<U>([&](auto u) __attribute__((always_inline)) {
-            load(x0, decltype(u)::value, s + decltype(u)::value);
-        });
+    auto load = [&](StreamBatch<S>& x, int batch) __attribute__((always_inline)) {
+        const int k = batch * 4 * KSTEP;
+        const char* a = reinterpret_cast<const char*>(A + k);
+        const char* b = reinterpret_cast<const char*>(B + k);
+#pragma unroll
+        for (int i = 0; i < RF; ++i)
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                x.a[i][t] = *reinterpret_cast<const u32x4_elem<T>*>(a + off_a[i][t]);
+        if constexpr (S::KC) {
+#pragma unroll
+            for (int j = 0; j < NF; ++j)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    x.b[j][t] = *reinterpret_cast<const u32x4_elem<T>*>(b + off_b[j][t]);
+        } else {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                load_rows(x.r[t], B + (int64_t)(k + VEC * t) * p.ldb, off_b[0][0]);
+        }
+    };
+    auto multiply = [&](StreamBatch<S>& x) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < RF; ++i) quad_turn(x.a[i], lane);
+        if constexpr (S::KC)
+#pragma unroll
+            for (int j = 0; j < NF; ++j) quad_turn(x.b[j], lane);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int j = 0; j < NF; ++j) {
+                u32x4 b;
+                if constexpr (S::KC) b = x.b[j][t];
+                else b = rows_fragment<S>(x.r[t], j);
+#pragma unroll
+                for (int i = 0; i < RF; ++i) mfma16<T>(x.a[i][t], b, acc[i][j]);
+            }
+    };
+    // whole batches of K, split evenly over the waves
+    const bool narrow = !S::KC && p.N < S::BN && p.N % NF != 0;
+    const int steps = narrow ? 0 : p.K / KSTEP, batches = steps / 4;
+    const int b_lo = (int)((int64_t)batches * wave / S::WAVES);
+    const int b_hi = (int)((int64_t)batches * (wave + 1) / S::WAVES);
+    // Loads stand in no branch inside the loop: the compiler would have to wait
+    // for all of them wherever such a branch ends.
+    StreamBatch<S> x0;
+    if (b_lo < b_hi) load(x0, b_lo);
+    if constexpr (RAG == RAG_LORA) map_adapters<S::BM, S::THREADS>(p, r0, tid, adapter);
+    if (b_lo < b_hi) {
+        int b = b_lo;
+        if constexpr (S::TWO) {
+            StreamBatch<S> x1;
+            for (; b + 2 < b_hi; b += 2) {
+                load(x1, b + 1);
+                multiply(x0);
+                load(x0, b + 2);
+                multiply(x1);
+            }
+            if (b + 1 < b_hi) {
+                load(x1, b + 1);
+                multiply(x0);
+                multiply(x1);
+            } else {
+                multiply(x0);
+            }
+        } else {
+            for (; b + 1 < b_hi; ++b) {
+                multiply(x0);
+                __builtin_amdgcn_sched_barrier(0);
+                load(x0, b + 1);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            multiply(x0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    // the steps that fill no batch, K's ragged end, and every step of a narrow
+    // matrix: one fragment step at a time, in the MFMA's lane order
+    const int all = (p.K + KSTEP - 1) / KSTEP;
+    for (int t = 4 * batches + (S::WAVES - 1 - wave); t < all; t += S::WAVES) {
+        const int k = t * KSTEP + VEC * (lane / 16);
+        const bool whole = t < steps;
+        u32x4 fa[RF];
+        uint32_t br[S::KC ? 1 : NF * 4];
+        if constexpr (!S::KC)
+            if (whole)
+                load_rows(br, B + (int64_t)t * KSTEP * p.ldb,
+                          off_b[0][0] - (uint32_t)((int64_t)3 * VEC * (lane / 16) * p.ldb * ES));
+#pragma unroll
+        for (int i = 0; i < RF; ++i) {
+            const T* row = A + (int64_t)last(i * 16 + lane % 16, rows) * p.lda;
+            fa[i] = whole ? *reinterpret_cast<const u32x4_elem<T>*>(row + k)
+                          : clamped_chunk<T>(row, 1, k, p.K);
+        }
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+            const int c = last(S::column(j, lane % 16), p.N - nb);
+            u32x4 fb;
+            if constexpr (S::KC) {
+                const T* row = B + (int64_t)c * p.ldb;
+                fb = whole ? *reinterpret_cast<const u32x4_elem<T>*>(row + k)
+                           : clamped_chunk<T>(row, 1, k, p.K);
+            } else {
+                fb = whole ? rows_fragment<S>(br, j) : clamped_chunk<T>(B + c, p.ldb, k, p.K);
+            }
+#pragma unroll
+            for (int i = 0; i < RF; ++i) mfma16<T>(fa[i], fb, acc[i][j]);
+        }
+    }
 
-    // the low-rank part of this thread's outputs, while the batches load
+    // the low-rank part of this thread's outputs
     f32x4 low[RAG == RAG_LORA ? S::PASSES * S::IPT : 1];
     if constexpr (RAG == RAG_LORA) {
-        for (int r = tid; r < S::BM; r += S::THREADS) adapter[r] = -1;
-        __syncthreads();
-        for (int sg = tid; sg < p.groups; sg += S::THREADS) {
-            int lo, n;
-            group_span(p, sg, lo, n);
-            const int hi = lo + n < r0 + S::BM ? lo + n : r0 + S::BM;
-            const int a = p.ids ? p.ids[sg] : sg;
-            if (a >= 0 && a < p.adapters)
-                for (int r = lo > r0 ? lo : r0; r < hi; ++r) adapter[r - r0] = a;
-        }
-        __syncthreads();
 #pragma unroll
         for (int q = 0; q < S::PASSES * S::IPT; ++q) {
             const int item = tid + (q % S::IPT) * S::THREADS, slot = item / 64, l = item & 63;
@@ -308,46 +322,7 @@ __global__ __launch_bounds__(S::THREADS) void stream_kernel(RaggedArgs p)
             const int col = nb + S::slot_column(slot % NF, l);
             low[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             if (item < S::ITEMS && row < rows && col < p.N && adapter[row] >= 0)
-                low[q] = lora_row<T>(p, r0 + row, col, adapter[row]);
-        }
-    }
-
-    static_for<U - 1>([&](auto u) __attribute__((always_inline)) {
-        if (decltype(u)::value < rest) multiply(x1, decltype(u)::value);
-    });
-    auto turn = [&](StreamBatch<S>& next, const StreamBatch<S>& cur, bool more)
-                    __attribute__((always_inline)) {
-        s += U;
-        if (more)
-            static_for<U>([&](auto u) __attribute__((always_inline)) {
-                load(next, decltype(u)::value, s + decltype(u)::value);
-            });
-        static_for<U>([&](auto u) __attribute__((always_inline)) {
-            multiply(cur, decltype(u)::value);
-        });
-    };
-    int b = 0;
-    for (; b + 2 <= batches; b += 2) {
-        turn(x1, x0, true);
-        turn(x0, x1, b + 2 < batches);
-    }
-    if (b < batches) turn(x1, x0, false);
-    // K's ragged end, and every step of a matrix narrower than the tile
-    const int all = (p.K + KSTEP - 1) / KSTEP;
-    for (int t = steps + (S::WAVES - 1 - wave); t < all; t += S::WAVES) {
-        const int k = t * KSTEP + VEC * (lane / 16);
-        u32x4 fa[RF];
-#pragma unroll
-        for (int i = 0; i < RF; ++i)
-            fa[i] = clamped_chunk<T>(A + (int64_t)arow(i) * p.lda, 1, k, p.K);
-#pragma unroll
-        for (int j = 0; j < NF; ++j) {
-            int c = S::column(j, lane % 16);
-            if (nb + c >= p.N) c = p.N - 1 - nb;
-            const u32x4 fb = clamped_chunk<T>(B + (S::KC ? (int64_t)c * p.ldb : c),
-                                              S::KC ? 1 : p.ldb, k, p.K);
-#pragma unroll
-            for (int i = 0; i < RF; ++i) mfma16<T>(fa[i], fb, acc[i][j]);
+                low[q] = lora_row<T>(p, r0 + row, col, adapter[row], nb + S::BN <= p.N);
         }
     }
 
@@ -371,7 +346,7 @@ __global__ __launch_bounds__(S::THREADS) void stream_kernel(RaggedArgs p)
             if (item >= S::ITEMS) break;
             const int row = (pass * S::PF + slot / NF) * 16 + l % 16;
             const int col = nb + S::slot_column(slot % NF, l);
-            if (row >= rows || col >= p.N) continue;
+            if (row >= rows || col >= (RAG == RAG_SHRINK ? p.rank_pad : p.N)) continue;
             f32x4 v = part[0][slot][l];
 #pragma unroll
             for (int w = 1; w < S::WAVES; ++w) v += part[w][slot][l];
@@ -380,6 +355,14 @@ __global__ __launch_bounds__(S::THREADS) void stream_kernel(RaggedArgs p)
             const int64_t at = start + r0 + row;
             OutT* d = reinterpret_cast<OutT*>(p.D) + at * p.ldd + col;
             const OutT* c = reinterpret_cast<const OutT*>(p.C) + at * p.ldc + col;
+            if constexpr (RAG == RAG_SHRINK) {  // columns past the rank are zero
+#pragma unroll
+                for (int s4 = 0; s4 < 4; ++s4) v[s4] = col + s4 < p.N ? v[s4] : 0.0f;
+                *reinterpret_cast<f32x4*>(d) = v;
+                if constexpr (ES == 2)
+                    if (p.t_terms) store_terms(p, at, col, v);
+                continue;
+            }
             if (col >= n0 && col + 4 <= p.N) {
                 if (p.beta != 0.0f) {
                     OutT e[4];
