@@ -435,44 +435,74 @@ def bind_tensors(h, A, B, D, C=None, transA="N", transB="N", alpha=1.0, beta=0.0
     return lambda: fn(*args)
 
 
-def _ld(t, dims=2):
-    """Leading dimension of a tensor whose last axis is contiguous."""
-    if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError(f"expected a {dims}-D tensor with unit stride in its last axis")
+# The ragged calls are made per token by a decoding loop, where the kernels take
+# a few microseconds, so their marshalling asks torch for each property once.
+def _matrix(t):
+    """Rows, columns and leading dimension of a 2-D tensor with unit stride in
+    its last axis."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
+        raise ValueError("expected a 2-D tensor with unit stride in its last axis")
+    rows, cols = shape
     # a single row has no stride of its own; too small a stride (an expanded
     # tensor) is refused by the library
-    return t.stride(-2) if t.shape[-2] > 1 else max(t.shape[-1], 1)
+    return rows, cols, stride[0] if rows > 1 else max(cols, 1)
+
+
+def _matrices(t):
+    """Count, rows, columns, leading dimension and stride between the matrices of
+    a 3-D tensor with unit stride in its last axis."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or (stride[2] != 1 and shape[2] > 1):
+        raise ValueError("expected a 3-D tensor with unit stride in its last axis")
+    count, rows, cols = shape
+    return count, rows, cols, stride[1] if rows > 1 else max(cols, 1), stride[0]
 
 
 def _ragged_dtype(A, B, D, C):
     """gemm_dtype_t of a ragged product's tensors."""
     import torch
 
-    if A.dtype == torch.float32 and B.dtype == torch.float32:
-        dtype, outs = GEMM_DTYPE_F32, (torch.float32,)
-    elif A.dtype == torch.bfloat16 and B.dtype == torch.bfloat16:
-        dtype = GEMM_DTYPE_BF16_BF16 if D.dtype == torch.bfloat16 else GEMM_DTYPE_BF16_F32
-        outs = (torch.float32, torch.bfloat16)
-    else:
-        raise TypeError("A and B must both be float32 or both bfloat16")
-    if D.dtype not in outs or (C is not None and C.dtype != D.dtype):
-        raise TypeError("C and D must be float32, or both bfloat16 with bfloat16 operands")
-    return dtype
+    ta, td = A.dtype, D.dtype
+    if ta is not B.dtype or (C is not None and C.dtype is not td):
+        raise TypeError("A and B, and C and D, must have one dtype each")
+    if ta is torch.bfloat16:
+        if td is torch.bfloat16:
+            return GEMM_DTYPE_BF16_BF16
+        if td is torch.float32:
+            return GEMM_DTYPE_BF16_F32
+    elif ta is torch.float32 and td is torch.float32:
+        return GEMM_DTYPE_F32
+    raise TypeError("A and B must be float32, or bfloat16 with float32 or bfloat16 C and D")
 
 
 def _device_vector(t, dtype, length, device, what):
-    """Data pointer of a contiguous 1-D device tensor (None stays None)."""
+    """Data pointer of a contiguous 1-D tensor on device index `device` (None
+    stays None)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != length or t.device != device or (
-            length > 1 and t.stride(0) != 1):
-        raise ValueError(f"{what} must be a contiguous length-{length} {dtype} tensor on {device}")
+    shape = t.shape
+    if len(shape) != 1 or shape[0] != length or t.dtype is not dtype or (
+            t.get_device() != device) or (length > 1 and t.stride()[0] != 1):
+        raise ValueError(f"{what} must be a contiguous length-{length} {dtype} tensor on D's device")
     return t.data_ptr()
 
 
-def _same_device(D, *tensors):
-    if any(t is not None and t.device != D.device for t in tensors):
-        raise ValueError("every tensor must be on D's device")
+def _device_of(D, *tensors):
+    """D's device index (-1 for the host), which every tensor has to share."""
+    device = D.get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError("every tensor must be on D's device")
+    return device
+
+
+def _stream_on(device):
+    """The current stream of a device, as an integer."""
+    import torch
+
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without a Stream object
+    return raw(device) if raw else torch.cuda.current_stream(device).cuda_stream
 
 
 def _finish(status, check, what):
@@ -494,21 +524,26 @@ def run_grouped(h, A, B, D, offsets, C=None, transB="N", scales=None, alpha=1.0,
     import torch
 
     dtype = _ragged_dtype(A, B, D, C)
-    lda, ldb, ldd = _ld(A), _ld(B, 3), _ld(D)
-    M, K = A.shape
-    groups = B.shape[0]
-    Kb, N = (B.shape[1], B.shape[2]) if transB == "N" else (B.shape[2], B.shape[1])
-    if Kb != K or tuple(D.shape) != (M, N) or (C is not None and tuple(C.shape) != (M, N)):
+    M, K, lda = _matrix(A)
+    groups, Kb, N, ldb, stride_b = _matrices(B)
+    if transB != "N":
+        Kb, N = N, Kb
+    Md, Nd, ldd = _matrix(D)
+    c, ldc = None, N
+    if C is not None:
+        c = C.data_ptr()
+        Mc, Nc, ldc = _matrix(C)
+        if Mc != M or Nc != N:
+            raise ValueError("inconsistent grouped GEMM shapes")
+    if Kb != K or Md != M or Nd != N:
         raise ValueError("inconsistent grouped GEMM shapes")
-    _same_device(D, A, B, C)
-    gr = GemmGroups(groups, _device_vector(offsets, torch.int32, groups + 1, D.device, "offsets"),
-                    _device_vector(scales, torch.float32, groups, D.device, "scales"))
-    if stream is None:
-        stream = torch.cuda.current_stream(D.device).cuda_stream
+    device = _device_of(D, A, B, C)
+    gr = GemmGroups(groups, _device_vector(offsets, torch.int32, groups + 1, device, "offsets"),
+                    _device_vector(scales, torch.float32, groups, device, "scales"))
     s = lib.gemm_run_grouped(
-        h, GEMM_OP_N if transB == "N" else GEMM_OP_T, M, N, K, float(alpha), A.data_ptr(), lda,
-        B.data_ptr(), ldb, B.stride(0), float(beta), None if C is None else C.data_ptr(),
-        N if C is None else _ld(C), D.data_ptr(), ldd, dtype, ctypes.byref(gr), stream)
+        h, GEMM_OP_N if transB == "N" else GEMM_OP_T, M, N, K, alpha, A.data_ptr(), lda,
+        B.data_ptr(), ldb, stride_b, beta, c, ldc, D.data_ptr(), ldd, dtype, ctypes.byref(gr),
+        _stream_on(device) if stream is None else stream)
     return _finish(s, check, "gemm_run_grouped")
 
 
@@ -524,22 +559,24 @@ def run_grouped_wgrad(h, A, B, D, offsets, C=None, scales=None, alpha=1.0, beta=
     import torch
 
     dtype = _ragged_dtype(A, B, D, C)
-    lda, ldb, ldd = _ld(A), _ld(B), _ld(D, 3)
-    rows, M = A.shape
-    groups, N = D.shape[0], B.shape[1]
-    if B.shape[0] != rows or tuple(D.shape) != (groups, M, N) or (
-            C is not None and C.shape != D.shape):
+    rows, M, lda = _matrix(A)
+    rows_b, N, ldb = _matrix(B)
+    groups, Md, Nd, ldd, stride_d = _matrices(D)
+    c, ldc, stride_c = None, N, 0
+    if C is not None:
+        if C.shape != D.shape:
+            raise ValueError("inconsistent grouped GEMM shapes")
+        c = C.data_ptr()
+        _, _, _, ldc, stride_c = _matrices(C)
+    if rows_b != rows or Md != M or Nd != N:
         raise ValueError("inconsistent grouped GEMM shapes")
-    _same_device(D, A, B, C)
-    gr = GemmGroups(groups, _device_vector(offsets, torch.int32, groups + 1, D.device, "offsets"),
-                    _device_vector(scales, torch.float32, groups, D.device, "scales"))
-    if stream is None:
-        stream = torch.cuda.current_stream(D.device).cuda_stream
+    device = _device_of(D, A, B, C)
+    gr = GemmGroups(groups, _device_vector(offsets, torch.int32, groups + 1, device, "offsets"),
+                    _device_vector(scales, torch.float32, groups, device, "scales"))
     s = lib.gemm_run_grouped_wgrad(
-        h, M, N, rows, float(alpha), A.data_ptr(), lda, B.data_ptr(), ldb, float(beta),
-        None if C is None else C.data_ptr(), N if C is None else _ld(C, 3),
-        0 if C is None else C.stride(0), D.data_ptr(), ldd, D.stride(0), dtype, ctypes.byref(gr),
-        stream)
+        h, M, N, rows, alpha, A.data_ptr(), lda, B.data_ptr(), ldb, beta, c, ldc, stride_c,
+        D.data_ptr(), ldd, stride_d, dtype, ctypes.byref(gr),
+        _stream_on(device) if stream is None else stream)
     return _finish(s, check, "gemm_run_grouped_wgrad")
 
 
@@ -569,33 +606,40 @@ def run_lora(h, A, B, D, offsets, down, up, workspace, ids=None, scales=None, C=
     import torch
 
     dtype = _ragged_dtype(A, B, D, C)
-    if down.dtype != A.dtype or up.dtype != A.dtype:
+    if down.dtype is not A.dtype or up.dtype is not A.dtype:
         raise TypeError("down and up must have A's dtype")
-    lda, ldb, ldd = _ld(A), _ld(B), _ld(D)
-    M, K = A.shape
-    Kb, N = (B.shape[0], B.shape[1]) if transB == "N" else (B.shape[1], B.shape[0])
-    ld_down, ld_up = _ld(down, 3), _ld(up, 3)
-    adapters, R = down.shape[0], down.shape[1] if transDown == "T" else down.shape[2]
-    if Kb != K or tuple(D.shape) != (M, N) or (C is not None and tuple(C.shape) != (M, N)) or (
-            tuple(down.shape) != ((adapters, R, K) if transDown == "T" else (adapters, K, R))) or (
-            tuple(up.shape) != ((adapters, N, R) if transUp == "T" else (adapters, R, N))):
+    M, K, lda = _matrix(A)
+    Kb, N, ldb = _matrix(B)
+    if transB != "N":
+        Kb, N = N, Kb
+    Md, Nd, ldd = _matrix(D)
+    adapters, R, Kd, ld_down, stride_down = _matrices(down)
+    if transDown == "N":
+        R, Kd = Kd, R
+    adapters_up, Nu, Ru, ld_up, stride_up = _matrices(up)
+    if transUp == "N":
+        Nu, Ru = Ru, Nu
+    c, ldc = None, N
+    if C is not None:
+        c = C.data_ptr()
+        Mc, Nc, ldc = _matrix(C)
+        if Mc != M or Nc != N:
+            raise ValueError("inconsistent low-rank adapter shapes")
+    if Kb != K or Md != M or Nd != N or Kd != K or adapters_up != adapters or Nu != N or Ru != R:
         raise ValueError("inconsistent low-rank adapter shapes")
-    _same_device(D, A, B, C, down, up, workspace)
+    device = _device_of(D, A, B, C, down, up, workspace)
     if offsets.dim() != 1 or offsets.shape[0] < 1:
         raise ValueError("offsets must hold segments + 1 entries")
     segments = offsets.shape[0] - 1
     lo = GemmLora(segments,
-                  _device_vector(offsets, torch.int32, segments + 1, D.device, "offsets"),
-                  _device_vector(ids, torch.int32, segments, D.device, "ids"), adapters, R,
-                  _device_vector(scales, torch.float32, adapters, D.device, "scales"),
+                  _device_vector(offsets, torch.int32, segments + 1, device, "offsets"),
+                  _device_vector(ids, torch.int32, segments, device, "ids"), adapters, R,
+                  _device_vector(scales, torch.float32, adapters, device, "scales"),
                   GEMM_OP_N if transDown == "N" else GEMM_OP_T, down.data_ptr(), ld_down,
-                  down.stride(0), GEMM_OP_N if transUp == "N" else GEMM_OP_T, up.data_ptr(), ld_up,
-                  up.stride(0))
-    if stream is None:
-        stream = torch.cuda.current_stream(D.device).cuda_stream
+                  stride_down, GEMM_OP_N if transUp == "N" else GEMM_OP_T, up.data_ptr(), ld_up,
+                  stride_up)
     s = lib.gemm_run_lora(
-        h, GEMM_OP_N if transB == "N" else GEMM_OP_T, M, N, K, float(alpha), A.data_ptr(), lda,
-        B.data_ptr(), ldb, float(beta), None if C is None else C.data_ptr(),
-        N if C is None else _ld(C), D.data_ptr(), ldd, dtype, ctypes.byref(lo),
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream)
+        h, GEMM_OP_N if transB == "N" else GEMM_OP_T, M, N, K, alpha, A.data_ptr(), lda,
+        B.data_ptr(), ldb, beta, c, ldc, D.data_ptr(), ldd, dtype, ctypes.byref(lo),
+        workspace.data_ptr(), workspace.nbytes, _stream_on(device) if stream is None else stream)
     return _finish(s, check, "gemm_run_lora")

@@ -747,7 +747,13 @@ __device__ __forceinline__ void dma_gemm_body(Args p)
     // chunk that straddles the end of the matrix would lose its last valid
     // bf16 element to the word-granular range check.  A ragged last step needs
     // exact zeros past K and is always register-staged.
-    const int nk_dma = ALIGNED ? ((last && (k_ragged || edge)) ? nk - 1 : nk) : 0;
+    // (The ragged calls, whose groups end inside tiles, look closer: only an
+    // odd bf16 extent leaves a chunk with half a word at its end, and RAG_K's
+    // rows past its K lie past the range of both operands, so a ragged K reads
+    // as zero too.)
+    const bool odd_end = Cfg::ES == 2 && edge && ((!A_KC && (p.M & 1)) || (!B_KC && (p.N & 1)));
+    const bool guard_last = RAG == RAG_NONE ? k_ragged || edge : (k_ragged && !REBASE) || odd_end;
+    const int nk_dma = ALIGNED ? ((last && guard_last) ? nk - 1 : nk) : 0;
 
     // step kt of the staged operands into a stage array
     auto load = [&](int kt, char* base) __attribute__((always_inline)) {

@@ -255,7 +255,11 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_handle_t h, int64_t M, int64_t N, int6
     a.tiles_m = (int)ceil_div(M, t.bm);
     a.tiles_n = (int)ceil_div(N, bn);
     a.group_m = std::min(a.tiles_m, 4);
-    const int64_t grid = G * a.tiles_m * a.tiles_n;
+    const int64_t per = (int64_t)a.tiles_m * a.tiles_n;
+    a.deal = !a.d_lines && rows < 128 * G ? DEAL_RANGES
+             : per < 2 * DEAL_XCDS        ? DEAL_TILES
+                                          : DEAL_SLICES;
+    const int64_t grid = deal_grid(a.deal, per, G);
     if (grid > INT_MAX) return GEMM_ERR_NOT_SUPPORTED;
     if (h->fail_launch) return GEMM_ERR_HIP;
     if (t.fn[0][dtype == GEMM_DTYPE_BF16_BF16](a, (int)grid, stream) != hipSuccess)
