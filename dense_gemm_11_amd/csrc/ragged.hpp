@@ -72,11 +72,25 @@ struct RowTile {
     int group, start, size, tiles_m, in_group;
 };
 
+// Number of the tile that workgroup w takes: workgroups go round the 8 XCDs, and
+// each XCD takes blocks of 32 consecutive numbers, a tile per compute unit, in
+// turn (of the last, smaller round an eighth).  So an XCD's concurrent tiles
+// share panels in its L2, and the XCDs' blocks share them in the cache behind:
+// with a range of all tiles each, eight experts' matrices stream from memory at
+// once.
+__device__ __forceinline__ int block_cyclic(int w, int tiles)
+{
+    constexpr int XCDS = 8, BLOCK = 32, ROUND = XCDS * BLOCK;
+    const int base = tiles / ROUND * ROUND;
+    const int block = w < base ? BLOCK : (tiles - base) / XCDS;
+    const int first = w < base ? w / ROUND * ROUND : base;
+    const int r = w - first;
+    return r < XCDS * block ? first + r % XCDS * block + r / XCDS : w;
+}
+
 // The tile of workgroup `w`, or false when there are fewer tiles.  Tiles are
-// numbered group after group, tiles_m * tiles_n of them each, and workgroups
-// of one XCD take a contiguous range of the numbers, so a group's weights are
-// read into one or two of the eight L2s.  Every lane of the wave takes part;
-// the result is the same in each.
+// numbered group after group, tiles_m * tiles_n of them each.  Every lane of
+// the wave takes part; the result is the same in each.
 template <int BM>
 __device__ __forceinline__ bool find_row_tile(const RaggedArgs& p, int w, int tiles_n, RowTile& t)
 {
@@ -95,9 +109,7 @@ __device__ __forceinline__ bool find_row_tile(const RaggedArgs& p, int w, int ti
     }
     const int tiles = total * tiles_n;
     if (w >= tiles) return false;
-    constexpr int XCDS = 8;
-    const int full = (tiles / XCDS) * XCDS;
-    if (w < full) w = (w % XCDS) * (full / XCDS) + (w / XCDS);
+    w = block_cyclic(w, tiles);
     const int q = w / tiles_n;  // tile-row number over all groups
     int base = 0;
     for (int g0 = 0;;) {
