@@ -9,8 +9,8 @@ namespace dg {
 const RaggedTile* ragged_rows_f32(int* count)
 {
     static const RaggedTile tiles[] = {
-        DG_RAGGED_F32(SelF32Mid, RAG_ROWS, {7.8f, 60.6f, 4.9f, 61.1f}),
-        DG_RAGGED_F32(RagF32Low, RAG_ROWS, {6.2f, 31.5f, 2.5f, 31.8f})};
+        DG_RAGGED_F32(SelF32Mid, RAG_ROWS, {8.1f, 58.65f, 4.4f, 57.93f}),
+        DG_RAGGED_F32(RagF32Low, RAG_ROWS, {5.7f, 30.59f, 2.2f, 31.59f})};
     *count = (int)(sizeof(tiles) / sizeof(tiles[0]));
     return tiles;
 }
@@ -18,8 +18,8 @@ const RaggedTile* ragged_rows_f32(int* count)
 const RaggedTile* ragged_lora_f32(int* count)
 {
     static const RaggedTile tiles[] = {
-        DG_RAGGED_F32(SelF32Mid, RAG_LORA, {5.0f, 37.4f, 21.3f, 62.6f}),
-        DG_RAGGED_F32(RagF32Low, RAG_LORA, {17.2f, 37.3f, 15.5f, 26.6f})};
+        DG_RAGGED_F32(SelF32Mid, RAG_LORA, {5.1f, 55.86f, 15.8f, 76.47f}),
+        DG_RAGGED_F32(RagF32Low, RAG_LORA, {17.2f, 36.79f, 6.0f, 47.04f})};
     *count = (int)(sizeof(tiles) / sizeof(tiles[0]));
     return tiles;
 }

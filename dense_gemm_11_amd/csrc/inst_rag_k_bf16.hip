@@ -8,11 +8,11 @@ namespace dg {
 const RaggedTile* ragged_k_bf16(int* count)
 {
     static const RaggedTile tiles[] = {
-        DG_RAGGED_K_BF16(SelBf16Big, {18.2f, 13.7f, 24.6f, 26.5f}),
-        DG_RAGGED_K_BF16(Dma192x256s3L, {21.9f, 22.2f, 17.2f, 23.3f}),
-        DG_RAGGED_K_BF16(Dma128x256s3L, {8.1f, 12.4f, 18.7f, 19.7f}),
-        DG_RAGGED_K_BF16(SelBf16Mid, {15.9f, 11.3f, 5.8f, 12.5f}),
-        DG_RAGGED_K_BF16(RagBf16Thin, {15.9f, 20.7f, 4.6f, 14.7f})};
+        DG_RAGGED_K_BF16(SelBf16Big, {8.0f, 3.40f, 22.1f, 26.08f}),
+        DG_RAGGED_K_BF16(Dma192x256s3L, {8.0f, 2.68f, 18.0f, 20.54f}),
+        DG_RAGGED_K_BF16(Dma128x256s3L, {19.7f, 16.58f, 11.2f, 14.69f}),
+        DG_RAGGED_K_BF16(SelBf16Mid, {11.4f, 10.71f, 4.9f, 9.67f}),
+        DG_RAGGED_K_BF16(RagBf16Thin, {10.8f, 22.55f, 3.8f, 9.47f})};
     *count = (int)(sizeof(tiles) / sizeof(tiles[0]));
     return tiles;
 }

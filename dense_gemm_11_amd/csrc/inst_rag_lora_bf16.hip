@@ -8,10 +8,10 @@ namespace dg {
 const RaggedTile* ragged_lora_bf16(int* count)
 {
     static const RaggedTile tiles[] = {
-        DG_RAGGED_BF16(SelBf16Big, RAG_LORA, {27.8f, 21.5f, 20.6f, 26.9f}),
-        DG_RAGGED_BF16(Dma192x256s3L, RAG_LORA, {25.2f, 15.5f, 17.4f, 21.3f}),
-        DG_RAGGED_BF16(RagBf16Mid, RAG_LORA, {20.0f, 8.9f, 6.0f, 10.8f}),
-        DG_RAGGED_BF16(RagBf16Low, RAG_LORA, {18.1f, 7.1f, 4.7f, 6.5f})};
+        DG_RAGGED_BF16(SelBf16Big, RAG_LORA, {8.0f, 22.84f, 20.8f, 22.75f}),
+        DG_RAGGED_BF16(Dma192x256s3L, RAG_LORA, {8.0f, 17.66f, 19.5f, 17.31f}),
+        DG_RAGGED_BF16(RagBf16Mid, RAG_LORA, {15.4f, 7.11f, 8.7f, 9.87f}),
+        DG_RAGGED_BF16(RagBf16Low, RAG_LORA, {14.0f, 6.08f, 6.6f, 6.41f})};
     *count = (int)(sizeof(tiles) / sizeof(tiles[0]));
     return tiles;
 }

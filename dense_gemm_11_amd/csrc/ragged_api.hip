@@ -58,9 +58,10 @@ TileList tile_list(TileTable dma, TileTable stream)
 }
 
 // The tallest tile up to the forced height, else the one of least expected
-// time; tiles(t) is the number of output tiles of t a call has, or expects.
+// time; tiles(t) is the number of output tiles of t a call has, or expects, and
+// `bytes` what it reads and writes at the least.
 template <class F>
-const RaggedTile& pick_tile(const TileList& t, int forced, int64_t K, F tiles)
+const RaggedTile& pick_tile(const TileList& t, int forced, bool b_kc, int64_t K, double bytes, F tiles)
 {
     int best = t.n - 1;
     if (forced > 0) {
@@ -70,7 +71,7 @@ const RaggedTile& pick_tile(const TileList& t, int forced, int64_t K, F tiles)
     }
     double best_us = 0.0;
     for (int i = 0; i < t.n; ++i) {
-        const double us = expected_us(t[i], tiles(t[i]), (double)K, device_cus());
+        const double us = expected_us(t[i], b_kc, tiles(t[i]), (double)K, bytes, device_cus());
         if (i == 0 || us < best_us) {
             best = i;
             best_us = us;
@@ -160,9 +161,10 @@ gemm_status_t gemm_run_grouped(gemm_handle_t h, gemm_op_t transB, int64_t M, int
     a.stride_b = strideB;
     // a group holds M / groups rows on average, and the host knows no more
     const int64_t busy = std::min<int64_t>(groups->groups, M);
+    const double bytes = (double)es * K * ((double)busy * N + M) + (double)eo * M * N;
     const TileList tiles = dtype == GEMM_DTYPE_F32 ? tile_list(ragged_rows_f32, stream_rows_f32)
                                                    : tile_list(ragged_rows_bf16, stream_rows_bf16);
-    const RaggedTile& t = pick_tile(tiles, h->forced_rows, K, [&](const RaggedTile& x) {
+    const RaggedTile& t = pick_tile(tiles, h->forced_rows, b_kc, K, bytes, [&](const RaggedTile& x) {
         return ceil_div(N, x.bn[b_kc]) *
                (busy > 1 ? row_tiles((double)busy, (double)M / busy, x.bm) : (double)ceil_div(M, x.bm));
     });
@@ -245,7 +247,7 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_handle_t h, int64_t M, int64_t N, int6
     a.stride_d = strideD;
     const TileList tiles =
         tile_list(dtype == GEMM_DTYPE_F32 ? ragged_k_f32 : ragged_k_bf16, nullptr);
-    const RaggedTile& t = pick_tile(tiles, h->forced_rows, rows / G, [&](const RaggedTile& x) {
+    const RaggedTile& t = pick_tile(tiles, h->forced_rows, false, rows / G, 0.0, [&](const RaggedTile& x) {
         return (double)(G * ceil_div(M, x.bm) * ceil_div(N, x.bn[0]));
     });
     const int bn = t.bn[0];
@@ -352,9 +354,10 @@ gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_
     a.ld_up = lora->ld_up;
     a.stride_up = lora->stride_up;
     a.up_kc = up_kc;
+    const double bytes = (double)es * K * (N + M) + (double)eo * M * N;
     const TileList tiles = dtype == GEMM_DTYPE_F32 ? tile_list(ragged_lora_f32, stream_lora_f32)
                                                    : tile_list(ragged_lora_bf16, stream_lora_bf16);
-    const RaggedTile& t = pick_tile(tiles, h->forced_rows, K, [&](const RaggedTile& x) {
+    const RaggedTile& t = pick_tile(tiles, h->forced_rows, b_kc, K, bytes, [&](const RaggedTile& x) {
         return (double)(ceil_div(M, x.bm) * ceil_div(N, x.bn[b_kc]));
     });
     const int bn = t.bn[b_kc];

@@ -22,18 +22,27 @@ struct RaggedTile {
 };
 
 // Expected time of `tiles` tiles of t.  The costs are least-squares fits of
-// this form to timings of every tile on random calls of each kind (70 to 140
+// this form to timings of every tile on random calls of each kind (80 to 170
 // of bf16 operands, 30 to 60 of fp32: 1 to 16384 rows, 1 to 128 groups, K 128
-// to 8192, N 8 to 14336); taking the tile of least expected time runs within 1
-// to 6 % of the best tile on average.
-inline double expected_us(const RaggedTile& t, double tiles, double K, int cus)
+// to 8192, N 8 to 14336).  The tile of least expected time was the fastest of
+// them in half of the calls, within 10 % of it in four fifths.  No tile is
+// expected to beat the time of the call's `bytes` at 5.2 TB/s, which tiles
+// narrower than 64 columns miss by 15 % (64 experts of 4096x1792, 384 rows:
+// 0.196 ms against 0.167 where B is n-contiguous, 0.178 against 0.163 where it
+// is not); among tiles held to it the one with the least to do is taken.
+inline double expected_us(const RaggedTile& t, bool b_kc, double tiles, double K, double bytes, int cus)
 {
     const double n = tiles > cus ? tiles / cus : 1.0, k = K / 1000.0;
     const double alone = t.cost.alone + k * t.cost.alone_k;
-    // workgroups that have a unit to themselves come in whole rounds
-    const double rounds = t.bm * t.bn[0] >= 192 * 256 ? (double)(int64_t)(n + 0.9) : n;
+    // tiles that have a unit to themselves come in whole rounds, the others
+    // leave a part of one
+    const double rounds = t.stream || t.bm * t.bn[0] >= 192 * 256 ? (double)(int64_t)(n + 0.9)
+                          : n > 1.0                               ? n + 0.4
+                                                                  : 1.0;
     const double full = rounds * (t.cost.each + k * t.cost.each_k);
-    return alone > full ? alone : full;
+    const double us = alone > full ? alone : full;
+    const double floor_us = bytes / 5.2e6 * (t.bn[b_kc] < 64 ? 1.15 : 1.0);
+    return (us > floor_us ? us : floor_us) + 0.01 * us;
 }
 
 // Streaming tiles (stream.hpp), tallest first, the narrowest last; *count of

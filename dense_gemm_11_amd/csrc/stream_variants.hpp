@@ -39,11 +39,26 @@ const RaggedTile* stream_tiles(int* count)
     // costs of bf16 and fp32 operands, without and with adapters
     constexpr int X = (sizeof(T) == 4 ? 1 : 0) + (RAG == RAG_LORA ? 2 : 0);
     constexpr TileCost cost[5][4] = {
-        {{5.5f, 1.4f, 3.3f, 2.9f}, {5.9f, 7.9f, 3.8f, 7.6f}, {11.9f, 3.0f, 5.8f, 3.6f}, {11.6f, 8.7f, 8.0f, 8.1f}},
-        {{6.1f, 1.7f, 4.2f, 3.5f}, {11.1f, 0.0f, 4.7f, 12.0f}, {12.9f, 3.6f, 8.2f, 4.4f}, {13.6f, 13.6f, 11.0f, 13.1f}},
-        {{4.4f, 2.0f, 2.8f, 2.1f}, {4.7f, 4.1f, 1.8f, 4.5f}, {10.5f, 2.4f, 5.8f, 2.1f}, {11.7f, 4.9f, 2.9f, 3.9f}},
-        {{5.5f, 2.5f, 4.0f, 3.0f}, {5.6f, 6.5f, 3.5f, 7.5f}, {11.1f, 3.3f, 7.1f, 3.0f}, {11.9f, 8.9f, 6.5f, 7.7f}},
-        {{5.4f, 1.2f, 2.0f, 1.6f}, {4.9f, 3.5f, 1.2f, 2.5f}, {11.4f, 1.5f, 2.3f, 1.5f}, {12.8f, 2.9f, 2.0f, 2.2f}}};
+        {{4.9f, 2.01f, 3.7f, 2.06f},
+         {5.8f, 6.69f, 3.6f, 7.30f},
+         {10.4f, 2.80f, 5.8f, 3.31f},
+         {9.7f, 9.04f, 8.0f, 8.59f}},
+        {{5.5f, 0.68f, 4.3f, 2.48f},
+         {8.6f, 3.26f, 4.1f, 12.44f},
+         {11.2f, 3.24f, 6.0f, 3.82f},
+         {15.7f, 6.93f, 9.5f, 14.13f}},
+        {{4.3f, 1.31f, 3.2f, 1.10f},
+         {4.5f, 3.75f, 2.0f, 3.57f},
+         {10.1f, 1.81f, 5.2f, 2.13f},
+         {10.1f, 5.32f, 3.3f, 4.14f}},
+        {{4.6f, 2.16f, 3.6f, 2.34f},
+         {5.4f, 6.27f, 3.6f, 6.77f},
+         {10.5f, 2.52f, 5.1f, 2.90f},
+         {11.1f, 7.66f, 7.3f, 7.54f}},
+        {{4.1f, 1.24f, 2.3f, 0.80f},
+         {4.4f, 2.07f, 1.5f, 1.93f},
+         {10.7f, 1.08f, 1.9f, 1.46f},
+         {9.5f, 4.17f, 2.4f, 2.16f}}};
     static constexpr RaggedTile tiles[] = {
         stream_tile<T, RAG, 4, 1, N1>(cost[0][X]), stream_tile<T, RAG, 2, 4, 4>(cost[1][X]),
         stream_tile<T, RAG, 2, 1, N1>(cost[2][X]), stream_tile<T, RAG, 1, 4, 4>(cost[3][X]),
