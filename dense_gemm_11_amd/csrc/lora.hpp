@@ -25,6 +25,9 @@ namespace dg {
 // T is padded to whole fragments of rank along k: LORA_PAD columns.
 constexpr int LORA_PAD = 16;
 
+// Ranks that RAG_LORA_ONE (stream.hpp) takes at most.
+constexpr int LORA_ONE_RANK = 32;
+
 // VEC consecutive k of one row (or column) with every index clamped into
 // [0, K) and zero past K.  `x` points at the row; ks: elements between k.
 template <typename T>
@@ -161,17 +164,17 @@ __device__ __forceinline__ void load_t(const RaggedArgs& p, int row, int k, f32x
     }
 }
 
-// T op(up_a) of row `row`, four columns from `col` (`inside`: of a tile that
-// lies inside the matrix, the same for every lane), in fp32 (T is not rounded
-// on this path), eight ranks at a time.
-template <typename T>
-__device__ __forceinline__ f32x4 lora_row(const RaggedArgs& p, int row, int col, int a, bool inside)
+// A row's T op(up_a), four columns from `col` (`inside`: of a tile that lies
+// inside the matrix, the same for every lane), in fp32 (T is not rounded on
+// this path), eight ranks at a time: get_t(r, t) gives ranks r .. r + 7.
+template <typename T, class F>
+__device__ __forceinline__ f32x4 lora_row(const RaggedArgs& p, int col, int a, bool inside, F get_t)
 {
     f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
     const T* up = static_cast<const T*>(p.up) + (int64_t)a * p.stride_up;
     for (int r = 0; r < p.rank; r += 8) {
         f32x4 t[2];
-        load_t(p, row, r, t);
+        get_t(r, t);
         T u[4][8];
         if (inside && p.up_kc && r + 8 <= p.rank) {
 #pragma unroll

@@ -19,8 +19,9 @@ namespace dg {
 //  RAG_LORA: D = alpha (A op(B) + T op(up_a)) + beta C, T the rows' products
 //            with their segment's adapter, already scaled (lora.hpp);
 //  RAG_SHRINK: those products, T[rows of s] = s_a A[rows of s] op(down_a)
-//            (stream.hpp).
-enum : int { RAG_NONE = 0, RAG_ROWS = 1, RAG_K = 2, RAG_LORA = 3, RAG_SHRINK = 4 };
+//            (stream.hpp);
+//  RAG_LORA_ONE: RAG_LORA and RAG_SHRINK in one launch, for one tile of rows.
+enum : int { RAG_NONE = 0, RAG_ROWS = 1, RAG_K = 2, RAG_LORA = 3, RAG_SHRINK = 4, RAG_LORA_ONE = 5 };
 
 struct RaggedArgs : GemmArgs {
     const int32_t* offsets;  // groups + 1
@@ -39,6 +40,8 @@ struct RaggedArgs : GemmArgs {
     const float* t;
     const void* up;
     int64_t ld_up, stride_up;
+    const void* down;        // RAG_LORA_ONE: rank x K
+    int64_t ld_down, stride_down;
     int up_kc;               // up stored N x rank (rank contiguous)
     int k_slice;             // RAG_SHRINK: K of each of the `splits` slices
     uint16_t* t_terms;       // bf16 operands: T as two terms (lora.hpp), or null

@@ -370,6 +370,24 @@ gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_
     a.group_m = std::min(a.tiles_m, 4);
     const int64_t grid = (int64_t)a.tiles_m * a.tiles_n;
     if (grid > INT_MAX) return GEMM_ERR_NOT_SUPPORTED;
+    // one tile of rows and little to do for T: both products in one launch
+    const int64_t segs = std::min<int64_t>(lora->segments, M);
+    if (t.stream && t.bm == 16 && M <= 16 && down_kc && R <= LORA_ONE_RANK &&
+        segs * ceil_div(R, 16) <= 2 && panel_fits(15, lora->ld_down, kk, es)) {
+        int n_one = 0;
+        const RaggedTile* one_launch =
+            (dtype == GEMM_DTYPE_F32 ? stream_lora_one_f32 : stream_lora_one_bf16)(&n_one);
+        const RaggedTile& ot = one_launch[t.bn[b_kc] < 64 ? 1 : 0];
+        a.down = lora->down;
+        a.ld_down = lora->ld_down;
+        a.stride_down = lora->stride_down;
+        if (h->fail_launch) return GEMM_ERR_HIP;
+        if (ot.fn[b_kc][dtype == GEMM_DTYPE_BF16_BF16](a, (int)grid, stream) != hipSuccess)
+            return GEMM_ERR_HIP;
+        h->last_rows = ot.bm;
+        log_call(h, "lora in one launch", a, ot.bm, bn, grid);
+        return GEMM_OK;
+    }
     // the first product: blocks of as many rows as a segment has on average,
     // as narrow as the rank allows, and slices of K until there is a
     // workgroup per compute unit or a slice is two batches per wave
@@ -384,7 +402,7 @@ gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_
     f.alpha = 1.0f;
     f.beta = 0.0f;
     f.group_m = 4;
-    const int64_t segs = std::min<int64_t>(lora->segments, M), avg = ceil_div(M, segs);
+    const int64_t avg = ceil_div(M, segs);
     int n_first = 0;
     const RaggedTile* first = (dtype == GEMM_DTYPE_F32 ? stream_shrink_f32 : stream_shrink_bf16)(&n_first);
     int fi = 0;

@@ -51,6 +51,9 @@ const RaggedTile* stream_rows_bf16(int* count);
 const RaggedTile* stream_rows_f32(int* count);
 const RaggedTile* stream_lora_bf16(int* count);
 const RaggedTile* stream_lora_f32(int* count);
+// RAG_LORA_ONE: 16 rows, the wide tile first
+const RaggedTile* stream_lora_one_bf16(int* count);
+const RaggedTile* stream_lora_one_f32(int* count);
 
 // Direct-to-LDS tiles, tallest first; *count of them.
 const RaggedTile* ragged_rows_bf16(int* count);

@@ -30,7 +30,10 @@
 // RAG_SHRINK forms the adapters' first product, T = s_a X op(down_a): the row
 // groups are the segments, B is their adapter's matrix and N its rank.
 // blockIdx.y takes a slice of K each, whose sums go to a part of T of their
-// own.
+// own.  RAG_LORA_ONE is RAG_LORA that forms its rows' T itself: every
+// workgroup reads the adapters' down again (from L2), which for one tile of
+// rows and one or two adapters costs less than a launch and T's way through
+// memory (one token, 2048x2048, rank 8: 12.6 -> 10.31 us).
 #pragma once
 
 #include "lora.hpp"
@@ -119,13 +122,176 @@ __device__ __forceinline__ u32x4 rows_fragment(const uint32_t (&x)[S::NF * 4], i
     return r;
 }
 
+// This wave's part of a tile's product, added to acc: `rows` rows of A (at least
+// one) and `cols` columns of B, from the tile's first, by all of K.  meanwhile()
+// runs once, while the first loads are under way.
+template <class S, class F>
+__device__ __forceinline__ void stream_product(const typename S::T* A, int64_t lda, int rows,
+                                               const typename S::T* B, int64_t ldb, int cols, int K,
+                                               int wave, int lane, f32x4 (&acc)[S::RF][S::NF],
+                                               F meanwhile)
+{
+    using T = typename S::T;
+    constexpr int RF = S::RF, NF = S::NF, KSTEP = S::KSTEP, VEC = S::VEC, ES = S::ES;
+    // the row (of A, or of a k-contiguous B) and chunk of 16 bytes that load t of
+    // a batch takes within a fragment of 16 rows
+    const int q_row = 4 * ((lane >> 2) & 3), q_chunk = 4 * (lane >> 4) + (lane & 3);
+    auto last = [](int r, int n) { return r < n ? r : n - 1; };
+    uint32_t off_a[RF][4], off_b[S::KC ? NF : 1][4];
+#pragma unroll
+    for (int i = 0; i < RF; ++i)
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            off_a[i][t] = (uint32_t)(((int64_t)last(i * 16 + q_row + t, rows) * lda + VEC * q_chunk) * ES);
+    if constexpr (S::KC) {
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                off_b[j][t] = (uint32_t)(((int64_t)last(j * 16 + q_row + t, cols) * ldb +
+                                          VEC * q_chunk) * ES);
+    } else {
+        const int c = NF * (lane % 16);
+        off_b[0][0] = (uint32_t)(((int64_t)4 * VEC * (lane / 16) * ldb +
+                                  (c < cols ? c : cols - NF)) * ES);
+    }
+    // VEC rows of an n-contiguous B, from the one at `row`
+    auto load_rows = [&](uint32_t (&x)[S::KC ? 1 : NF * 4], const T* row, uint32_t off)
+                         __attribute__((always_inline)) {
+        if constexpr (!S::KC) {
+            constexpr int W = NF * ES / 4, PW = W > 4 ? 4 : W;  // words per row of k, per load
+            using V = typename RawLoad<4 * PW>::T;
+#pragma unroll
+            for (int r = 0; r < VEC; ++r) {
+                const char* b = reinterpret_cast<const char*>(row + (int64_t)r * ldb);
+#pragma unroll
+                for (int h = 0; h < W / PW; ++h) {
+                    const V v = *reinterpret_cast<const V*>(b + off + h * 16);
+#pragma unroll
+                    for (int q = 0; q < PW; ++q) x[W * r + PW * h + q] = v[q];
+                }
+            }
+        }
+    };
+    auto load = [&](StreamBatch<S>& x, int batch) __attribute__((always_inline)) {
+        const int k = batch * 4 * KSTEP;
+        const char* a = reinterpret_cast<const char*>(A + k);
+        const char* b = reinterpret_cast<const char*>(B + k);
+#pragma unroll
+        for (int i = 0; i < RF; ++i)
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                x.a[i][t] = *reinterpret_cast<const u32x4_elem<T>*>(a + off_a[i][t]);
+        if constexpr (S::KC) {
+#pragma unroll
+            for (int j = 0; j < NF; ++j)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    x.b[j][t] = *reinterpret_cast<const u32x4_elem<T>*>(b + off_b[j][t]);
+        } else {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                load_rows(x.r[t], B + (int64_t)(k + VEC * t) * ldb, off_b[0][0]);
+        }
+    };
+    auto multiply = [&](StreamBatch<S>& x) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < RF; ++i) quad_turn(x.a[i], lane);
+        if constexpr (S::KC)
+#pragma unroll
+            for (int j = 0; j < NF; ++j) quad_turn(x.b[j], lane);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int j = 0; j < NF; ++j) {
+                u32x4 b;
+                if constexpr (S::KC) b = x.b[j][t];
+                else b = rows_fragment<S>(x.r[t], j);
+#pragma unroll
+                for (int i = 0; i < RF; ++i) mfma16<T>(x.a[i][t], b, acc[i][j]);
+            }
+    };
+    // whole batches of K, split evenly over the waves
+    const bool narrow = !S::KC && cols < S::BN && cols % NF != 0;
+    const int steps = narrow ? 0 : K / KSTEP, batches = steps / 4;
+    const int b_lo = (int)((int64_t)batches * wave / S::WAVES);
+    const int b_hi = (int)((int64_t)batches * (wave + 1) / S::WAVES);
+    // Loads stand in no branch inside the loop: the compiler would have to wait
+    // for all of them wherever such a branch ends.
+    StreamBatch<S> x0;
+    if (b_lo < b_hi) load(x0, b_lo);
+    meanwhile();
+    if (b_lo < b_hi) {
+        int b = b_lo;
+        if constexpr (S::TWO) {
+            StreamBatch<S> x1;
+            for (; b + 2 < b_hi; b += 2) {
+                load(x1, b + 1);
+                multiply(x0);
+                load(x0, b + 2);
+                multiply(x1);
+            }
+            if (b + 1 < b_hi) {
+                load(x1, b + 1);
+                multiply(x0);
+                multiply(x1);
+            } else {
+                multiply(x0);
+            }
+        } else {
+            for (; b + 1 < b_hi; ++b) {
+                multiply(x0);
+                __builtin_amdgcn_sched_barrier(0);
+                load(x0, b + 1);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            multiply(x0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    // the steps that fill no batch, K's ragged end, and every step of a narrow
+    // matrix: one fragment step at a time, in the MFMA's lane order
+    const int all = (K + KSTEP - 1) / KSTEP;
+    for (int t = 4 * batches + (S::WAVES - 1 - wave); t < all; t += S::WAVES) {
+        const int k = t * KSTEP + VEC * (lane / 16);
+        const bool whole = t < steps;
+        u32x4 fa[RF];
+        uint32_t br[S::KC ? 1 : NF * 4];
+        if constexpr (!S::KC)
+            if (whole)
+                load_rows(br, B + (int64_t)t * KSTEP * ldb,
+                          off_b[0][0] - (uint32_t)((int64_t)3 * VEC * (lane / 16) * ldb * ES));
+#pragma unroll
+        for (int i = 0; i < RF; ++i) {
+            const T* row = A + (int64_t)last(i * 16 + lane % 16, rows) * lda;
+            fa[i] = whole ? *reinterpret_cast<const u32x4_elem<T>*>(row + k)
+                          : clamped_chunk<T>(row, 1, k, K);
+        }
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+            const int c = last(S::column(j, lane % 16), cols);
+            u32x4 fb;
+            if constexpr (S::KC) {
+                const T* row = B + (int64_t)c * ldb;
+                fb = whole ? *reinterpret_cast<const u32x4_elem<T>*>(row + k)
+                           : clamped_chunk<T>(row, 1, k, K);
+            } else {
+                fb = whole ? rows_fragment<S>(br, j) : clamped_chunk<T>(B + c, ldb, k, K);
+            }
+#pragma unroll
+            for (int i = 0; i < RF; ++i) mfma16<T>(fa[i], fb, acc[i][j]);
+        }
+    }
+}
+
 template <class S, typename OutT, int RAG>
 __global__ __launch_bounds__(S::THREADS) void stream_kernel(RaggedArgs p)
 {
     using T = typename S::T;
-    constexpr int RF = S::RF, NF = S::NF, KSTEP = S::KSTEP, VEC = S::VEC, ES = S::ES;
+    constexpr int RF = S::RF, NF = S::NF, ES = S::ES;
     __shared__ f32x4 part[S::WAVES][S::SLOTS][64];
-    __shared__ int adapter[RAG == RAG_LORA ? S::BM : 1];
+    constexpr bool LORA = RAG == RAG_LORA || RAG == RAG_LORA_ONE;
+    __shared__ int adapter[LORA ? S::BM : 1];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int tm, tn, start = 0, size = p.M, g = 0;
@@ -162,159 +328,45 @@ __global__ __launch_bounds__(S::THREADS) void stream_kernel(RaggedArgs p)
     const int rows = size - r0;  // of the group, from the tile's first
 
     f32x4 acc[RF][NF] = {};
-    // the row (of A, or of a k-contiguous B) and chunk of 16 bytes that load t of
-    // a batch takes within a fragment of 16 rows
-    const int q_row = 4 * ((lane >> 2) & 3), q_chunk = 4 * (lane >> 4) + (lane & 3);
-    auto last = [](int r, int n) { return r < n ? r : n - 1; };
-    uint32_t off_a[RF][4], off_b[S::KC ? NF : 1][4];
+    stream_product<S>(A, p.lda, rows, B, p.ldb, p.N - nb, p.K, wave, lane, acc, [&] {
+        if constexpr (LORA) map_adapters<S::BM, S::THREADS>(p, r0, tid, adapter);
+    });
+
+    // RAG_LORA_ONE: T here instead of in a launch of its own, an adapter and 16
+    // ranks at a time
+    __shared__ __attribute__((aligned(16))) float t_row[RAG == RAG_LORA_ONE ? S::BM : 1][LORA_ONE_RANK];
+    if constexpr (RAG == RAG_LORA_ONE) {
+        using D = StreamConfig<T, true, 1, 1>;
+        static_assert(RF == 1, "a fragment of rows");
+        const int mine = lane % 16 < rows ? adapter[lane % 16] : -1;
+        for (uint64_t left = __ballot(mine >= 0); left != 0;) {
+            const int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
+            left &= ~__ballot(mine == a);
+            const T* down = static_cast<const T*>(p.down) + (int64_t)a * p.stride_down;
+            for (int c0 = 0; c0 < p.rank; c0 += 16) {
+                f32x4 t[1][1] = {};
+                stream_product<D>(A, p.lda, rows, down + (int64_t)c0 * p.ld_down, p.ld_down,
+                                  p.rank - c0, p.K, wave, lane, t, [] {});
+                part[wave][0][lane] = t[0][0];
+                __syncthreads();
+                if (wave == 0 && mine == a) {
+                    f32x4 v = part[0][0][lane];
 #pragma unroll
-    for (int i = 0; i < RF; ++i)
+                    for (int w = 1; w < S::WAVES; ++w) v += part[w][0][lane];
+                    v *= p.scales ? p.scales[a] : 1.0f;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-            off_a[i][t] = (uint32_t)(((int64_t)last(i * 16 + q_row + t, rows) * p.lda + VEC * q_chunk) * ES);
-    if constexpr (S::KC) {
-#pragma unroll
-        for (int j = 0; j < NF; ++j)
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-                off_b[j][t] = (uint32_t)(((int64_t)last(j * 16 + q_row + t, p.N - nb) * p.ldb +
-                                          VEC * q_chunk) * ES);
-    } else {
-        const int c = NF * (lane % 16);
-        off_b[0][0] = (uint32_t)(((int64_t)4 * VEC * (lane / 16) * p.ldb +
-                                  (nb + c < p.N ? c : p.N - NF - nb)) * ES);
-    }
-    // VEC rows of an n-contiguous B, from the one at `row`
-    auto load_rows = [&](uint32_t (&x)[S::KC ? 1 : NF * 4], const T* row, uint32_t off)
-                         __attribute__((always_inline)) {
-        if constexpr (!S::KC) {
-            constexpr int W = NF * ES / 4, PW = W > 4 ? 4 : W;  // words per row of k, per load
-            using V = typename RawLoad<4 * PW>::T;
-#pragma unroll
-            for (int r = 0; r < VEC; ++r) {
-                const char* b = reinterpret_cast<const char*>(row + (int64_t)r * p.ldb);
-#pragma unroll
-                for (int h = 0; h < W / PW; ++h) {
-                    const V v = *reinterpret_cast<const V*>(b + off + h * 16);
-#pragma unroll
-                    for (int q = 0; q < PW; ++q) x[W * r + PW * h + q] = v[q];
+                    for (int e = 0; e < 4; ++e)
+                        t_row[lane % 16][c0 + 4 * (lane / 16) + e] =
+                            c0 + 4 * (lane / 16) + e < p.rank ? v[e] : 0.0f;
                 }
+                __syncthreads();
             }
-        }
-    };
-    auto load = [&](StreamBatch<S>& x, int batch) __attribute__((always_inline)) {
-        const int k = batch * 4 * KSTEP;
-        const char* a = reinterpret_cast<const char*>(A + k);
-        const char* b = reinterpret_cast<const char*>(B + k);
-#pragma unroll
-        for (int i = 0; i < RF; ++i)
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-                x.a[i][t] = *reinterpret_cast<const u32x4_elem<T>*>(a + off_a[i][t]);
-        if constexpr (S::KC) {
-#pragma unroll
-            for (int j = 0; j < NF; ++j)
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    x.b[j][t] = *reinterpret_cast<const u32x4_elem<T>*>(b + off_b[j][t]);
-        } else {
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-                load_rows(x.r[t], B + (int64_t)(k + VEC * t) * p.ldb, off_b[0][0]);
-        }
-    };
-    auto multiply = [&](StreamBatch<S>& x) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < RF; ++i) quad_turn(x.a[i], lane);
-        if constexpr (S::KC)
-#pragma unroll
-            for (int j = 0; j < NF; ++j) quad_turn(x.b[j], lane);
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int j = 0; j < NF; ++j) {
-                u32x4 b;
-                if constexpr (S::KC) b = x.b[j][t];
-                else b = rows_fragment<S>(x.r[t], j);
-#pragma unroll
-                for (int i = 0; i < RF; ++i) mfma16<T>(x.a[i][t], b, acc[i][j]);
-            }
-    };
-    // whole batches of K, split evenly over the waves
-    const bool narrow = !S::KC && p.N < S::BN && p.N % NF != 0;
-    const int steps = narrow ? 0 : p.K / KSTEP, batches = steps / 4;
-    const int b_lo = (int)((int64_t)batches * wave / S::WAVES);
-    const int b_hi = (int)((int64_t)batches * (wave + 1) / S::WAVES);
-    // Loads stand in no branch inside the loop: the compiler would have to wait
-    // for all of them wherever such a branch ends.
-    StreamBatch<S> x0;
-    if (b_lo < b_hi) load(x0, b_lo);
-    if constexpr (RAG == RAG_LORA) map_adapters<S::BM, S::THREADS>(p, r0, tid, adapter);
-    if (b_lo < b_hi) {
-        int b = b_lo;
-        if constexpr (S::TWO) {
-            StreamBatch<S> x1;
-            for (; b + 2 < b_hi; b += 2) {
-                load(x1, b + 1);
-                multiply(x0);
-                load(x0, b + 2);
-                multiply(x1);
-            }
-            if (b + 1 < b_hi) {
-                load(x1, b + 1);
-                multiply(x0);
-                multiply(x1);
-            } else {
-                multiply(x0);
-            }
-        } else {
-            for (; b + 1 < b_hi; ++b) {
-                multiply(x0);
-                __builtin_amdgcn_sched_barrier(0);
-                load(x0, b + 1);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            multiply(x0);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    }
-    // the steps that fill no batch, K's ragged end, and every step of a narrow
-    // matrix: one fragment step at a time, in the MFMA's lane order
-    const int all = (p.K + KSTEP - 1) / KSTEP;
-    for (int t = 4 * batches + (S::WAVES - 1 - wave); t < all; t += S::WAVES) {
-        const int k = t * KSTEP + VEC * (lane / 16);
-        const bool whole = t < steps;
-        u32x4 fa[RF];
-        uint32_t br[S::KC ? 1 : NF * 4];
-        if constexpr (!S::KC)
-            if (whole)
-                load_rows(br, B + (int64_t)t * KSTEP * p.ldb,
-                          off_b[0][0] - (uint32_t)((int64_t)3 * VEC * (lane / 16) * p.ldb * ES));
-#pragma unroll
-        for (int i = 0; i < RF; ++i) {
-            const T* row = A + (int64_t)last(i * 16 + lane % 16, rows) * p.lda;
-            fa[i] = whole ? *reinterpret_cast<const u32x4_elem<T>*>(row + k)
-                          : clamped_chunk<T>(row, 1, k, p.K);
-        }
-#pragma unroll
-        for (int j = 0; j < NF; ++j) {
-            const int c = last(S::column(j, lane % 16), p.N - nb);
-            u32x4 fb;
-            if constexpr (S::KC) {
-                const T* row = B + (int64_t)c * p.ldb;
-                fb = whole ? *reinterpret_cast<const u32x4_elem<T>*>(row + k)
-                           : clamped_chunk<T>(row, 1, k, p.K);
-            } else {
-                fb = whole ? rows_fragment<S>(br, j) : clamped_chunk<T>(B + c, p.ldb, k, p.K);
-            }
-#pragma unroll
-            for (int i = 0; i < RF; ++i) mfma16<T>(fa[i], fb, acc[i][j]);
         }
     }
 
     // the low-rank part of this thread's outputs
-    f32x4 low[RAG == RAG_LORA ? S::PASSES * S::IPT : 1];
-    if constexpr (RAG == RAG_LORA) {
+    f32x4 low[LORA ? S::PASSES * S::IPT : 1];
+    if constexpr (LORA) {
 #pragma unroll
         for (int q = 0; q < S::PASSES * S::IPT; ++q) {
             const int item = tid + (q % S::IPT) * S::THREADS, slot = item / 64, l = item & 63;
@@ -322,7 +374,15 @@ __global__ __launch_bounds__(S::THREADS) void stream_kernel(RaggedArgs p)
             const int col = nb + S::slot_column(slot % NF, l);
             low[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             if (item < S::ITEMS && row < rows && col < p.N && adapter[row] >= 0)
-                low[q] = lora_row<T>(p, r0 + row, col, adapter[row], nb + S::BN <= p.N);
+                low[q] = lora_row<T>(p, col, adapter[row], nb + S::BN <= p.N,
+                                     [&](int r, f32x4 (&t)[2]) __attribute__((always_inline)) {
+                                         if constexpr (RAG == RAG_LORA) {
+                                             load_t(p, r0 + row, r, t);
+                                         } else {
+                                             t[0] = *reinterpret_cast<const f32x4*>(&t_row[row][r]);
+                                             t[1] = *reinterpret_cast<const f32x4*>(&t_row[row][r + 4]);
+                                         }
+                                     });
         }
     }
 
@@ -350,7 +410,7 @@ __global__ __launch_bounds__(S::THREADS) void stream_kernel(RaggedArgs p)
             f32x4 v = part[0][slot][l];
 #pragma unroll
             for (int w = 1; w < S::WAVES; ++w) v += part[w][slot][l];
-            if constexpr (RAG == RAG_LORA) v += low[pass * S::IPT + h];
+            if constexpr (LORA) v += low[pass * S::IPT + h];
             v *= p.alpha;
             const int64_t at = start + r0 + row;
             OutT* d = reinterpret_cast<OutT*>(p.D) + at * p.ldd + col;

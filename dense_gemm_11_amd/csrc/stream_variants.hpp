@@ -68,6 +68,15 @@ const RaggedTile* stream_tiles(int* count)
 }
 
 template <typename T>
+const RaggedTile* stream_tiles_lora_one(int* count)
+{
+    static constexpr RaggedTile tiles[] = {stream_tile<T, RAG_LORA_ONE, 1, 4, 4>(),
+                                           stream_tile<T, RAG_LORA_ONE, 1, 1, STREAM_N1<T>>()};
+    *count = (int)(sizeof(tiles) / sizeof(tiles[0]));
+    return tiles;
+}
+
+template <typename T>
 const RaggedTile* stream_tiles_shrink(int* count)
 {
     constexpr int N1 = STREAM_N1<T>;
