@@ -36,13 +36,10 @@ template <typename T, int RAG>
 const RaggedTile* stream_tiles(int* count)
 {
     constexpr int N1 = STREAM_N1<T>;
-    // costs of bf16 and fp32 operands, without and with adapters
+    // costs of bf16 and fp32 operands without adapters, then with
     constexpr int X = (sizeof(T) == 4 ? 1 : 0) + (RAG == RAG_LORA ? 2 : 0);
     constexpr TileCost cost[5][4] = {
-        {{4.9f, 2.01f, 3.7f, 2.06f},
-         {5.8f, 6.69f, 3.6f, 7.30f},
-         {10.4f, 2.80f, 5.8f, 3.31f},
-         {9.7f, 9.04f, 8.0f, 8.59f}},
+        {{4.9f, 2.01f, 3.7f, 2.06f}, {}, {10.4f, 2.80f, 5.8f, 3.31f}, {}},
         {{5.5f, 0.68f, 4.3f, 2.48f},
          {8.6f, 3.26f, 4.1f, 12.44f},
          {11.2f, 3.24f, 6.0f, 3.82f},
@@ -59,12 +56,20 @@ const RaggedTile* stream_tiles(int* count)
          {4.4f, 2.07f, 1.5f, 1.93f},
          {10.7f, 1.08f, 1.9f, 1.46f},
          {9.5f, 4.17f, 2.4f, 2.16f}}};
-    static constexpr RaggedTile tiles[] = {
-        stream_tile<T, RAG, 4, 1, N1>(cost[0][X]), stream_tile<T, RAG, 2, 4, 4>(cost[1][X]),
-        stream_tile<T, RAG, 2, 1, N1>(cost[2][X]), stream_tile<T, RAG, 1, 4, 4>(cost[3][X]),
-        stream_tile<T, RAG, 1, 1, N1>(cost[4][X])};
-    *count = (int)(sizeof(tiles) / sizeof(tiles[0]));
-    return tiles;
+    // 64 rows of fp32 go to the direct-to-LDS tile of that height instead
+    constexpr RaggedTile low[] = {
+        stream_tile<T, RAG, 2, 4, 4>(cost[1][X]), stream_tile<T, RAG, 2, 1, N1>(cost[2][X]),
+        stream_tile<T, RAG, 1, 4, 4>(cost[3][X]), stream_tile<T, RAG, 1, 1, N1>(cost[4][X])};
+    if constexpr (sizeof(T) == 4) {
+        static constexpr RaggedTile tiles[] = {low[0], low[1], low[2], low[3]};
+        *count = 4;
+        return tiles;
+    } else {
+        static constexpr RaggedTile tiles[] = {stream_tile<T, RAG, 4, 1, N1>(cost[0][X]), low[0], low[1],
+                                               low[2], low[3]};
+        *count = 5;
+        return tiles;
+    }
 }
 
 template <typename T>
