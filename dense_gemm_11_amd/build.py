@@ -32,7 +32,7 @@ SOURCES = ["api.hip", "inst_bf16.hip", "inst_bf16_dma.hip", "inst_bf16_dma_out.h
            "inst_rag_rows_bf16.hip", "inst_rag_lora_bf16.hip", "inst_rag_k_bf16.hip",
            "inst_rag_f32.hip", "inst_rag_stream_rows.hip",
            "inst_rag_stream_lora.hip", "inst_rag_stream_lora_one.hip",
-           "inst_rag_stream_shrink.hip"]
+           "inst_rag_stream_shrink.hip", "inst_rag_stream_k.hip"]
 
 
 def hipcc() -> str:

@@ -27,8 +27,8 @@ const RaggedTile* ragged_lora_f32(int* count)
 const RaggedTile* ragged_k_f32(int* count)
 {
     static const RaggedTile tiles[] = {
-        DG_RAGGED_K_F32(SelF32Mid, {9.0f, 0.0f, 8.1f, 89.8f}),
-        DG_RAGGED_K_F32(RagF32Low, {7.8f, 40.8f, 4.7f, 41.4f})};
+        DG_RAGGED_K_F32(SelF32Mid, {11.9f, 71.58f, 5.9f, 70.77f}),
+        DG_RAGGED_K_F32(RagF32Low, {7.3f, 49.28f, 3.0f, 35.35f})};
     *count = (int)(sizeof(tiles) / sizeof(tiles[0]));
     return tiles;
 }

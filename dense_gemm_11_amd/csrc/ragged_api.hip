@@ -39,7 +39,7 @@ bool c_d_ok(const void* C, int64_t span_c, const void* D, int64_t span_d, bool s
 }
 
 // A call's tiles, tallest first: the direct-to-LDS ones, then the streaming
-// ones (if it has any).
+// ones.
 struct TileList {
     const RaggedTile* dma;
     const RaggedTile* stream;
@@ -52,7 +52,7 @@ TileList tile_list(TileTable dma, TileTable stream)
     TileList l{};
     int n_stream = 0;
     l.dma = dma(&l.n_dma);
-    if (stream) l.stream = stream(&n_stream);
+    l.stream = stream(&n_stream);
     l.n = l.n_dma + n_stream;
     return l;
 }
@@ -246,13 +246,15 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_handle_t h, int64_t M, int64_t N, int6
     a.stride_c = strideC;
     a.stride_d = strideD;
     const TileList tiles =
-        tile_list(dtype == GEMM_DTYPE_F32 ? ragged_k_f32 : ragged_k_bf16, nullptr);
+        dtype == GEMM_DTYPE_F32 ? tile_list(ragged_k_f32, stream_k_f32)
+                                : tile_list(ragged_k_bf16, stream_k_bf16);
     const RaggedTile& t = pick_tile(tiles, h->forced_rows, false, rows / G, 0.0, [&](const RaggedTile& x) {
         return (double)(G * ceil_div(M, x.bm) * ceil_div(N, x.bn[0]));
     });
     const int bn = t.bn[0];
-    // one K-step's offsets (the kernel bases each step anew)
-    if (!panel_fits(t.bk, 2 * lda, t.bm, es) || !panel_fits(t.bk, 2 * ldb, bn, es))
+    // offsets of one K-step, or of one batch of them (the kernels base each anew)
+    const int64_t ks = t.stream ? 4 * t.bk : t.bk;
+    if (!panel_fits(ks, 2 * lda, t.bm, es) || !panel_fits(ks, 2 * ldb, bn, es))
         return GEMM_ERR_NOT_SUPPORTED;
     a.tiles_m = (int)ceil_div(M, t.bm);
     a.tiles_n = (int)ceil_div(N, bn);

@@ -49,6 +49,8 @@ inline double expected_us(const RaggedTile& t, bool b_kc, double tiles, double K
 // them.
 const RaggedTile* stream_rows_bf16(int* count);
 const RaggedTile* stream_rows_f32(int* count);
+const RaggedTile* stream_k_bf16(int* count);
+const RaggedTile* stream_k_f32(int* count);
 const RaggedTile* stream_lora_bf16(int* count);
 const RaggedTile* stream_lora_f32(int* count);
 // RAG_LORA_ONE: 16 rows, the wide tile first

@@ -58,7 +58,7 @@ struct StreamConfig {
     static constexpr int IPT = (ITEMS + THREADS - 1) / THREADS;
     // a second batch in flight where the registers hold it
     static constexpr bool TWO = (RF + NF) * 36 - (KC ? 0 : 4 * NF) + 4 * RF * NF < 240;
-    static_assert(RF % PF == 0 && NF <= 8, "exchange");
+    static_assert(RF % PF == 0 && NF <= 4, "exchange");
     static_assert(KC || NF * ES >= 4, "an n-contiguous row piece of at least 4 bytes");
     // Column within the tile of fragment j's column c.
     __device__ static constexpr int column(int j, int c) { return KC ? j * 16 + c : NF * c + j; }
@@ -104,16 +104,31 @@ __device__ __forceinline__ void quad_turn(u32x4 (&x)[4], int lane)
     swap(x[1], x[3], high, X2{});
 }
 
-// Fragment j of the rows of k in r as the MFMA operand.
-template <class S>
-__device__ __forceinline__ u32x4 rows_fragment(const uint32_t (&x)[S::NF * 4], int j)
+// VEC rows of k, `bytes` apart, of NF adjacent columns per lane (lane % 16 the
+// columns' place, lane / 16 the rows'), `off` the lane's place in them.
+template <typename T, int NF>
+__device__ __forceinline__ void load_rows(uint32_t (&x)[NF * 4], const T* row, int64_t ld, uint32_t off)
+{
+    constexpr int VEC = 16 / sizeof(T), W = NF * sizeof(T) / 4;  // words per row of k
+    using V = typename RawLoad<4 * W>::T;
+#pragma unroll
+    for (int r = 0; r < VEC; ++r) {
+        const V v = *reinterpret_cast<const V*>(reinterpret_cast<const char*>(row + (int64_t)r * ld) + off);
+#pragma unroll
+        for (int q = 0; q < W; ++q) x[W * r + q] = v[q];
+    }
+}
+
+// Fragment j of them (columns j, j + NF, ...) as the MFMA operand.
+template <typename T, int NF>
+__device__ __forceinline__ u32x4 rows_fragment(const uint32_t (&x)[NF * 4], int j)
 {
     u32x4 r;
-    if constexpr (S::ES == 4) {          // row k: words NF*k .. of the columns
+    if constexpr (sizeof(T) == 4) {      // row k: words NF*k .. of the columns
 #pragma unroll
-        for (int q = 0; q < 4; ++q) r[q] = x[S::NF * q + j];
+        for (int q = 0; q < 4; ++q) r[q] = x[NF * q + j];
     } else {                             // row k: words NF/2*k .., two columns each
-        constexpr int W = S::NF / 2;
+        constexpr int W = NF / 2;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
             r[q] = __builtin_amdgcn_perm(x[W * (2 * q + 1) + j / 2], x[W * (2 * q) + j / 2],
@@ -155,24 +170,6 @@ __device__ __forceinline__ void stream_product(const typename S::T* A, int64_t l
         off_b[0][0] = (uint32_t)(((int64_t)4 * VEC * (lane / 16) * ldb +
                                   (c < cols ? c : cols - NF)) * ES);
     }
-    // VEC rows of an n-contiguous B, from the one at `row`
-    auto load_rows = [&](uint32_t (&x)[S::KC ? 1 : NF * 4], const T* row, uint32_t off)
-                         __attribute__((always_inline)) {
-        if constexpr (!S::KC) {
-            constexpr int W = NF * ES / 4, PW = W > 4 ? 4 : W;  // words per row of k, per load
-            using V = typename RawLoad<4 * PW>::T;
-#pragma unroll
-            for (int r = 0; r < VEC; ++r) {
-                const char* b = reinterpret_cast<const char*>(row + (int64_t)r * ldb);
-#pragma unroll
-                for (int h = 0; h < W / PW; ++h) {
-                    const V v = *reinterpret_cast<const V*>(b + off + h * 16);
-#pragma unroll
-                    for (int q = 0; q < PW; ++q) x[W * r + PW * h + q] = v[q];
-                }
-            }
-        }
-    };
     auto load = [&](StreamBatch<S>& x, int batch) __attribute__((always_inline)) {
         const int k = batch * 4 * KSTEP;
         const char* a = reinterpret_cast<const char*>(A + k);
@@ -191,7 +188,7 @@ __device__ __forceinline__ void stream_product(const typename S::T* A, int64_t l
         } else {
 #pragma unroll
             for (int t = 0; t < 4; ++t)
-                load_rows(x.r[t], B + (int64_t)(k + VEC * t) * ldb, off_b[0][0]);
+                load_rows<T, NF>(x.r[t], B + (int64_t)(k + VEC * t) * ldb, ldb, off_b[0][0]);
         }
     };
     auto multiply = [&](StreamBatch<S>& x) __attribute__((always_inline)) {
@@ -206,7 +203,7 @@ __device__ __forceinline__ void stream_product(const typename S::T* A, int64_t l
             for (int j = 0; j < NF; ++j) {
                 u32x4 b;
                 if constexpr (S::KC) b = x.b[j][t];
-                else b = rows_fragment<S>(x.r[t], j);
+                else b = rows_fragment<T, NF>(x.r[t], j);
 #pragma unroll
                 for (int i = 0; i < RF; ++i) mfma16<T>(x.a[i][t], b, acc[i][j]);
             }
@@ -259,7 +256,7 @@ __device__ __forceinline__ void stream_product(const typename S::T* A, int64_t l
         uint32_t br[S::KC ? 1 : NF * 4];
         if constexpr (!S::KC)
             if (whole)
-                load_rows(br, B + (int64_t)t * KSTEP * ldb,
+                load_rows<T, NF>(br, B + (int64_t)t * KSTEP * ldb, ldb,
                           off_b[0][0] - (uint32_t)((int64_t)3 * VEC * (lane / 16) * ldb * ES));
 #pragma unroll
         for (int i = 0; i < RF; ++i) {
@@ -276,10 +273,41 @@ __device__ __forceinline__ void stream_product(const typename S::T* A, int64_t l
                 fb = whole ? *reinterpret_cast<const u32x4_elem<T>*>(row + k)
                            : clamped_chunk<T>(row, 1, k, K);
             } else {
-                fb = whole ? rows_fragment<S>(br, j) : clamped_chunk<T>(B + c, ldb, k, K);
+                fb = whole ? rows_fragment<T, NF>(br, j) : clamped_chunk<T>(B + c, ldb, k, K);
             }
 #pragma unroll
             for (int i = 0; i < RF; ++i) mfma16<T>(fa[i], fb, acc[i][j]);
+        }
+    }
+}
+
+// Four adjacent columns of D from `col`, plus beta times C's; those outside
+// [n0, N) are not stored.
+template <typename OutT>
+__device__ __forceinline__ void store_piece(OutT* d, const OutT* c, f32x4 v, float beta, int col, int n0,
+                                            int N)
+{
+    using Piece = typename RawLoad<4 * sizeof(OutT)>::T;
+    if (col >= n0 && col + 4 <= N) {
+        OutT e[4];
+        if (beta != 0.0f) {
+            const Piece w = *reinterpret_cast<const Piece*>(c);
+            __builtin_memcpy(e, &w, sizeof(e));
+#pragma unroll
+            for (int s = 0; s < 4; ++s) v[s] += beta * to_f32(e[s]);
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s) e[s] = from_f32<OutT>(v[s]);
+        Piece w;
+        __builtin_memcpy(&w, e, sizeof(e));
+        *reinterpret_cast<Piece*>(d) = w;
+    } else {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            if (col + s < n0 || col + s >= N) continue;
+            float o = v[s];
+            if (beta != 0.0f) o += beta * to_f32(c[s]);
+            d[s] = from_f32<OutT>(o);
         }
     }
 }
@@ -423,30 +451,159 @@ __global__ __launch_bounds__(S::THREADS) void stream_kernel(RaggedArgs p)
                     if (p.t_terms) store_terms(p, at, col, v);
                 continue;
             }
-            if (col >= n0 && col + 4 <= p.N) {
-                if (p.beta != 0.0f) {
-                    OutT e[4];
-                    const typename RawLoad<4 * sizeof(OutT)>::T w =
-                        *reinterpret_cast<const typename RawLoad<4 * sizeof(OutT)>::T*>(c);
-                    __builtin_memcpy(e, &w, sizeof(e));
+            store_piece(d, c, v, p.beta, col, n0, p.N);
+        }
+    });
+}
+
+// The K-ragged product (RAG_K) in the same manner, for outputs of few tiles
+// over many rows (adapters' gradients: 64 x 4096 from thousands of rows): tiles
+// of 16 F x 16 F, the eight waves splitting the group's rows, which are K, so
+// 36 tiles use the card as 288 would.  Both operands are stored by rows of K.
+// Four adapters' gradients of 64x4096 from 8192 rows: 26 -> 22.5 us; three of
+// 192x200 in fp32 from 11000 rows: 127 -> 35 us.
+template <typename T, int F, typename OutT>
+__global__ __launch_bounds__(512) void stream_k_kernel(RaggedArgs p)
+{
+    using S = StreamConfig<T, false, F, F>;
+    constexpr int KSTEP = S::KSTEP, VEC = S::VEC, ES = S::ES;
+    __shared__ f32x4 part[S::WAVES][S::SLOTS][64];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int g, t, tm, tn;
+    if (!find_k_tile(p, blockIdx.x, g, t)) return;
+    tile_of(p, t, tm, tn);
+    int start, K;
+    group_span(p, g, start, K);
+    start = __builtin_amdgcn_readfirstlane(start);
+    K = __builtin_amdgcn_readfirstlane(K);
+    if (p.scales) p.alpha *= p.scales[g];
+    // the last tile of a row or column moves back to end at the matrix's end
+    auto moved = [](int x0, int extent) {
+        return x0 + S::BM <= extent ? x0 : (extent >= S::BM ? extent - S::BM : 0);
+    };
+    const int m0 = tm * S::BM, n0 = tn * S::BN, mb = moved(m0, p.M), nb = moved(n0, p.N);
+    const int rows = p.M - mb, cols = p.N - nb;
+    const T* A = static_cast<const T*>(p.A) + (int64_t)start * p.lda + mb;
+    const T* B = static_cast<const T*>(p.B) + (int64_t)start * p.ldb + nb;
+
+    f32x4 acc[F][F] = {};
+    const int c = F * (lane % 16);
+    const uint32_t ca = (uint32_t)((c < rows ? c : rows - F) * ES);
+    const uint32_t cb = (uint32_t)((c < cols ? c : cols - F) * ES);
+    const uint32_t ka = (uint32_t)((int64_t)VEC * (lane / 16) * p.lda * ES);
+    const uint32_t kb = (uint32_t)((int64_t)VEC * (lane / 16) * p.ldb * ES);
+    struct Batch {
+        uint32_t a[4][F * 4], b[4][F * 4];
+    };
+    // lane group lane / 16 takes the VEC rows from VEC (4 (lane / 16) + s) in step s
+    auto load = [&](Batch& x, int batch) __attribute__((always_inline)) {
+        const int k = batch * 4 * KSTEP;
 #pragma unroll
-                    for (int s4 = 0; s4 < 4; ++s4) v[s4] += p.beta * to_f32(e[s4]);
-                }
-                OutT e[4];
+        for (int s = 0; s < 4; ++s) {
+            load_rows<T, F>(x.a[s], A + (int64_t)(k + VEC * s) * p.lda, p.lda, 4 * ka + ca);
+            load_rows<T, F>(x.b[s], B + (int64_t)(k + VEC * s) * p.ldb, p.ldb, 4 * kb + cb);
+        }
+    };
+    auto multiply_step = [&](const uint32_t (&a)[F * 4], const uint32_t (&b)[F * 4])
+                             __attribute__((always_inline)) {
+        u32x4 fa[F];
 #pragma unroll
-                for (int s4 = 0; s4 < 4; ++s4) e[s4] = from_f32<OutT>(v[s4]);
-                typename RawLoad<4 * sizeof(OutT)>::T w;
-                __builtin_memcpy(&w, e, sizeof(e));
-                *reinterpret_cast<typename RawLoad<4 * sizeof(OutT)>::T*>(d) = w;
-            } else {
+        for (int i = 0; i < F; ++i) fa[i] = rows_fragment<T, F>(a, i);
 #pragma unroll
-                for (int s4 = 0; s4 < 4; ++s4) {
-                    if (col + s4 < n0 || col + s4 >= p.N) continue;
-                    float o = v[s4];
-                    if (p.beta != 0.0f) o += p.beta * to_f32(c[s4]);
-                    d[s4] = from_f32<OutT>(o);
-                }
+        for (int j = 0; j < F; ++j) {
+            const u32x4 fb = rows_fragment<T, F>(b, j);
+#pragma unroll
+            for (int i = 0; i < F; ++i) mfma16<T>(fa[i], fb, acc[i][j]);
+        }
+    };
+    auto multiply = [&](const Batch& x) __attribute__((always_inline)) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) multiply_step(x.a[s], x.b[s]);
+    };
+    const bool narrow = rows < F || cols < F || (rows < S::BM && rows % F != 0) ||
+                        (cols < S::BN && cols % F != 0);
+    const int steps = narrow ? 0 : K / KSTEP, batches = steps / 4;
+    const int b_lo = (int)((int64_t)batches * wave / S::WAVES);
+    const int b_hi = (int)((int64_t)batches * (wave + 1) / S::WAVES);
+    if (b_lo < b_hi) {
+        Batch x0;
+        load(x0, b_lo);
+        int b = b_lo;
+        if constexpr (F <= 2) {
+            Batch x1;
+            for (; b + 2 < b_hi; b += 2) {
+                load(x1, b + 1);
+                multiply(x0);
+                load(x0, b + 2);
+                multiply(x1);
             }
+            if (b + 1 < b_hi) {
+                load(x1, b + 1);
+                multiply(x0);
+                multiply(x1);
+            } else {
+                multiply(x0);
+            }
+        } else {
+            for (; b + 1 < b_hi; ++b) {
+                multiply(x0);
+                __builtin_amdgcn_sched_barrier(0);
+                load(x0, b + 1);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            multiply(x0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    // the steps that fill no batch, K's ragged end and narrow matrices
+    const int all = (K + KSTEP - 1) / KSTEP;
+    for (int s = 4 * batches + (S::WAVES - 1 - wave); s < all; s += S::WAVES) {
+        if (s < steps) {
+            uint32_t xa[F * 4], xb[F * 4];
+            load_rows<T, F>(xa, A + (int64_t)s * KSTEP * p.lda, p.lda, ka + ca);
+            load_rows<T, F>(xb, B + (int64_t)s * KSTEP * p.ldb, p.ldb, kb + cb);
+            multiply_step(xa, xb);
+            continue;
+        }
+        const int k = s * KSTEP + VEC * (lane / 16);
+        u32x4 fa[F];
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+            fa[i] = clamped_chunk<T>(A + (c + i < rows ? c + i : rows - 1), p.lda, k, K);
+#pragma unroll
+        for (int j = 0; j < F; ++j) {
+            const u32x4 fb = clamped_chunk<T>(B + (c + j < cols ? c + j : cols - 1), p.ldb, k, K);
+#pragma unroll
+            for (int i = 0; i < F; ++i) mfma16<T>(fa[i], fb, acc[i][j]);
+        }
+    }
+
+    static_for<S::PASSES>([&](auto pass_c) __attribute__((always_inline)) {
+        constexpr int pass = decltype(pass_c)::value;
+        if constexpr (pass > 0) __syncthreads();
+        static_for<S::SLOTS>([&](auto q_c) __attribute__((always_inline)) {
+            constexpr int slot = decltype(q_c)::value, i = pass * S::PF + slot / F, q = slot % F;
+            f32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = acc[i][(4 * q + e) % F][(4 * q + e) / F];
+            part[wave][slot][lane] = v;
+        });
+        __syncthreads();
+#pragma unroll
+        for (int h = 0; h < S::IPT; ++h) {
+            const int item = tid + h * S::THREADS, slot = item / 64, l = item & 63;
+            if (item >= S::ITEMS) break;
+            const int row = mb + F * (l % 16) + pass * S::PF + slot / F;
+            const int col = nb + S::slot_column(slot % F, l);
+            if (row < m0 || row >= p.M || col >= p.N) continue;
+            f32x4 v = part[0][slot][l];
+#pragma unroll
+            for (int w = 1; w < S::WAVES; ++w) v += part[w][slot][l];
+            v *= p.alpha;
+            store_piece(reinterpret_cast<OutT*>(p.D) + g * p.stride_d + (int64_t)row * p.ldd + col,
+                        reinterpret_cast<const OutT*>(p.C) + g * p.stride_c + (int64_t)row * p.ldc + col,
+                        v, p.beta, col, n0, p.N);
         }
     });
 }

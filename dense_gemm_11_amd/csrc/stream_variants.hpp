@@ -72,6 +72,32 @@ const RaggedTile* stream_tiles(int* count)
     }
 }
 
+// ... of the K-ragged product.
+template <typename T, int F>
+constexpr RaggedTile stream_k_tile(TileCost cost)
+{
+    RaggedTile t{16 * F,
+                 {16 * F, 16 * F},
+                 StreamConfig<T, false, F, F>::KSTEP,
+                 {{launch_ragged<stream_k_kernel<T, F, float>, 512>, nullptr}, {nullptr, nullptr}},
+                 true,
+                 cost};
+    if constexpr (sizeof(T) == 2) t.fn[0][1] = launch_ragged<stream_k_kernel<T, F, bf16_t>, 512>;
+    return t;
+}
+
+template <typename T>
+const RaggedTile* stream_k_tiles(int* count)
+{
+    constexpr int X = sizeof(T) == 4;
+    constexpr TileCost cost[2][2] = {{{8.3f, 5.95f, 5.5f, 4.51f}, {8.9f, 46.83f, 6.1f, 26.99f}},
+                                     {{6.1f, 2.89f, 2.6f, 2.64f}, {5.3f, 9.50f, 1.7f, 8.59f}}};
+    static constexpr RaggedTile tiles[] = {stream_k_tile<T, 4>(cost[0][X]),
+                                           stream_k_tile<T, 2>(cost[1][X])};
+    *count = (int)(sizeof(tiles) / sizeof(tiles[0]));
+    return tiles;
+}
+
 template <typename T>
 const RaggedTile* stream_tiles_lora_one(int* count)
 {

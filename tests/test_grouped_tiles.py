@@ -94,6 +94,36 @@ def test_wgrad_deals_every_tile(sizes, M, N, dtype, tile):
 
 
 @gpu
+@pytest.mark.parametrize("tile", [0, 32, 64])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "bf16_out"])
+@pytest.mark.parametrize("M,N", [(8, 200), (3, 70), (65, 33), (64, 130), (1, 1)])
+def test_wgrad_of_many_rows_and_few_columns(M, N, dtype, tile):
+    """Several batches of rows per wave, a remainder, extents below and off a
+    tile, factors and gradients added to."""
+    require_gpu()
+    announce("wgrad long", M, N, dtype, tile)
+    ti, to = TYPES[dtype]
+    sizes = [3000, 1, 0, 1153]
+    at = bounds_of(sizes)
+    A, B, C = draw((at[-1], M), 1, ti), draw((at[-1], N), 2, ti), draw((4, M, N), 3, to)
+    s = draw((4,), 4, torch.float32)
+    val = 0.5 * C.double()
+    den = val.abs()
+    for i in range(4):
+        a, b = A[at[i]:at[i + 1]].double(), B[at[i]:at[i + 1]].double()
+        val[i] += float(s[i]) * (a.T @ b)
+        den[i] += abs(float(s[i])) * (a.abs().T @ b.abs())
+    h = handle(tile)
+    try:
+        D = padded(torch.full((4, M, N), float("nan"), dtype=to), 1)
+        g().run_grouped_wgrad(h, padded(A, 1, 1), padded(B, 3, 1), D, int32(at), C=C.cuda(), beta=0.5,
+                              scales=s.cuda())
+        check(D.cpu(), val, den, max(sizes), "wgrad long")
+    finally:
+        g().gemm_destroy(h)
+
+
+@gpu
 @pytest.mark.parametrize("tile", [64, 128, 192, 256])
 @pytest.mark.parametrize("up", ["N", "T"])
 @pytest.mark.parametrize("trans", ["N", "T"])
