@@ -501,6 +501,8 @@ def _stream_on(device):
     """The current stream of a device, as an integer."""
     import torch
 
+    if device < 0:
+        raise ValueError("the tensors must be on a GPU")
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without a Stream object
     return raw(device) if raw else torch.cuda.current_stream(device).cuda_stream
 

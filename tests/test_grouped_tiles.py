@@ -209,3 +209,20 @@ def test_lora_of_few_rows_keeps_requests_apart(tile):
             assert torch.isnan(got[0:4] if bad == 0 else got[4:7]).all()
     finally:
         g().gemm_destroy(h)
+
+
+def test_host_tensors_are_refused():
+    """Nothing is launched on pointers of host memory."""
+    h = g().gemm_create()
+    A, B, D = torch.zeros(4, 6), torch.zeros(2, 6, 5), torch.zeros(4, 5)
+    off = torch.zeros(3, dtype=torch.int32)
+    try:
+        with pytest.raises(ValueError, match="GPU"):
+            g().run_grouped(h, A, B, D, off)
+        with pytest.raises(ValueError, match="GPU"):
+            g().run_grouped_wgrad(h, A, D, torch.zeros(2, 6, 5), off)
+        with pytest.raises(ValueError, match="GPU"):
+            g().run_lora(h, A, B[0], D, off, torch.zeros(2, 3, 6), torch.zeros(2, 5, 3),
+                         torch.zeros(4096, dtype=torch.uint8))
+    finally:
+        g().gemm_destroy(h)
