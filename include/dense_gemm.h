@@ -347,8 +347,8 @@ gemm_status_t gemm_set_stream_k_poll_limit(gemm_handle_t h, int polls);
  * later values.  Groups may be empty, and rows before offsets[0] or from
  * offsets[groups] on belong to no group.  Entries outside [0, M] are taken as
  * the nearest bound and a negative length as an empty group: no value leads
- * outside the operands (rows that overlapping groups share then hold one
- * group's result).  At most 65536 groups (GEMM_ERR_NOT_SUPPORTED beyond).
+ * outside the operands (with offsets that decrease, rows that groups share
+ * hold one group's result, and where they share many some stay unwritten).  At most 65536 groups (GEMM_ERR_NOT_SUPPORTED beyond).
  * scales, when not NULL, holds one fp32 factor per group on the device, and
  * alpha is multiplied by it.
  *
@@ -402,6 +402,10 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_handle_t h, int64_t M, int64_t N, int6
  * scales: one fp32 factor per adapter on the device, or NULL.
  * The gradient with respect to A is the same call on D's gradient with the
  * other transB, up and down in each other's place and both GEMM_OP_N.
+ *
+ * With bf16 operands the rows' products with down may enter the second product
+ * as a sum of two bf16 terms (16 bits); an infinity in up can then come out as
+ * NaN, in the rows of that adapter only.
  *
  * The rows' products with down are formed in fp32 in `workspace`, device
  * memory of at least gemm_lora_workspace_bytes(M, rank) bytes that is 256-byte
