@@ -348,7 +348,8 @@ gemm_status_t gemm_set_stream_k_poll_limit(gemm_handle_t h, int polls);
  * offsets[groups] on belong to no group.  Entries outside [0, M] are taken as
  * the nearest bound and a negative length as an empty group: no value leads
  * outside the operands (with offsets that decrease, rows that groups share
- * hold one group's result, and where they share many some stay unwritten).  At most 65536 groups (GEMM_ERR_NOT_SUPPORTED beyond).
+ * hold one group's result, and where they share many some stay unwritten).
+ * At most 65536 groups (GEMM_ERR_NOT_SUPPORTED beyond).
  * scales, when not NULL, holds one fp32 factor per group on the device, and
  * alpha is multiplied by it.
  *

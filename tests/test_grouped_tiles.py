@@ -211,6 +211,52 @@ def test_lora_of_few_rows_keeps_requests_apart(tile):
         g().gemm_destroy(h)
 
 
+@gpu
+@pytest.mark.parametrize("tile", [0, 16, 32, 64, 128, 192, 256])
+def test_rows_past_32_bits(tile):
+    """Groups whose rows lie 2^31 elements and 2^32 bytes into A, and
+    matrices 1 GiB apart: the three calls on the last rows."""
+    require_gpu()
+    announce("past 32 bits", tile)
+    bf16 = torch.bfloat16
+    M, K, N, R, tail = 264000, 8192, 24, 8, 70
+    sizes = [M - tail, 0, 41, 29]
+    off = int32(bounds_of(sizes))
+    A = torch.zeros(M, K, dtype=bf16, device="cuda")
+    last = draw((tail, K), 1, bf16)
+    A[M - tail:] = last.cuda()
+    far = torch.zeros(4, 2 ** 30 // 2, dtype=bf16, device="cuda")   # matrices 2^30 bytes apart
+    B = far.as_strided((4, N, K), (far.stride(0), K, 1))
+    b = draw((4, N, K), 2, bf16)
+    B.copy_(b.cuda())
+    val, den = (torch.cat(x) for x in zip(*(
+        (last[lo:hi].double() @ b[i].double().T, last[lo:hi].double().abs() @ b[i].double().abs().T)
+        for i, lo, hi in ((2, 0, 41), (3, 41, 70)))))
+    h = handle(tile)
+    try:
+        D = torch.full((M, N), 7.0, device="cuda")
+        g().run_grouped(h, A, B, D, off, transB="T")
+        check(D[M - tail:].cpu(), val, den, K, "rows")
+        assert not D[:M - tail].any()
+        dn, u = draw((4, R, K), 3, bf16), draw((4, N, R), 4, bf16)
+        g().run_lora(h, A, B[0], D, off, dn.cuda(), u.cuda(), g().lora_workspace(M, R), transB="T")
+        ref = lora_reference(last, b[0], None, [0, 0, 41, 29], 0, None, dn, u, "T", 1.0, 0.0, None)
+        check(D[M - tail:].cpu(), ref[0], ref[1], 2 * K + R, "adapters", 2.0 ** -18, ref[2])
+        assert not D[:M - tail].any()
+        Y = torch.zeros(M, 8, dtype=bf16, device="cuda")
+        y = draw((tail, 8), 5, bf16)
+        Y[M - tail:] = y.cuda()
+        dB = torch.empty(4, 8, K, device="cuda")
+        g().run_grouped_wgrad(h, Y, A, dB, off)
+        got = dB.cpu()
+        assert not got[:2].any()
+        for i, lo, hi in ((2, 0, 41), (3, 41, 70)):
+            p, q = y[lo:hi].double(), last[lo:hi].double()
+            check(got[i], p.T @ q, p.abs().T @ q.abs(), hi - lo, f"gradient {i}")
+    finally:
+        g().gemm_destroy(h)
+
+
 def test_host_tensors_are_refused():
     """Nothing is launched on pointers of host memory."""
     h = g().gemm_create()
