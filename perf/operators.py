@@ -231,8 +231,12 @@ def prepare(case, seed):
         if op in ("lora", "lora_grad"):
             st["ws"] = g.lora_workspace(rows, case["rank"])
         if op == "lora_grad":
-            st["T"] = torch.empty(rows, case["rank"], dtype=ti, device="cuda")
-            st["U"] = torch.empty(rows, case["rank"], dtype=ti, device="cuda")
+            r, f32 = case["rank"], torch.float32
+            st["TU"] = torch.empty(2, rows, r, dtype=f32, device="cuda")
+            if ti is not f32:
+                st["terms"] = torch.empty(2, rows, 2, r, dtype=ti, device="cuda")
+                st["ddown2"] = torch.empty(case["adapters"], 2, r, k, dtype=f32, device="cuda")
+                st["dup2"] = torch.empty(case["adapters"], n, 2, r, dtype=f32, device="cuda")
     return st
 
 
@@ -257,11 +261,26 @@ def _run_own(st):
         g.run_lora(h, st["X"], st["W"], st["D"], off, st["down"], st["up"], st["ws"],
                    ids=st["ids_gpu"], scales=st["scales"], transB=st["trans"])
         return st["D"]
-    # the adapters' activations and gradients in the operands' type between the calls
-    g.run_grouped(h, st["X"], st["down"], st["T"], off, transB="T", scales=st["scales"])
-    g.run_grouped(h, st["dY"], st["up"], st["U"], off, transB="N", scales=st["scales"])
-    g.run_grouped_wgrad(h, st["U"], st["X"], st["ddown"], off)
-    g.run_grouped_wgrad(h, st["dY"], st["T"], st["dup"], off)
+    # the adapters' activations T and gradients U, in fp32
+    T, U = st["TU"]
+    g.run_grouped(h, st["X"], st["down"], T, off, transB="T", scales=st["scales"])
+    g.run_grouped(h, st["dY"], st["up"], U, off, transB="N", scales=st["scales"])
+    if "terms" not in st:
+        g.run_grouped_wgrad(h, U, st["X"], st["ddown"], off)
+        g.run_grouped_wgrad(h, st["dY"], T, st["dup"], off)
+    else:
+        # as operands of bf16 products they go in as two terms side by side, hi +
+        # lo (16 bits: one bf16 rounding would be as large as the gradients' own),
+        # whose two fp32 products are then added and rounded once
+        hi, lo = st["terms"][:, :, 0], st["terms"][:, :, 1]
+        hi.copy_(st["TU"])
+        torch.sub(st["TU"], hi, out=lo)
+        T2, U2 = st["terms"].flatten(2)
+        dd, du = st["ddown2"], st["dup2"]
+        g.run_grouped_wgrad(h, U2, st["X"], dd.flatten(1, 2), off)
+        g.run_grouped_wgrad(h, st["dY"], T2, du.flatten(2), off)
+        torch.add(dd[:, 0], dd[:, 1], out=st["ddown"])
+        torch.add(du[:, :, 0], du[:, :, 1], out=st["dup"])
     g.run_lora(h, st["dY"], st["W"], st["dX"], off, st["up"], st["down"], st["ws"],
                ids=st["ids_gpu"], scales=st["scales"], transB=flip, transDown="N", transUp="N")
     return st["dX"], st["ddown"], st["dup"]
