@@ -402,7 +402,12 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_handle_t h, int64_t M, int64_t N, int6
  * type, element alignment, and adapter a's at a*stride elements (>= 0).
  * scales: one fp32 factor per adapter on the device, or NULL.
  * The gradient with respect to A is the same call on D's gradient with the
- * other transB, up and down in each other's place and both GEMM_OP_N.
+ * other transB, up and down in each other's place and both GEMM_OP_N.  Those of
+ * down_a and up_a are gemm_run_grouped_wgrad on T = s_a A op(down_a) and U =
+ * s_a dD op(up_a)^T, by gemm_run_grouped with the segments as groups.  With bf16
+ * operands, T and U as bf16 cost the gradients about what their own rounding to
+ * bf16 does; in fp32 and then as two bf16 terms side by side (hi, and lo = T -
+ * hi: 2 rank columns, whose two products add up) they cost nothing to speak of.
  *
  * With bf16 operands the rows' products with down may enter the second product
  * as a sum of two bf16 terms (16 bits); an infinity in up can then come out as
