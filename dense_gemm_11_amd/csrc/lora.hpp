@@ -74,6 +74,17 @@ __device__ __forceinline__ void store_terms(const RaggedArgs& p, int64_t row, in
     *reinterpret_cast<uint2*>(d + p.rank_pad) = uint2{lo[0], lo[1]};
 }
 
+// ... one column.
+__device__ __forceinline__ void store_term(const RaggedArgs& p, int64_t row, int col, float t)
+{
+    const float e[8] = {t};
+    u32x4 hi, lo;
+    split_terms(e, hi, lo);
+    uint16_t* d = p.t_terms + row * 2 * p.rank_pad + col;
+    d[0] = (uint16_t)hi[0];
+    d[p.rank_pad] = (uint16_t)lo[0];
+}
+
 // adapter[r] = the adapter of row m0 + r for the BM rows of a tile, or -1;
 // ends with a barrier.  (Where segments overlap, one of theirs.)
 template <int BM, int THREADS>

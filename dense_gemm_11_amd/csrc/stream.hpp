@@ -312,6 +312,36 @@ __device__ __forceinline__ void store_piece(OutT* d, const OutT* c, f32x4 v, flo
     }
 }
 
+// Four columns of a row of T from `col`, and of its terms; columns from the rank
+// to rank_pad are zero (the direct-to-LDS kernels read them).  A tile that moved
+// back to end at the rank (`moved`) has its first column n0 anywhere in a piece
+// and reaches none of the padding: it stores element by element, and the piece
+// that ends at the rank goes on to rank_pad.
+template <typename T>
+__device__ __forceinline__ void store_t(const RaggedArgs& p, int64_t row, int col, f32x4 v, int n0,
+                                        bool moved)
+{
+    float* d = reinterpret_cast<float*>(p.D) + row * p.ldd;
+    if (!moved) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) v[s] = col + s < p.N ? v[s] : 0.0f;
+        *reinterpret_cast<f32x4*>(d + col) = v;
+        if constexpr (sizeof(T) == 2)
+            if (p.t_terms) store_terms(p, row, col, v);
+        return;
+    }
+    auto store = [&](int k, float t) __attribute__((always_inline)) {
+        d[k] = t;
+        if constexpr (sizeof(T) == 2)
+            if (p.t_terms) store_term(p, row, k, t);
+    };
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+        if (col + s >= n0) store(col + s, v[s]);
+    if (col + 4 == p.N)
+        for (int k = p.N; k < p.rank_pad; ++k) store(k, 0.0f);
+}
+
 template <class S, typename OutT, int RAG>
 __global__ __launch_bounds__(S::THREADS) void stream_kernel(RaggedArgs p)
 {
@@ -443,12 +473,8 @@ __global__ __launch_bounds__(S::THREADS) void stream_kernel(RaggedArgs p)
             const int64_t at = start + r0 + row;
             OutT* d = reinterpret_cast<OutT*>(p.D) + at * p.ldd + col;
             const OutT* c = reinterpret_cast<const OutT*>(p.C) + at * p.ldc + col;
-            if constexpr (RAG == RAG_SHRINK) {  // columns past the rank are zero
-#pragma unroll
-                for (int s4 = 0; s4 < 4; ++s4) v[s4] = col + s4 < p.N ? v[s4] : 0.0f;
-                *reinterpret_cast<f32x4*>(d) = v;
-                if constexpr (ES == 2)
-                    if (p.t_terms) store_terms(p, at, col, v);
+            if constexpr (RAG == RAG_SHRINK) {
+                store_t<T>(p, at, col, v, n0, nb != n0);
                 continue;
             }
             store_piece(d, c, v, p.beta, col, n0, p.N);

@@ -15,6 +15,36 @@ INF, NAN = float("inf"), float("nan")
 
 
 @gpu
+@pytest.mark.parametrize("tile", [0, 16, 64, 128, 192, 256])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "bf16_out"])
+@pytest.mark.parametrize("down", ["N", "T"])
+@pytest.mark.parametrize("R", [72, 100, 130, 201])
+def test_lora_ranks_past_a_tile_of_the_first_product(R, down, dtype, tile):
+    """Ranks above 64 that are no multiple of 16, in a workspace of NaN: tiles of
+    one adapter, mixed tiles, rows without one."""
+    require_gpu()
+    announce("rank", R, down, dtype, tile)
+    ti, to = TYPES[dtype]
+    sizes, ids, K, N = [300, 40, 21, 3, 60], [1, 0, 1, -1, 0], 96, 136
+    M = sum(sizes)
+    A, B = draw((M, K), 1, ti), draw((N, K), 2, ti)
+    dn, up, s = draw((2, R, K), 3, ti), draw((2, N, R), 4, ti), draw((2,), 5, torch.float32)
+    flip = down == "N"
+    d_, u_ = (x.transpose(1, 2).contiguous() if flip else x for x in (dn, up))
+    h = handle(tile)
+    try:
+        ws = g().lora_workspace(M, R)
+        ws.fill_(255)
+        D = torch.full((M, N), NAN, dtype=to, device="cuda")
+        g().run_lora(h, A.cuda(), B.cuda(), D, int32(bounds_of(sizes)), d_.cuda(), u_.cuda(), ws,
+                     ids=int32(ids), scales=s.cuda(), transB="T", transDown=down, transUp=down)
+        val, den, low = lora_reference(A, B, None, sizes, 0, ids, dn, up, "T", 1.0, 0.0, s)
+        check(D.cpu(), val, den, 2 * K + R, "rank", 2.0 ** -17 if dtype != "f32" else 0.0, low)
+    finally:
+        g().gemm_destroy(h)
+
+
+@gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "bf16_f32"])
 @pytest.mark.parametrize("rank", [8, 33, 64])
 def test_adapters_gradients_round_once(rank, dtype):
