@@ -173,6 +173,13 @@ __device__ __forceinline__ bool find_k_tile(const RaggedArgs& p, int w, int& g, 
     return true;
 }
 
+// alpha times group g's factor.  An empty group of a RAG_K launch has no product
+// and takes none: its factor may well be infinite (one over its rows).
+__device__ __forceinline__ float group_alpha(const RaggedArgs& p, int g, int rows)
+{
+    return rows == 0 ? 0.0f : p.scales ? p.alpha * p.scales[g] : p.alpha;
+}
+
 // Narrow p to the workgroup's group: operands, output, M (or K) and alpha
 // become those of the group, and (tm, tn) its output tile.  False when the
 // workgroup has none.
@@ -208,7 +215,7 @@ __device__ __forceinline__ bool narrow_to_group(RaggedArgs& p, int& tm, int& tn)
         if (C) p.C = reinterpret_cast<const float*>(C + (int64_t)g * p.stride_c);
         p.D = reinterpret_cast<float*>(D + (int64_t)g * p.stride_d);
     }
-    if (p.scales) p.alpha *= p.scales[g];
+    p.alpha = group_alpha(p, g, RAG == RAG_K ? p.K : p.M);
     return true;
 }
 

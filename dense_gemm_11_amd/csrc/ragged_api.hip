@@ -149,13 +149,13 @@ gemm_status_t gemm_run_grouped(gemm_handle_t h, gemm_op_t transB, int64_t M, int
     a.M = (int)M;
     a.N = (int)N;
     a.K = reads_ab ? (int)K : 0;  // no K-steps: D = beta * C
-    a.alpha = alpha;
+    a.alpha = reads_ab ? alpha : 0.0f;
     a.beta = beta;
     a.c_vec = beta != 0.0f && aligned_to(C, eo);
     a.d_vec = aligned_to(D, eo);
     a.d_lines = aligned_to(D, 128) && ldd * eo % 128 == 0;
     a.offsets = groups->offsets;
-    a.scales = groups->scales;
+    a.scales = reads_ab ? groups->scales : nullptr;
     a.groups = groups->groups;
     a.rows = (int)M;
     a.stride_b = strideB;

@@ -503,7 +503,7 @@ __global__ __launch_bounds__(512) void stream_k_kernel(RaggedArgs p)
     group_span(p, g, start, K);
     start = __builtin_amdgcn_readfirstlane(start);
     K = __builtin_amdgcn_readfirstlane(K);
-    if (p.scales) p.alpha *= p.scales[g];
+    p.alpha = group_alpha(p, g, K);
     // the last tile of a row or column moves back to end at the matrix's end
     auto moved = [](int x0, int extent) {
         return x0 + S::BM <= extent ? x0 : (extent >= S::BM ? extent - S::BM : 0);

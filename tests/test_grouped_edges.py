@@ -45,6 +45,66 @@ def test_lora_ranks_past_a_tile_of_the_first_product(R, down, dtype, tile):
 
 
 @gpu
+@pytest.mark.parametrize("tile", [0, 32, 64, 128, 192, 256])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("beta", [0.0, 0.5])
+def test_wgrad_of_empty_groups_takes_no_factor(beta, dtype, tile):
+    """A factor of 1 / rows is infinite for an empty group, whose D_g is beta C_g
+    (0 when beta == 0) all the same."""
+    require_gpu()
+    announce("factors of empty groups", beta, dtype, tile)
+    ti, to = TYPES[dtype]
+    sizes, M, N = [0, 40, 0, 7, 0], 70, 130
+    at = bounds_of(sizes)
+    A, B, C = draw((47, M), 1, ti), draw((47, N), 2, ti), draw((5, M, N), 3, to)
+    s = torch.tensor([INF, 1 / 40, NAN, 1 / 7, -INF])
+    val, den = beta * C.double(), (beta * C.double()).abs()
+    for i in (1, 3):
+        a, b = A[at[i]:at[i + 1]].double(), B[at[i]:at[i + 1]].double()
+        val[i] += float(s[i]) * (a.T @ b)
+        den[i] += abs(float(s[i])) * (a.abs().T @ b.abs())
+    h = handle(tile)
+    try:
+        D = torch.full((5, M, N), NAN, dtype=to, device="cuda")
+        g().run_grouped_wgrad(h, A.cuda(), B.cuda(), D, int32(at), C=C.cuda() if beta else None,
+                              beta=beta, scales=s.cuda())
+        check(D.cpu(), val, den, 40, "factors")
+    finally:
+        g().gemm_destroy(h)
+
+
+@gpu
+@pytest.mark.parametrize("tile", [0, 16, 64, 128, 256])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("beta", [0.0, 0.5])
+def test_calls_without_a_product_take_no_factor(beta, dtype, tile):
+    """alpha == 0, K == 0 and no rows leave beta C, whatever the groups' factors and
+    alpha hold."""
+    require_gpu()
+    announce("no product", beta, dtype, tile)
+    ti, to = TYPES[dtype]
+    sizes, K, N = [9, 0, 30], 24, 72
+    M = sum(sizes)
+    off, s = int32(bounds_of(sizes)), torch.tensor([INF, 1.0, NAN], device="cuda")
+    A, B = draw((M, K), 1, ti).cuda(), draw((3, K, N), 2, ti).cuda()
+    Y, C, G = draw((M, N), 3, ti).cuda(), draw((M, N), 4, to), draw((3, K, N), 5, to)
+    h = handle(tile)
+    try:
+        for a, b, alpha in ((A, B, 0.0), (A[:, :0], B[:, :0], 1.0), (A[:, :0], B[:, :0], INF)):
+            D = torch.full((M, N), NAN, dtype=to, device="cuda")
+            g().run_grouped(h, a, b, D, off, C=C.cuda() if beta else None, scales=s, alpha=alpha,
+                            beta=beta)
+            check(D.cpu(), beta * C.double(), beta * C.double().abs(), 0, "rows")
+        for a, y, alpha in ((A, Y, 0.0), (A[:0], Y[:0], 1.0), (A[:0], Y[:0], INF)):
+            D = torch.full((3, K, N), NAN, dtype=to, device="cuda")
+            g().run_grouped_wgrad(h, a, y, D, off, C=G.cuda() if beta else None, scales=s,
+                                  alpha=alpha, beta=beta)
+            check(D.cpu(), beta * G.double(), beta * G.double().abs(), 0, "gradients")
+    finally:
+        g().gemm_destroy(h)
+
+
+@gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "bf16_f32"])
 @pytest.mark.parametrize("rank", [8, 33, 64])
 def test_adapters_gradients_round_once(rank, dtype):
