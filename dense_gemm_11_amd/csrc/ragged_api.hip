@@ -303,11 +303,18 @@ gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_
     const bool b_kc = transB == GEMM_OP_T;
     const bool down_kc = lora->trans_down == GEMM_OP_T, up_kc = lora->trans_up == GEMM_OP_T;
     h->last_rows = 0;
-    // without an adapter, or with nothing to multiply, the call is gemm_run
+    // without an adapter, or with nothing to multiply, the call is gemm_run on a
+    // handle of its own: h's forced variant and stream-K workspace, which other
+    // streams may be using, have no part in it
     if (M == 0 || N == 0 || K == 0 || alpha == 0.0f || R == 0 || lora->segments == 0 ||
-        lora->adapters == 0)
-        return gemm_run(h, GEMM_OP_N, transB, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, D, ldd,
-                        dtype, stream);
+        lora->adapters == 0) {
+        gemm_handle_s dense = *h;
+        dense.forced_variant = dense.stream_k_mode = -1;
+        dense.ws = nullptr;
+        dense.ws_bytes = 0;
+        return gemm_run(&dense, GEMM_OP_N, transB, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, D,
+                        ldd, dtype, stream);
+    }
     if (lda < K || ldb < (b_kc ? K : N) || ldd < N || (beta != 0.0f && ldc < N) ||
         lora->ld_down < (down_kc ? K : R) || lora->ld_up < (up_kc ? R : N))
         return GEMM_ERR_INVALID_VALUE;

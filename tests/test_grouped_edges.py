@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from .gpu_support import announce, require_gpu
-from .test_grouped import TYPES, bounds_of, check, draw, g, handle, lora_reference
+from .test_grouped import TYPES, bounds_of, check, draw, g, handle, lora_reference, raw_lora
 from .test_grouped_tiles import int32
 
 gpu = pytest.mark.gpu
@@ -102,6 +102,72 @@ def test_calls_without_a_product_take_no_factor(beta, dtype, tile):
             check(D.cpu(), beta * G.double(), beta * G.double().abs(), 0, "gradients")
     finally:
         g().gemm_destroy(h)
+
+
+# calls of run_lora that no adapter takes part in: keyword changes to a call of
+# rank 8 over two adapters
+WITHOUT = [dict(R=0), dict(adapters=0), dict(sizes=[], ids=[]), dict(K=0), dict(alpha=0.0)]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("kw", WITHOUT, ids=str)
+def test_lora_without_adapters_leaves_the_handle_alone(kw, dtype):
+    """The shared product alone, whatever the handle's workspace, stream-K mode and
+    forced variant are: the same bits as from a new handle, and the workspace
+    untouched."""
+    require_gpu()
+    announce("without adapters", kw, dtype)
+    ti, to = TYPES[dtype]
+    a = dict(dict(sizes=[300, 212], ids=[0, 1], adapters=2, R=8, K=4096, alpha=0.5), **kw)
+    M, N, K, R = 512, 520, a["K"], a["R"]
+    A, B, C = draw((M, K), 1, ti), draw((K, N), 2, ti), draw((M, N), 3, to)
+    dn = draw((a["adapters"], R, K), 4, ti).cuda()
+    up = draw((a["adapters"], N, R), 5, ti).cuda()
+    p, off, ids = g(), int32(bounds_of(a["sizes"])), int32(a["ids"])
+    got = []
+    for attached in (False, True):
+        h = p.gemm_create()
+        try:
+            if attached:
+                ws = p.attach_workspace(h)
+                torch.cuda.synchronize()
+                before = ws.clone()
+                assert p.gemm_set_stream_k(h, 1) == p.GEMM_OK
+                # a variant of the other operand type, which gemm_run refuses
+                other = next(i for i, _, d, _ in p.variants() if (d == p.GEMM_DTYPE_F32) != (dtype == "f32"))
+                assert p.gemm_set_variant(h, other) == p.GEMM_OK
+            D = torch.full((M, N), NAN, dtype=to, device="cuda")
+            p.run_lora(h, A.cuda(), B.cuda(), D, off, dn, up, p.lora_workspace(M, 8), ids=ids,
+                       C=C.cuda(), alpha=a["alpha"], beta=0.25)
+            torch.cuda.synchronize()
+            assert p.gemm_last_stream_k(h) == 0 and p.gemm_last_variant(h) == -1
+            if attached:
+                assert torch.equal(ws, before)
+            got.append(D.cpu())
+        finally:
+            p.gemm_destroy(h)
+    a64, b64, c64 = A.double(), B.double(), 0.25 * C.double()
+    check(got[0], a["alpha"] * (a64 @ b64) + c64,
+          abs(a["alpha"]) * (a64.abs() @ b64.abs()) + c64.abs(), K, "without adapters")
+    assert torch.equal(*(x.view(torch.int16 if to is torch.bfloat16 else torch.int32) for x in got))
+
+
+@pytest.mark.parametrize("kw", [dict(rank=0), dict(adapters=0), dict(segments=0)], ids=str)
+def test_lora_without_adapters_is_planned_without_the_handle(kw, monkeypatch):
+    """A forced variant of the other operand type does not refuse the call, which
+    gets as far as its launch (switched off)."""
+    p = g()
+    monkeypatch.setenv("GEMM_DEBUG_FAIL_LAUNCH", "1")
+    h = p.gemm_create()
+    p.gemm_set_planning_model(256, [1] * p.gemm_variant_count())
+    try:
+        bf16 = next(i for i, _, d, _ in p.variants() if d != p.GEMM_DTYPE_F32)
+        assert p.gemm_set_variant(h, bf16) == p.GEMM_OK
+        assert raw_lora(h, **kw) == p.GEMM_ERR_HIP
+    finally:
+        p.gemm_set_planning_model(0, None)
+        p.gemm_destroy(h)
 
 
 @gpu
