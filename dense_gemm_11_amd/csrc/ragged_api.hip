@@ -13,6 +13,11 @@ namespace {
 
 constexpr int MAX_GROUPS = 1 << 16;
 
+// The kernels form row, column and step numbers in 32 bits up to a tile or a
+// batch of steps past the end (a last tile of 192 rows would pass 2^31 from M =
+// 2^31 - 128), and twice the padded rank.
+constexpr int64_t MAX_EXTENT = INT_MAX - 512;
+
 // The layout, type and size checks that the three calls share.
 gemm_status_t check_common(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_t N, int64_t K,
                            gemm_dtype_t dtype)
@@ -129,7 +134,7 @@ gemm_status_t gemm_run_grouped(gemm_handle_t h, gemm_op_t transB, int64_t M, int
     const bool reads_ab = K > 0 && alpha != 0.0f;
     if (!groups->offsets || !D || (beta != 0.0f && !C) || (reads_ab && (!A || !B)))
         return GEMM_ERR_INVALID_VALUE;
-    if (M > INT_MAX || N > INT_MAX || K > INT_MAX || lda > INT_MAX || ldb > INT_MAX ||
+    if (M > MAX_EXTENT || N > MAX_EXTENT || K > MAX_EXTENT || lda > INT_MAX || ldb > INT_MAX ||
         ldd > INT_MAX || (beta != 0.0f && ldc > INT_MAX) || groups->groups > MAX_GROUPS)
         return GEMM_ERR_NOT_SUPPORTED;
     if (beta != 0.0f &&
@@ -206,7 +211,7 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_handle_t h, int64_t M, int64_t N, int6
     const bool reads_ab = rows > 0 && alpha != 0.0f;
     if (!groups->offsets || !D || (beta != 0.0f && !C) || (reads_ab && (!A || !B)))
         return GEMM_ERR_INVALID_VALUE;
-    if (M > INT_MAX || N > INT_MAX || rows > INT_MAX || lda > INT_MAX || ldb > INT_MAX ||
+    if (M > MAX_EXTENT || N > MAX_EXTENT || rows > MAX_EXTENT || lda > INT_MAX || ldb > INT_MAX ||
         ldd > INT_MAX || (beta != 0.0f && ldc > INT_MAX) || G > MAX_GROUPS)
         return GEMM_ERR_NOT_SUPPORTED;
     // the groups' outputs apart from each other: one after another, or
@@ -320,8 +325,8 @@ gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_
         return GEMM_ERR_INVALID_VALUE;
     if (!A || !B || !D || (beta != 0.0f && !C) || !lora->offsets || !lora->down || !lora->up)
         return GEMM_ERR_INVALID_VALUE;
-    if (M > INT_MAX || N > INT_MAX || K > INT_MAX || lda > INT_MAX || ldb > INT_MAX ||
-        ldd > INT_MAX || (beta != 0.0f && ldc > INT_MAX) || lora->segments > MAX_GROUPS ||
+    if (M > MAX_EXTENT || N > MAX_EXTENT || K > MAX_EXTENT || lda > INT_MAX || ldb > INT_MAX ||
+        ldd > INT_MAX || (beta != 0.0f && ldc > INT_MAX) || lora->segments > MAX_GROUPS || R > MAX_EXTENT / 2 ||
         lora->ld_down > INT_MAX || lora->ld_up > INT_MAX)
         return GEMM_ERR_NOT_SUPPORTED;
     if (beta != 0.0f &&

@@ -7,7 +7,8 @@ import pytest
 import torch
 
 from .gpu_support import announce, require_gpu
-from .test_grouped import TYPES, bounds_of, check, draw, g, handle, lora_reference, raw_lora
+from .test_grouped import (TYPES, bounds_of, check, draw, g, handle, lora_reference, raw_grouped, raw_lora,
+                           raw_wgrad)
 from .test_grouped_tiles import int32
 
 gpu = pytest.mark.gpu
@@ -202,3 +203,32 @@ def test_adapters_gradients_round_once(rank, dtype):
         check(ddown[a], u.T @ x, u_abs.T @ x.abs(), terms, "down", t_rel, u.abs().T @ x.abs())
         t, t_abs = s[a] * (x @ down[a].T), s[a] * (x.abs() @ down[a].abs().T)
         check(dup[a], y.T @ t, y.abs().T @ t_abs, terms, "up", t_rel, y.abs().T @ t.abs())
+
+
+# ---------------------------------------------------------------- limits (no GPU)
+@pytest.fixture
+def unlaunched(monkeypatch):
+    """A handle whose calls report GEMM_ERR_HIP where they would launch."""
+    monkeypatch.setenv("GEMM_DEBUG_FAIL_LAUNCH", "1")
+    p = g()
+    h = p.gemm_create()
+    p.gemm_set_planning_model(256, [1] * p.gemm_variant_count())
+    yield h
+    p.gemm_set_planning_model(0, None)
+    p.gemm_destroy(h)
+
+
+def test_extents_that_32_bit_sums_cannot_carry(unlaunched):
+    """Row and step numbers up to a tile past the end are formed in 32 bits."""
+    p, h, top = g(), unlaunched, 2 ** 31 - 1
+    fits = top - 512
+    assert raw_grouped(h, M=top) == raw_grouped(h, M=fits + 1) == p.GEMM_ERR_NOT_SUPPORTED
+    assert raw_grouped(h, M=fits) == p.GEMM_ERR_HIP
+    assert raw_wgrad(h, rows=top) == raw_wgrad(h, rows=fits + 1) == p.GEMM_ERR_NOT_SUPPORTED
+    assert raw_wgrad(h, rows=fits) == p.GEMM_ERR_HIP
+    big = dict(bytes=1 << 62)
+    assert raw_lora(h, M=top, **big) == p.GEMM_ERR_NOT_SUPPORTED
+    assert raw_lora(h, M=fits, **big) == p.GEMM_ERR_HIP
+    for rank in (top, 2 ** 30):
+        assert raw_lora(h, rank=rank, ld_up=top, stride_up=0, **big) == p.GEMM_ERR_NOT_SUPPORTED
+    assert raw_lora(h, rank=1 << 20, ld_up=1 << 20, stride_up=0, **big) == p.GEMM_ERR_HIP
