@@ -37,6 +37,9 @@ bool panel_fits(int64_t rows, int64_t ld, int64_t cols, int64_t es)
     return (rows * ld + cols) * es < ((int64_t)1 << 32) - 64;
 }
 
+// A launch has fewer than 2^32 threads along its first axis.
+bool grid_fits(int64_t grid, int threads) { return grid * threads < (int64_t)1 << 32; }
+
 // C against D: the same matrix with the same strides, or disjoint.
 bool c_d_ok(const void* C, int64_t span_c, const void* D, int64_t span_d, bool same_strides)
 {
@@ -63,10 +66,12 @@ TileList tile_list(TileTable dma, TileTable stream)
 }
 
 // The tallest tile up to the forced height, else the one of least expected
-// time; tiles(t) is the number of output tiles of t a call has, or expects, and
-// `bytes` what it reads and writes at the least.
-template <class F>
-const RaggedTile& pick_tile(const TileList& t, int forced, bool b_kc, int64_t K, double bytes, F tiles)
+// time among those whose grid fits; tiles(t) is the number of output tiles of t a
+// call has, or expects, grid(t) its workgroups, and `bytes` what it reads and
+// writes at the least.
+template <class F, class G>
+const RaggedTile& pick_tile(const TileList& t, int forced, bool b_kc, int64_t K, double bytes, F tiles,
+                            G grid)
 {
     int best = t.n - 1;
     if (forced > 0) {
@@ -76,8 +81,9 @@ const RaggedTile& pick_tile(const TileList& t, int forced, bool b_kc, int64_t K,
     }
     double best_us = 0.0;
     for (int i = 0; i < t.n; ++i) {
-        const double us = expected_us(t[i], b_kc, tiles(t[i]), (double)K, bytes, device_cus());
-        if (i == 0 || us < best_us) {
+        if (!grid_fits(grid(t[i]), t[i].threads)) continue;
+        const double us = expected_us(t[i], b_kc, (double)tiles(t[i]), (double)K, bytes, device_cus());
+        if (best_us == 0.0 || us < best_us) {
             best = i;
             best_us = us;
         }
@@ -169,10 +175,14 @@ gemm_status_t gemm_run_grouped(gemm_handle_t h, gemm_op_t transB, int64_t M, int
     const double bytes = (double)es * K * ((double)busy * N + M) + (double)eo * M * N;
     const TileList tiles = dtype == GEMM_DTYPE_F32 ? tile_list(ragged_rows_f32, stream_rows_f32)
                                                    : tile_list(ragged_rows_bf16, stream_rows_bf16);
+    // the most tile-rows any split into groups needs
+    auto grid_of = [&](const RaggedTile& x) {
+        return (M + busy * (x.bm - 1)) / x.bm * ceil_div(N, x.bn[b_kc]);
+    };
     const RaggedTile& t = pick_tile(tiles, h->forced_rows, b_kc, K, bytes, [&](const RaggedTile& x) {
         return ceil_div(N, x.bn[b_kc]) *
                (busy > 1 ? row_tiles((double)busy, (double)M / busy, x.bm) : (double)ceil_div(M, x.bm));
-    });
+    }, grid_of);
     const int bn = t.bn[b_kc];
     const int64_t kk = K + t.bk;
     if (!panel_fits(t.bm - 1, lda, kk, es) ||
@@ -180,9 +190,8 @@ gemm_status_t gemm_run_grouped(gemm_handle_t h, gemm_op_t transB, int64_t M, int
         return GEMM_ERR_NOT_SUPPORTED;
     a.tiles_n = (int)ceil_div(N, bn);
     a.group_m = 4;
-    // the most tile-rows any split into groups needs
-    const int64_t grid = (M + busy * (t.bm - 1)) / t.bm * a.tiles_n;
-    if (grid > INT_MAX) return GEMM_ERR_NOT_SUPPORTED;
+    const int64_t grid = grid_of(t);
+    if (!grid_fits(grid, t.threads)) return GEMM_ERR_NOT_SUPPORTED;
     if (h->fail_launch) return GEMM_ERR_HIP;
     if (t.fn[b_kc][dtype == GEMM_DTYPE_BF16_BF16](a, (int)grid, stream) != hipSuccess)
         return GEMM_ERR_HIP;
@@ -253,9 +262,10 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_handle_t h, int64_t M, int64_t N, int6
     const TileList tiles =
         dtype == GEMM_DTYPE_F32 ? tile_list(ragged_k_f32, stream_k_f32)
                                 : tile_list(ragged_k_bf16, stream_k_bf16);
-    const RaggedTile& t = pick_tile(tiles, h->forced_rows, false, rows / G, 0.0, [&](const RaggedTile& x) {
-        return (double)(G * ceil_div(M, x.bm) * ceil_div(N, x.bn[0]));
-    });
+    auto tiles_of = [&](const RaggedTile& x) { return G * ceil_div(M, x.bm) * ceil_div(N, x.bn[0]); };
+    // (every way of dealing them: a slice may round up to a tile more per XCD)
+    auto most = [&](const RaggedTile& x) { return tiles_of(x) + DEAL_XCDS * G; };
+    const RaggedTile& t = pick_tile(tiles, h->forced_rows, false, rows / G, 0.0, tiles_of, most);
     const int bn = t.bn[0];
     // offsets of one K-step, or of one batch of them (the kernels base each anew)
     const int64_t ks = t.stream ? 4 * t.bk : t.bk;
@@ -269,7 +279,7 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_handle_t h, int64_t M, int64_t N, int6
              : per < 2 * DEAL_XCDS        ? DEAL_TILES
                                           : DEAL_SLICES;
     const int64_t grid = deal_grid(a.deal, per, G);
-    if (grid > INT_MAX) return GEMM_ERR_NOT_SUPPORTED;
+    if (!grid_fits(grid, t.threads)) return GEMM_ERR_NOT_SUPPORTED;
     if (h->fail_launch) return GEMM_ERR_HIP;
     if (t.fn[0][dtype == GEMM_DTYPE_BF16_BF16](a, (int)grid, stream) != hipSuccess)
         return GEMM_ERR_HIP;
@@ -326,8 +336,8 @@ gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_
     if (!A || !B || !D || (beta != 0.0f && !C) || !lora->offsets || !lora->down || !lora->up)
         return GEMM_ERR_INVALID_VALUE;
     if (M > MAX_EXTENT || N > MAX_EXTENT || K > MAX_EXTENT || lda > INT_MAX || ldb > INT_MAX ||
-        ldd > INT_MAX || (beta != 0.0f && ldc > INT_MAX) || lora->segments > MAX_GROUPS || R > MAX_EXTENT / 2 ||
-        lora->ld_down > INT_MAX || lora->ld_up > INT_MAX)
+        ldd > INT_MAX || (beta != 0.0f && ldc > INT_MAX) || lora->segments > MAX_GROUPS ||
+        R > MAX_EXTENT / 2 || lora->ld_down > INT_MAX || lora->ld_up > INT_MAX)
         return GEMM_ERR_NOT_SUPPORTED;
     if (beta != 0.0f &&
         !c_d_ok(C, ((M - 1) * ldc + N) * eo, D, ((M - 1) * ldd + N) * eo, ldc == ldd))
@@ -371,9 +381,8 @@ gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_
     const double bytes = (double)es * K * (N + M) + (double)eo * M * N;
     const TileList tiles = dtype == GEMM_DTYPE_F32 ? tile_list(ragged_lora_f32, stream_lora_f32)
                                                    : tile_list(ragged_lora_bf16, stream_lora_bf16);
-    const RaggedTile& t = pick_tile(tiles, h->forced_rows, b_kc, K, bytes, [&](const RaggedTile& x) {
-        return (double)(ceil_div(M, x.bm) * ceil_div(N, x.bn[b_kc]));
-    });
+    auto grid_of = [&](const RaggedTile& x) { return ceil_div(M, x.bm) * ceil_div(N, x.bn[b_kc]); };
+    const RaggedTile& t = pick_tile(tiles, h->forced_rows, b_kc, K, bytes, grid_of, grid_of);
     const int bn = t.bn[b_kc];
     const int64_t kk = K + t.bk;
     if (!panel_fits(t.bm - 1, lda, kk, es) ||
@@ -382,8 +391,8 @@ gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_
     a.tiles_m = (int)ceil_div(M, t.bm);
     a.tiles_n = (int)ceil_div(N, bn);
     a.group_m = std::min(a.tiles_m, 4);
-    const int64_t grid = (int64_t)a.tiles_m * a.tiles_n;
-    if (grid > INT_MAX) return GEMM_ERR_NOT_SUPPORTED;
+    const int64_t grid = grid_of(t);
+    if (!grid_fits(grid, t.threads)) return GEMM_ERR_NOT_SUPPORTED;
     // one tile of rows and little to do for T: both products in one launch
     const int64_t segs = std::min<int64_t>(lora->segments, M);
     if (t.stream && t.bm == 16 && M <= 16 && down_kc && R <= LORA_ONE_RANK &&
@@ -435,7 +444,7 @@ gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_
         a.t_terms = f.t_terms = reinterpret_cast<uint16_t*>(static_cast<float*>(ws) + M * a.rank_pad);
     f.k_slice = (int)(ceil_div(ceil_div(K, splits), ft.bk) * ft.bk);
     f.splits = a.splits = (int)ceil_div(K, f.k_slice);
-    if (blocks > INT_MAX ||
+    if (!grid_fits(blocks, ft.threads) ||
         !(down_kc ? panel_fits(ft.bn[1] - 1, f.ldb, kk, es) : panel_fits(kk, f.ldb, ft.bn[0], es)))
         return GEMM_ERR_NOT_SUPPORTED;
     if (h->fail_launch) return GEMM_ERR_HIP;

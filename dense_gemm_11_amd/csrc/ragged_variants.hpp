@@ -15,7 +15,7 @@ struct TileCost {
 };
 
 struct RaggedTile {
-    int bm, bn[2], bk;  // bn of either layout of B
+    int bm, bn[2], bk, threads;  // bn of either layout of B
     RaggedFn fn[2][2];  // [B k-contiguous][bf16 output] (RAG_K: [0] only)
     bool stream;        // a streaming tile
     TileCost cost;
@@ -85,25 +85,25 @@ hipError_t launch_ragged(const RaggedArgs& a, int grid, hipStream_t s)
 // RaggedTile entry of configuration CFG for launch kind RAG, with its cost, A
 // stored by rows: both layouts of B, both output types (fp32 operands: fp32 only).
 #define DG_RAGGED_BF16(CFG, RAG, ...)                                                        \
-    {CFG::BM, {CFG::BN, CFG::BN}, CFG::BK,                                                   \
+    {CFG::BM, {CFG::BN, CFG::BN}, CFG::BK, CFG::THREADS,                                     \
      {{dg::launch_ragged<dg::dma_ragged_kernel<CFG, true, false, false, RAG>, CFG::THREADS>, \
        dg::launch_ragged<dg::dma_ragged_kernel<CFG, true, false, true, RAG>, CFG::THREADS>}, \
       {dg::launch_ragged<dg::dma_ragged_kernel<CFG, true, true, false, RAG>, CFG::THREADS>,  \
        dg::launch_ragged<dg::dma_ragged_kernel<CFG, true, true, true, RAG>, CFG::THREADS>}}, false, __VA_ARGS__}
 #define DG_RAGGED_F32(CFG, RAG, ...)                                                         \
-    {CFG::BM, {CFG::BN, CFG::BN}, CFG::BK,                                                   \
+    {CFG::BM, {CFG::BN, CFG::BN}, CFG::BK, CFG::THREADS,                                     \
      {{dg::launch_ragged<dg::dma_ragged_kernel<CFG, true, false, false, RAG>, CFG::THREADS>, \
        nullptr},                                                                             \
       {dg::launch_ragged<dg::dma_ragged_kernel<CFG, true, true, false, RAG>, CFG::THREADS>,  \
        nullptr}}, false, __VA_ARGS__}
 // ... and for RAG_K (both operands stored by rows).
 #define DG_RAGGED_K_BF16(CFG, ...)                                                                 \
-    {CFG::BM, {CFG::BN, CFG::BN}, CFG::BK,                                                         \
+    {CFG::BM, {CFG::BN, CFG::BN}, CFG::BK, CFG::THREADS,                                           \
      {{dg::launch_ragged<dg::dma_ragged_kernel<CFG, false, false, false, RAG_K>, CFG::THREADS>,    \
        dg::launch_ragged<dg::dma_ragged_kernel<CFG, false, false, true, RAG_K>, CFG::THREADS>},    \
       {nullptr, nullptr}}, false, __VA_ARGS__}
 #define DG_RAGGED_K_F32(CFG, ...)                                                                  \
-    {CFG::BM, {CFG::BN, CFG::BN}, CFG::BK,                                                         \
+    {CFG::BM, {CFG::BN, CFG::BN}, CFG::BK, CFG::THREADS,                                           \
      {{dg::launch_ragged<dg::dma_ragged_kernel<CFG, false, false, false, RAG_K>, CFG::THREADS>,    \
        nullptr},                                                                                   \
       {nullptr, nullptr}}, false, __VA_ARGS__}

@@ -17,6 +17,7 @@ constexpr RaggedTile stream_tile(TileCost cost = {})
     RaggedTile t{SN::BM,
                  {SN::BN, SK::BN},
                  SN::KSTEP,
+                 SN::THREADS,
                  {{launch_ragged<stream_kernel<SN, float, RAG>, SN::THREADS, SPLIT>, nullptr},
                   {launch_ragged<stream_kernel<SK, float, RAG>, SK::THREADS, SPLIT>, nullptr}},
                  true,
@@ -79,6 +80,7 @@ constexpr RaggedTile stream_k_tile(TileCost cost)
     RaggedTile t{16 * F,
                  {16 * F, 16 * F},
                  StreamConfig<T, false, F, F>::KSTEP,
+                 StreamConfig<T, false, F, F>::THREADS,
                  {{launch_ragged<stream_k_kernel<T, F, float>, 512>, nullptr}, {nullptr, nullptr}},
                  true,
                  cost};

@@ -349,8 +349,8 @@ gemm_status_t gemm_set_stream_k_poll_limit(gemm_handle_t h, int polls);
  * the nearest bound and a negative length as an empty group: no value leads
  * outside the operands (with offsets that decrease, rows that groups share
  * hold one group's result, and where they share many some stay unwritten).
- * At most 65536 groups, M, N, K and rows of 2^31 - 513, and ranks of half that
- * (GEMM_ERR_NOT_SUPPORTED beyond).
+ * At most 65536 groups, M, N, K and rows of 2^31 - 513, ranks of half that, and
+ * output tiles for 2^32 threads (GEMM_ERR_NOT_SUPPORTED beyond).
  * scales, when not NULL, holds one fp32 factor per group on the device, and
  * alpha is multiplied by it.
  *

@@ -228,7 +228,22 @@ def test_extents_that_32_bit_sums_cannot_carry(unlaunched):
     assert raw_wgrad(h, rows=fits) == p.GEMM_ERR_HIP
     big = dict(bytes=1 << 62)
     assert raw_lora(h, M=top, **big) == p.GEMM_ERR_NOT_SUPPORTED
-    assert raw_lora(h, M=fits, **big) == p.GEMM_ERR_HIP
+    assert raw_lora(h, M=2 ** 27, **big) == p.GEMM_ERR_HIP   # more are 2^32 threads
     for rank in (top, 2 ** 30):
         assert raw_lora(h, rank=rank, ld_up=top, stride_up=0, **big) == p.GEMM_ERR_NOT_SUPPORTED
     assert raw_lora(h, rank=1 << 20, ld_up=1 << 20, stride_up=0, **big) == p.GEMM_ERR_HIP
+
+
+def test_grids_of_2_32_threads_are_refused(unlaunched):
+    """65536 groups of one row by 2^24 columns are 2^41 threads of the largest tile,
+    which no launch takes; a forced height whose grid is too large is refused where
+    the automatic choice finds one that fits."""
+    p, h = g(), unlaunched
+    wide = dict(M=65536, groups=65536, strideB=0, dtype=2)
+    assert raw_grouped(h, N=2 ** 24, ldb=2 ** 24, ldd=2 ** 24, **wide) == p.GEMM_ERR_NOT_SUPPORTED
+    fits = dict(N=8192, ldb=8192, ldd=8192, **wide)
+    assert raw_grouped(h, **fits) == p.GEMM_ERR_HIP
+    assert p.gemm_set_group_tile(h, 16) == p.GEMM_OK
+    assert raw_grouped(h, **fits) == p.GEMM_ERR_NOT_SUPPORTED
+    assert raw_lora(h, M=2 ** 30, N=2 ** 10, ldb=2 ** 10, ldd=2 ** 10, ld_up=3, stride_up=2 ** 12,
+                    bytes=1 << 62) == p.GEMM_ERR_NOT_SUPPORTED
