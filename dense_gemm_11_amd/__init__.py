@@ -49,7 +49,8 @@ EXPORTS = ("gemm_create", "gemm_destroy", "gemm_run", "gemm_status_string",
            "gemm_variant_pipeline", "gemm_variant_occupancy", "gemm_stream_k_status",
            "gemm_set_stream_k_poll_limit", "gemm_run_no_alloc", "gemm_set_planning_model",
            "gemm_run_grouped", "gemm_run_grouped_wgrad", "gemm_run_lora",
-           "gemm_lora_workspace_bytes", "gemm_set_group_tile", "gemm_last_group_tile")
+           "gemm_lora_workspace_bytes", "gemm_set_group_tile", "gemm_last_group_tile",
+           "gemm_set_group_tile_nth", "gemm_last_group_launch")
 
 
 class GemmEpilogue(ctypes.Structure):
@@ -75,6 +76,12 @@ class GemmLora(ctypes.Structure):
                 ("down", ctypes.c_void_p), ("ld_down", ctypes.c_int64),
                 ("stride_down", ctypes.c_int64), ("trans_up", ctypes.c_int),
                 ("up", ctypes.c_void_p), ("ld_up", ctypes.c_int64), ("stride_up", ctypes.c_int64)]
+
+
+class GemmGroupLaunch(ctypes.Structure):
+    """gemm_group_launch_t: what the last ragged call launched."""
+    _fields_ = [(n, ctypes.c_int) for n in ("rows", "columns", "nth", "launches", "first_rows",
+                                            "first_columns", "first_slices")]
 
 
 class GemmError(RuntimeError):
@@ -171,6 +178,10 @@ def _load():
     lib.gemm_set_group_tile.restype = i32
     lib.gemm_last_group_tile.argtypes = [vp]
     lib.gemm_last_group_tile.restype = i32
+    lib.gemm_set_group_tile_nth.argtypes = [vp, i32, i32]
+    lib.gemm_set_group_tile_nth.restype = i32
+    lib.gemm_last_group_launch.argtypes = [vp, ctypes.POINTER(GemmGroupLaunch)]
+    lib.gemm_last_group_launch.restype = i32
     return lib
 
 
@@ -335,6 +346,18 @@ def gemm_set_group_tile(h, rows: int) -> int:
 
 def gemm_last_group_tile(h) -> int:
     return lib.gemm_last_group_tile(h)
+
+
+def gemm_set_group_tile_nth(h, rows: int, nth: int) -> int:
+    return lib.gemm_set_group_tile_nth(h, rows, nth)
+
+
+def gemm_last_group_launch(h) -> GemmGroupLaunch:
+    out = GemmGroupLaunch()
+    s = lib.gemm_last_group_launch(h, ctypes.byref(out))
+    if s != GEMM_OK:
+        raise GemmError(s, "gemm_last_group_launch")
+    return out
 
 
 def attach_workspace(h, nbytes=None, device=None):

@@ -924,7 +924,7 @@ gemm_status_t gemm_create(gemm_handle_t* out)
     };
     gemm_handle_t h = new (std::nothrow) gemm_handle_s{
         -1, -1, -1, 0, nullptr, 0, dg::SK_SPIN_DEFAULT, env_on("GEMM_LOG"),
-        env_on("GEMM_DEBUG_FAIL_LAUNCH"), 0, 0};
+        env_on("GEMM_DEBUG_FAIL_LAUNCH"), 0, 0, {}};
     if (!h) return GEMM_ERR_ALLOC;
     *out = h;
     return GEMM_OK;

@@ -17,7 +17,8 @@ struct gemm_handle_s {
     int log;             // GEMM_LOG: one line per call on stderr
     int fail_launch;     // GEMM_DEBUG_FAIL_LAUNCH: report GEMM_ERR_HIP instead of launching
     int forced_rows;     // row-tile height the ragged calls take (0: automatic)
-    int last_rows;       // ... and the last one took (0: none)
+    int forced_nth;      // ... and which of the tiles of that height
+    gemm_group_launch_t last_group;  // ... and the last one took (rows 0: none)
 };
 
 namespace dg {

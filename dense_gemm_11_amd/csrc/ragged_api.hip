@@ -65,18 +65,32 @@ TileList tile_list(TileTable dma, TileTable stream)
     return l;
 }
 
-// The tallest tile up to the forced height, else the one of least expected
+// Number of tile i among those of its height.
+int nth_of_height(const TileList& t, int i)
+{
+    int n = 0;
+    for (int j = 0; j < i; ++j) n += t[j].bm == t[i].bm;
+    return n;
+}
+
+// The forced tile (gemm_set_group_tile_nth), else the one of least expected
 // time among those whose grid fits; tiles(t) is the number of output tiles of t a
 // call has, or expects, grid(t) its workgroups, and `bytes` what it reads and
 // writes at the least.
 template <class F, class G>
-const RaggedTile& pick_tile(const TileList& t, int forced, bool b_kc, int64_t K, double bytes, F tiles,
-                            G grid)
+const RaggedTile& pick_tile(gemm_handle_t h, const TileList& t, bool b_kc, int64_t K, double bytes,
+                            F tiles, G grid)
 {
     int best = t.n - 1;
-    if (forced > 0) {
+    if (h->forced_rows > 0) {
+        int height = t[best].bm;
         for (int i = 0; i < t.n; ++i)
-            if (t[i].bm <= forced) return t[i];
+            if (t[i].bm <= h->forced_rows && t[i].bm > height) height = t[i].bm;
+        for (int i = 0; i < t.n; ++i)
+            if (t[i].bm == height) {
+                best = i;
+                if (nth_of_height(t, i) == h->forced_nth) break;
+            }
         return t[best];
     }
     double best_us = 0.0;
@@ -98,8 +112,14 @@ double row_tiles(double busy, double avg, int bm)
     return busy * std::max(1.0, avg / bm + 0.5);
 }
 
-void log_call(gemm_handle_t h, const char* what, const RaggedArgs& a, int bm, int bn, int64_t grid)
+// Notes and logs the launch of tile t.
+void note_call(gemm_handle_t h, const char* what, const RaggedArgs& a, const TileList& tiles,
+               const RaggedTile& t, int bn, int64_t grid, int launches = 1)
 {
+    int i = 0;
+    while (&tiles[i] != &t) ++i;
+    const int bm = t.bm;
+    h->last_group = gemm_group_launch_t{bm, bn, nth_of_height(tiles, i), launches, 0, 0, 0};
     if (h->log)
         std::fprintf(stderr, "gemm: %s %dx%d rows=%d groups=%d M=%d N=%d K=%d grid=%lld\n", what, bm,
                      bn, a.rows, a.groups, a.M, a.N, a.K, (long long)grid);
@@ -110,14 +130,27 @@ void log_call(gemm_handle_t h, const char* what, const RaggedArgs& a, int bm, in
 
 extern "C" {
 
-gemm_status_t gemm_set_group_tile(gemm_handle_t h, int rows)
+gemm_status_t gemm_set_group_tile_nth(gemm_handle_t h, int rows, int nth)
 {
-    if (!h || rows < 0) return GEMM_ERR_INVALID_VALUE;
+    if (!h || rows < 0 || nth < 0) return GEMM_ERR_INVALID_VALUE;
     h->forced_rows = rows;
+    h->forced_nth = nth;
     return GEMM_OK;
 }
 
-int gemm_last_group_tile(gemm_handle_t h) { return h ? h->last_rows : -1; }
+gemm_status_t gemm_set_group_tile(gemm_handle_t h, int rows)
+{
+    return gemm_set_group_tile_nth(h, rows, 0);
+}
+
+int gemm_last_group_tile(gemm_handle_t h) { return h ? h->last_group.rows : -1; }
+
+gemm_status_t gemm_last_group_launch(gemm_handle_t h, gemm_group_launch_t* out)
+{
+    if (!h || !out) return GEMM_ERR_INVALID_VALUE;
+    *out = h->last_group;
+    return GEMM_OK;
+}
 
 gemm_status_t gemm_run_grouped(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_t N, int64_t K,
                                float alpha, const void* A, int64_t lda, const void* B, int64_t ldb,
@@ -135,7 +168,7 @@ gemm_status_t gemm_run_grouped(gemm_handle_t h, gemm_op_t transB, int64_t M, int
     if (lda < std::max(one, K) || ldb < std::max(one, b_kc ? K : N) || ldd < std::max(one, N) ||
         (beta != 0.0f && ldc < std::max(one, N)))
         return GEMM_ERR_INVALID_VALUE;
-    h->last_rows = 0;
+    h->last_group = {};
     if (M == 0 || N == 0 || groups->groups == 0) return GEMM_OK;
     const bool reads_ab = K > 0 && alpha != 0.0f;
     if (!groups->offsets || !D || (beta != 0.0f && !C) || (reads_ab && (!A || !B)))
@@ -179,7 +212,7 @@ gemm_status_t gemm_run_grouped(gemm_handle_t h, gemm_op_t transB, int64_t M, int
     auto grid_of = [&](const RaggedTile& x) {
         return (M + busy * (x.bm - 1)) / x.bm * ceil_div(N, x.bn[b_kc]);
     };
-    const RaggedTile& t = pick_tile(tiles, h->forced_rows, b_kc, K, bytes, [&](const RaggedTile& x) {
+    const RaggedTile& t = pick_tile(h, tiles, b_kc, K, bytes, [&](const RaggedTile& x) {
         return ceil_div(N, x.bn[b_kc]) *
                (busy > 1 ? row_tiles((double)busy, (double)M / busy, x.bm) : (double)ceil_div(M, x.bm));
     }, grid_of);
@@ -195,8 +228,7 @@ gemm_status_t gemm_run_grouped(gemm_handle_t h, gemm_op_t transB, int64_t M, int
     if (h->fail_launch) return GEMM_ERR_HIP;
     if (t.fn[b_kc][dtype == GEMM_DTYPE_BF16_BF16](a, (int)grid, stream) != hipSuccess)
         return GEMM_ERR_HIP;
-    h->last_rows = t.bm;
-    log_call(h, "grouped", a, t.bm, bn, grid);
+    note_call(h, "grouped", a, tiles, t, bn, grid);
     return GEMM_OK;
 }
 
@@ -215,7 +247,7 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_handle_t h, int64_t M, int64_t N, int6
     if (lda < std::max(one, M) || ldb < std::max(one, N) || ldd < std::max(one, N) ||
         (beta != 0.0f && ldc < std::max(one, N)))
         return GEMM_ERR_INVALID_VALUE;
-    h->last_rows = 0;
+    h->last_group = {};
     if (M == 0 || N == 0 || G == 0) return GEMM_OK;
     const bool reads_ab = rows > 0 && alpha != 0.0f;
     if (!groups->offsets || !D || (beta != 0.0f && !C) || (reads_ab && (!A || !B)))
@@ -265,7 +297,7 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_handle_t h, int64_t M, int64_t N, int6
     auto tiles_of = [&](const RaggedTile& x) { return G * ceil_div(M, x.bm) * ceil_div(N, x.bn[0]); };
     // (every way of dealing them: a slice may round up to a tile more per XCD)
     auto most = [&](const RaggedTile& x) { return tiles_of(x) + DEAL_XCDS * G; };
-    const RaggedTile& t = pick_tile(tiles, h->forced_rows, false, rows / G, 0.0, tiles_of, most);
+    const RaggedTile& t = pick_tile(h, tiles, false, rows / G, 0.0, tiles_of, most);
     const int bn = t.bn[0];
     // offsets of one K-step, or of one batch of them (the kernels base each anew)
     const int64_t ks = t.stream ? 4 * t.bk : t.bk;
@@ -283,8 +315,7 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_handle_t h, int64_t M, int64_t N, int6
     if (h->fail_launch) return GEMM_ERR_HIP;
     if (t.fn[0][dtype == GEMM_DTYPE_BF16_BF16](a, (int)grid, stream) != hipSuccess)
         return GEMM_ERR_HIP;
-    h->last_rows = t.bm;
-    log_call(h, "grouped wgrad", a, t.bm, bn, grid);
+    note_call(h, "grouped wgrad", a, tiles, t, bn, grid);
     return GEMM_OK;
 }
 
@@ -317,7 +348,7 @@ gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_
     const int64_t es = dtype == GEMM_DTYPE_F32 ? 4 : 2, eo = dtype == GEMM_DTYPE_BF16_BF16 ? 2 : 4;
     const bool b_kc = transB == GEMM_OP_T;
     const bool down_kc = lora->trans_down == GEMM_OP_T, up_kc = lora->trans_up == GEMM_OP_T;
-    h->last_rows = 0;
+    h->last_group = {};
     // without an adapter, or with nothing to multiply, the call is gemm_run on a
     // handle of its own: h's forced variant and stream-K workspace, which other
     // streams may be using, have no part in it
@@ -382,7 +413,7 @@ gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_
     const TileList tiles = dtype == GEMM_DTYPE_F32 ? tile_list(ragged_lora_f32, stream_lora_f32)
                                                    : tile_list(ragged_lora_bf16, stream_lora_bf16);
     auto grid_of = [&](const RaggedTile& x) { return ceil_div(M, x.bm) * ceil_div(N, x.bn[b_kc]); };
-    const RaggedTile& t = pick_tile(tiles, h->forced_rows, b_kc, K, bytes, grid_of, grid_of);
+    const RaggedTile& t = pick_tile(h, tiles, b_kc, K, bytes, grid_of, grid_of);
     const int bn = t.bn[b_kc];
     const int64_t kk = K + t.bk;
     if (!panel_fits(t.bm - 1, lda, kk, es) ||
@@ -407,8 +438,7 @@ gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_
         if (h->fail_launch) return GEMM_ERR_HIP;
         if (ot.fn[b_kc][dtype == GEMM_DTYPE_BF16_BF16](a, (int)grid, stream) != hipSuccess)
             return GEMM_ERR_HIP;
-        h->last_rows = ot.bm;
-        log_call(h, "lora in one launch", a, ot.bm, bn, grid);
+        note_call(h, "lora in one launch", a, tiles, t, bn, grid);
         return GEMM_OK;
     }
     // the first product: blocks of as many rows as a segment has on average,
@@ -451,8 +481,10 @@ gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_
     if (ft.fn[down_kc][0](f, (int)blocks, stream) != hipSuccess ||
         t.fn[b_kc][dtype == GEMM_DTYPE_BF16_BF16](a, (int)grid, stream) != hipSuccess)
         return GEMM_ERR_HIP;
-    h->last_rows = t.bm;
-    log_call(h, "lora", a, t.bm, bn, grid);
+    note_call(h, "lora", a, tiles, t, bn, grid, 2);
+    h->last_group.first_rows = ft.bm;
+    h->last_group.first_columns = ft.bn[down_kc];
+    h->last_group.first_slices = f.splits;
     return GEMM_OK;
 }
 

@@ -441,15 +441,29 @@ gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_
                             gemm_dtype_t dtype, const gemm_lora_t* lora, void* workspace,
                             size_t workspace_bytes, hipStream_t stream);
 
-/* Rows of the output tile that h's later calls of the three functions above
- * take: the tallest there is up to `rows`, else the smallest (0, the default:
- * chosen from the call's sizes).  Tests use this to run every tile.
- * GEMM_ERR_INVALID_VALUE for a negative value or a NULL handle. */
+/* Output tile that h's later calls of the three functions above take: of the
+ * tallest height there is up to `rows`, else the smallest, the first tile
+ * (gemm_set_group_tile) or the nth from 0, or the last of that height
+ * (gemm_set_group_tile_nth).  rows == 0, the default: chosen from the call's
+ * sizes.  Tests use this to run every tile.  GEMM_ERR_INVALID_VALUE for a
+ * negative value or a NULL handle. */
 gemm_status_t gemm_set_group_tile(gemm_handle_t h, int rows);
+gemm_status_t gemm_set_group_tile_nth(gemm_handle_t h, int rows, int nth);
 
-/* Rows of the output tile of h's last such call (0: none launched; -1 for a
- * NULL handle). */
+/* Rows of the output tile of h's last such call (0: none launched, or the dense
+ * product; -1 for a NULL handle). */
 int gemm_last_group_tile(gemm_handle_t h);
+
+/* What that call launched (all zero where gemm_last_group_tile is 0):
+ * GEMM_ERR_INVALID_VALUE for a NULL pointer. */
+typedef struct {
+    int rows, columns; /* the output tile */
+    int nth;           /* its number among the call's tiles of that height */
+    int launches;
+    int first_rows, first_columns, first_slices; /* gemm_run_lora in two launches: the tile
+                                                  * of A op(down), and slices of K (else 0) */
+} gemm_group_launch_t;
+gemm_status_t gemm_last_group_launch(gemm_handle_t h, gemm_group_launch_t* out);
 
 #ifdef __cplusplus
 }
