@@ -347,8 +347,9 @@ gemm_status_t gemm_set_stream_k_poll_limit(gemm_handle_t h, int polls);
  * later values.  Groups may be empty, and rows before offsets[0] or from
  * offsets[groups] on belong to no group.  Entries outside [0, M] are taken as
  * the nearest bound and a negative length as an empty group: no value leads
- * outside the operands (with offsets that decrease, rows that groups share
- * hold one group's result, and where they share many some stay unwritten).
+ * outside the operands.  (With offsets that decrease, elements of rows that
+ * groups share hold one group's result, or with C == D one added to another's,
+ * and where they share many rows some stay unwritten.)
  * At most 65536 groups, M, N, K and rows of 2^31 - 513, ranks of half that, and
  * output tiles for 2^32 threads (GEMM_ERR_NOT_SUPPORTED beyond).
  * scales, when not NULL, holds one fp32 factor per group on the device, and
@@ -394,7 +395,9 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_handle_t h, int64_t M, int64_t N, int6
 /* Low-rank adapters of many requests beside a shared product:
  *     D = alpha (A op(B) + s_a (A op(down_a)) op(up_a)) + beta C
  * where a is the adapter of the row's segment.  Segment s holds rows
- * offsets[s] .. offsets[s+1]-1 (device, as for gemm_groups_t) and uses adapter
+ * offsets[s] .. offsets[s+1]-1 (device, as for gemm_groups_t, but with offsets
+ * that decrease the low-rank part of rows in segments is undefined: one
+ * adapter's product with another's, or what the workspace held) and uses adapter
  * ids[s] (device; NULL: adapter s).  A row in no segment, or in one whose id
  * is negative or >= adapters, gets the shared product alone, whatever the
  * adapters hold.  op(down_a) is K x rank: stored rank x K with trans_down ==
@@ -411,8 +414,12 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_handle_t h, int64_t M, int64_t N, int6
  * hi: 2 rank columns, whose two products add up) they cost nothing to speak of.
  *
  * With bf16 operands the rows' products with down may enter the second product
- * as a sum of two bf16 terms (16 bits); an infinity in up can then come out as
- * NaN, in the rows of that adapter only.
+ * as a sum of two bf16 terms (16 bits), by the tile that the call's sizes choose;
+ * an infinity in up can then come out as NaN, in the rows of that adapter only,
+ * and a product with down above bf16's largest value, 3.39e38, counts as infinite.
+ *
+ * Without an adapter (rank, adapters or segments 0) the call is gemm_run's on a
+ * handle without workspace or forced variant.
  *
  * The rows' products with down are formed in fp32 in `workspace`, device
  * memory of at least gemm_lora_workspace_bytes(M, rank) bytes that is 256-byte

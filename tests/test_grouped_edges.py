@@ -205,6 +205,41 @@ def test_adapters_gradients_round_once(rank, dtype):
         check(dup[a], y.T @ t, y.abs().T @ t_abs, terms, "up", t_rel, y.abs().T @ t.abs())
 
 
+@gpu
+@pytest.mark.parametrize("tile", [0, 16, 64, 128, 256])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_offsets_past_the_rows_are_clamped(dtype, tile):
+    """The adapted product and the matrices' gradients with offsets below 0 and past
+    the rows; with offsets that decrease, nothing outside D is written."""
+    require_gpu()
+    announce("clamped offsets", dtype, tile)
+    ti, to = TYPES[dtype]
+    M, K, N, R = 50, 64, 80, 8
+    A, B = draw((M, K), 1, ti), draw((K, N), 2, ti)
+    dn, up = draw((3, R, K), 3, ti), draw((3, N, R), 4, ti)
+    val, den, low = lora_reference(A, B, None, [20, 0, 30], 0, [0, 1, 2], dn, up, "N", 1.0, 0.0, None)
+    h = handle(tile)
+    try:
+        ws = g().lora_workspace(M, R)
+        for off in ([-9, 20, 20, 4000], [40, -3, 35, 10]):
+            D = torch.full((M + 4, N), 7.0, dtype=to, device="cuda")
+            g().run_lora(h, A.cuda(), B.cuda(), D[2:M + 2], int32(off), dn.cuda(), up.cuda(), ws)
+            got = D.cpu()
+            assert torch.all(got[:2] == 7.0) and torch.all(got[M + 2:] == 7.0)
+            if off[0] < 0:
+                check(got[2:M + 2], val, den, 2 * K + R, "clamped", 2.0 ** -17, low)
+        Y = draw((M, N), 5, ti)
+        D = torch.full((5, K, N), 7.0, dtype=to, device="cuda")
+        g().run_grouped_wgrad(h, A.cuda(), Y.cuda(), D[1:4], int32([-9, 20, 20, 4000]))
+        got = D.cpu()
+        assert torch.all(got[0] == 7.0) and torch.all(got[4] == 7.0)
+        for i, r in enumerate((slice(0, 20), slice(0, 0), slice(20, 50))):
+            a, y = A[r].double(), Y[r].double()
+            check(got[1 + i], a.T @ y, a.abs().T @ y.abs(), 30, "gradient")
+    finally:
+        g().gemm_destroy(h)
+
+
 # ---------------------------------------------------------------- limits (no GPU)
 @pytest.fixture
 def unlaunched(monkeypatch):
