@@ -512,8 +512,10 @@ def _device_vector(t, dtype, length, device, what):
 
 
 def _device_of(D, *tensors):
-    """D's device index (-1 for the host), which every tensor has to share."""
+    """D's device index, which every tensor has to share."""
     device = D.get_device()
+    if device < 0:
+        raise ValueError("the tensors must be on a GPU")
     for t in tensors:
         if t is not None and t.get_device() != device:
             raise ValueError("every tensor must be on D's device")
@@ -524,8 +526,6 @@ def _stream_on(device):
     """The current stream of a device, as an integer."""
     import torch
 
-    if device < 0:
-        raise ValueError("the tensors must be on a GPU")
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without a Stream object
     return raw(device) if raw else torch.cuda.current_stream(device).cuda_stream
 

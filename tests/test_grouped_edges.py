@@ -282,3 +282,17 @@ def test_grids_of_2_32_threads_are_refused(unlaunched):
     assert raw_grouped(h, **fits) == p.GEMM_ERR_NOT_SUPPORTED
     assert raw_lora(h, M=2 ** 30, N=2 ** 10, ldb=2 ** 10, ldd=2 ** 10, ld_up=3, stride_up=2 ** 12,
                     bytes=1 << 62) == p.GEMM_ERR_NOT_SUPPORTED
+
+
+def test_host_tensors_are_refused_on_a_given_stream(unlaunched):
+    """... as on the current one: no pointer of host memory reaches a launch."""
+    h, A, B, D = unlaunched, torch.zeros(4, 6), torch.zeros(2, 6, 5), torch.zeros(4, 5)
+    off = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="GPU"):
+        g().run_grouped(h, A, B, D, off, stream=0)
+    with pytest.raises(ValueError, match="GPU"):
+        g().run_grouped_wgrad(h, A, D, torch.zeros(2, 6, 5), off, stream=0)
+    ws = torch.zeros(65536, dtype=torch.uint8)
+    ws = ws[-ws.data_ptr() % 256:]
+    with pytest.raises(ValueError, match="GPU"):
+        g().run_lora(h, A, B[0], D, off, torch.zeros(2, 3, 6), torch.zeros(2, 5, 3), ws, stream=0)
