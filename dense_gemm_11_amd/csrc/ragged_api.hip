@@ -424,10 +424,16 @@ gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_
     a.group_m = std::min(a.tiles_m, 4);
     const int64_t grid = grid_of(t);
     if (!grid_fits(grid, t.threads)) return GEMM_ERR_NOT_SUPPORTED;
-    // one tile of rows and little to do for T: both products in one launch
-    const int64_t segs = std::min<int64_t>(lora->segments, M);
-    if (t.stream && t.bm == 16 && M <= 16 && down_kc && R <= LORA_ONE_RANK &&
-        segs * ceil_div(R, 16) <= 2 && panel_fits(15, lora->ld_down, kk, es)) {
+    // One tile of rows and little to do for T: both products in one launch, whose
+    // workgroups each go through all of down, a block of 16 ranks of an adapter
+    // at a time, after W's.  Against two launches (1 to 16 rows, both layouts of
+    // B): two blocks take 11.2 us for 14.5 at K, N = 1024, 11.8 for 16.3 at 2048,
+    // 17.8 for 18.9 at 4096 and 35.5 for 35.5 at K = 4096, N = 14336, but 24.6 for
+    // 20.1 at K = 8192, N = 2048 and 58.7 for 51.9 at N = 14336; one block takes
+    // 17.8 for 19.6 and 51.4 for 50.9 there.
+    const int64_t segs = std::min<int64_t>(lora->segments, M), t_blocks = segs * ceil_div(R, 16);
+    if (t.stream && t.bm == 16 && M <= 16 && down_kc && R <= LORA_ONE_RANK && t_blocks <= 2 &&
+        t_blocks * K <= 8192 && panel_fits(15, lora->ld_down, kk, es)) {
         int n_one = 0;
         const RaggedTile* one_launch =
             (dtype == GEMM_DTYPE_F32 ? stream_lora_one_f32 : stream_lora_one_bf16)(&n_one);

@@ -225,6 +225,23 @@ def test_few_rows_take_one_launch_or_two(sizes, of, R, down, launches, dtype, tr
         g().gemm_destroy(h)
 
 
+@gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("sizes,of,R,K,launches", [
+    ([14], [1], 32, 4096, 1), ([14], [1], 32, 4100, 2), ([7, 7], [1, 0], 8, 4096, 1),
+    ([7, 7], [1, 0], 8, 8192, 2), ([14], [1], 16, 8192, 1), ([14], [1], 16, 8200, 2)])
+def test_one_launch_by_the_length_of_down(sizes, of, R, K, launches, dtype):
+    """Two blocks of ranks up to K = 4096, one up to 8192."""
+    require_gpu()
+    announce("length of down", sizes, R, K, dtype)
+    h = forced(16, 0)
+    try:
+        adapted(h, dtype, "T", sizes, of, 2, R, K, 70, 0)
+        ran(h, 16, 64, 0, launches)
+    finally:
+        g().gemm_destroy(h)
+
+
 def test_forced_tiles_are_checked():
     p = g()
     h = p.gemm_create()
