@@ -11,9 +11,11 @@
 // adapter, T and up are more of the product's K instead: T's terms and up_a
 // go through LDS behind the last step of X and W.
 // The second product costs 2 M R N operations beside 2 M K N.  T stays fp32
-// in memory; as bf16 MFMA operands it goes in as two terms, T = hi + lo with
-// lo = bf16(T - hi), which keeps 16 of its bits: as one bf16 term its rounding
-// (2^-9 of the low-rank part) would be as large as that of D itself.
+// in memory; as bf16 MFMA operands it goes in as a sum of bf16 terms (each of
+// what the ones before leave), two where D is bf16 and three where D is fp32.
+// One term's rounding, up to 2^-8 of the low-rank part, would be as large as that
+// of a bf16 D itself; two keep 16 bits, which an fp32 D shows (487 rows of
+// 4608x1152, rank 4: 1.3e-6 off the 64-bit result, 0.6e-6 with fp32 T), three 24.
 #pragma once
 
 #include "common.hpp"
@@ -42,47 +44,60 @@ __device__ __forceinline__ u32x4 clamped_chunk(const T* x, int64_t ks, int k, in
     return pack_chunk<T>(e);
 }
 
-// fp32 values as MFMA operand terms: bf16 as hi + lo, fp32 as itself.  An
-// infinite or NaN hi takes a zero lo, so an infinity stays one.
-__device__ __forceinline__ void split_terms(const float (&t)[8], u32x4& hi, u32x4& lo)
+// Terms of T that make up one MFMA operand of KIND's type beside a D of bf16
+// (OUT_BF16) or fp32.
+template <typename T, bool OUT_BF16>
+constexpr int LORA_TERMS = sizeof(T) == 4 ? 1 : OUT_BF16 ? 2 : 3;
+
+// fp32 values as MFMA operand terms: bf16 as a sum of N, fp32 as itself.  An
+// infinite or NaN term takes zeros behind it, so an infinity stays one.
+template <int N>
+__device__ __forceinline__ void split_terms(const float (&t)[8], u32x4 (&v)[N])
 {
-    bf16x8 h, l;
+    float rest[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        h[e] = (__bf16)t[e];
-        const float hf = (float)h[e];
-        l[e] = (__bf16)(fabsf(hf) <= 3.402823466e38f ? t[e] - hf : 0.0f);
+    for (int e = 0; e < 8; ++e) rest[e] = t[e];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        bf16x8 h;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            h[e] = (__bf16)rest[e];
+            const float hf = (float)h[e];
+            rest[e] = fabsf(hf) <= 3.402823466e38f ? rest[e] - hf : 0.0f;
+        }
+        v[n] = __builtin_bit_cast(u32x4, h);
     }
-    hi = __builtin_bit_cast(u32x4, h);
-    lo = __builtin_bit_cast(u32x4, l);
 }
-__device__ __forceinline__ void split_terms(const float (&t)[4], u32x4& hi, u32x4&)
+__device__ __forceinline__ void split_terms(const float (&t)[4], u32x4 (&v)[1])
 {
-    hi = u32x4{__float_as_uint(t[0]), __float_as_uint(t[1]), __float_as_uint(t[2]),
-               __float_as_uint(t[3])};
+    v[0] = u32x4{__float_as_uint(t[0]), __float_as_uint(t[1]), __float_as_uint(t[2]),
+                 __float_as_uint(t[3])};
 }
 
-// T as bf16 operand terms in memory: row r holds hi in columns 0 .. rank_pad-1
-// and lo behind it.  Four columns of it.
+// T as bf16 operand terms in memory: row r holds p.terms (2 or 3) runs of
+// rank_pad columns, one per term.  Four columns of it.
 __device__ __forceinline__ void store_terms(const RaggedArgs& p, int64_t row, int col, const f32x4& t)
 {
-    float e[8] = {t[0], t[1], t[2], t[3]};
-    u32x4 hi, lo;
-    split_terms(e, hi, lo);
-    uint16_t* d = p.t_terms + row * 2 * p.rank_pad + col;
-    *reinterpret_cast<uint2*>(d) = uint2{hi[0], hi[1]};
-    *reinterpret_cast<uint2*>(d + p.rank_pad) = uint2{lo[0], lo[1]};
+    const float e[8] = {t[0], t[1], t[2], t[3]};
+    u32x4 v[3];
+    split_terms(e, v);
+    uint16_t* d = p.t_terms + row * p.terms * p.rank_pad + col;
+#pragma unroll
+    for (int n = 0; n < 3; ++n)
+        if (n < p.terms) *reinterpret_cast<uint2*>(d + n * p.rank_pad) = uint2{v[n][0], v[n][1]};
 }
 
 // ... one column.
 __device__ __forceinline__ void store_term(const RaggedArgs& p, int64_t row, int col, float t)
 {
     const float e[8] = {t};
-    u32x4 hi, lo;
-    split_terms(e, hi, lo);
-    uint16_t* d = p.t_terms + row * 2 * p.rank_pad + col;
-    d[0] = (uint16_t)hi[0];
-    d[p.rank_pad] = (uint16_t)lo[0];
+    u32x4 v[3];
+    split_terms(e, v);
+    uint16_t* d = p.t_terms + row * p.terms * p.rank_pad + col;
+#pragma unroll
+    for (int n = 0; n < 3; ++n)
+        if (n < p.terms) d[n * p.rank_pad] = (uint16_t)v[n][0];
 }
 
 // adapter[r] = the adapter of row m0 + r for the BM rows of a tile, or -1;
@@ -237,7 +252,7 @@ __device__ __forceinline__ f32x4 lora_row(const RaggedArgs& p, int col, int a, b
 // (infinities, NaN) reaches no other row.  The loads are free of branches
 // (clamped and zeroed instead), and the first adapter's are issued ahead of
 // T's, so a fragment of one adapter waits for memory once per 32 ranks.
-template <int KIND, int NQ, int VG>
+template <int KIND, bool OUT_BF16, int NQ, int VG>
 __device__ __forceinline__ void lora_fragment(const RaggedArgs& p, const int* adapter, int m_tile,
                                               int row0, int col0, int lane, f32x4 (&sum)[NQ][VG])
 {
@@ -245,6 +260,7 @@ __device__ __forceinline__ void lora_fragment(const RaggedArgs& p, const int* ad
     using Acc = typename AccType<KIND>::type;
     constexpr int FM = MfmaShape<KIND>::FM, VEC = 16 / sizeof(T), KSTEP = 64 / FM * VEC;
     constexpr int NK = 2;  // fragment steps of rank at once
+    constexpr int TERMS = LORA_TERMS<T, OUT_BF16>;
     static_assert(FM == 32 && VG == 4, "accumulator layout");
     int row = row0 + lane % FM;
     const int mine = row < p.M ? adapter[row - m_tile] : -1;
@@ -284,7 +300,7 @@ __device__ __forceinline__ void lora_fragment(const RaggedArgs& p, const int* ad
         int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(some));
         load_up(a);
         // the rows' T as operand terms
-        u32x4 hi[NK], lo[NK];
+        u32x4 terms[NK][TERMS];
 #pragma unroll
         for (int kk = 0; kk < NK; ++kk) {
             const int k = r0 + kk * KSTEP + kl;
@@ -293,7 +309,7 @@ __device__ __forceinline__ void lora_fragment(const RaggedArgs& p, const int* ad
             float t[VEC];
 #pragma unroll
             for (int e = 0; e < VEC; ++e) t[e] = k < p.rank_pad ? q[e / 4][e % 4] : 0.0f;
-            split_terms(t, hi[kk], lo[kk]);
+            split_terms(t, terms[kk]);
         }
         for (uint64_t left = some;;) {
             left &= ~__ballot(mine == a);
@@ -301,10 +317,9 @@ __device__ __forceinline__ void lora_fragment(const RaggedArgs& p, const int* ad
             for (int q = 0; q < NQ; ++q) {
                 Acc v = {};
 #pragma unroll
-                for (int kk = 0; kk < NK; ++kk) {
-                    mfma_step<KIND>(b[q][kk], hi[kk], v);
-                    if constexpr (sizeof(T) == 2) mfma_step<KIND>(b[q][kk], lo[kk], v);
-                }
+                for (int kk = 0; kk < NK; ++kk)
+#pragma unroll
+                    for (int n = 0; n < TERMS; ++n) mfma_step<KIND>(b[q][kk], terms[kk][n], v);
 #pragma unroll
                 for (int e = 0; e < 4 * VG; ++e) sum[q][e / 4][e % 4] += mine == a ? v[e] : 0.0f;
             }

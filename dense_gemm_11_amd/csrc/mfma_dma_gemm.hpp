@@ -1022,10 +1022,11 @@ __device__ __forceinline__ void dma_gemm_body(Args p)
             if (kt + 5 < nk) step(I5{}, kt + 5);
     }
     // RAG_LORA, a tile of one adapter: BK ranks at a time of T (its terms in
-    // slots 0 and 1) and up, through LDS.  Not in the pipeline above: there the
+    // slots 0, 1 and, for an fp32 D, 2) and up, through LDS.  Not in the pipeline above: there the
     // copies' registers would meet the fragments'.
     if constexpr (RAG == RAG_LORA) {
-        constexpr int TERMS = Cfg::ES == 2 ? 2 : 1;
+        constexpr int TERMS = LORA_TERMS<T, OUT_BF16>;
+        static_assert(TERMS <= S && TERMS <= P, "a slot for each term");
         const int ldt = TERMS * p.rank_pad;
         const T* t = (Cfg::ES == 2 ? reinterpret_cast<const T*>(p.t_terms)
                                    : reinterpret_cast<const T*>(p.t)) + (int64_t)m0 * ldt;
@@ -1043,8 +1044,8 @@ __device__ __forceinline__ void dma_gemm_body(Args p)
             __syncthreads();  // every wave is done reading the slots
             static_for<TERMS>([&](auto u_c) __attribute__((always_inline)) {
                 constexpr int u = decltype(u_c)::value;
-                oa.put(va[u], a_lds(u), tid, PA ? u : 0);
-                ob.put(vb, b_lds(u), tid, PB ? u : 0);
+                oa.put(va[u], a_lds(u), tid, PA ? u & 1 : 0);
+                ob.put(vb, b_lds(u), tid, PB ? u & 1 : 0);
             });
             __syncthreads();
             oa.refresh();
@@ -1207,7 +1208,7 @@ __device__ __forceinline__ void dma_gemm_body(Args p)
         }
         if constexpr (RAG == RAG_LORA)
             if (tile_a == TILE_MIXED)
-                lora_fragment<Cfg::KIND>(p, adapter, m0, m0 + wave_m0 + o * FM,
+                lora_fragment<Cfg::KIND, OUT_BF16>(p, adapter, m0, m0 + wave_m0 + o * FM,
                                          n0 + wave_n0 + qh * DC, lane, sum);
         if constexpr (SK) {
             for (int64_t c = c0; c < c1; ++c) {

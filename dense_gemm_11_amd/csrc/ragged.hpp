@@ -44,7 +44,8 @@ struct RaggedArgs : GemmArgs {
     int64_t ld_down, stride_down;
     int up_kc;               // up stored N x rank (rank contiguous)
     int k_slice;             // RAG_SHRINK: K of each of the `splits` slices
-    uint16_t* t_terms;       // bf16 operands: T as two terms (lora.hpp), or null
+    uint16_t* t_terms;       // bf16 operands: T as `terms` terms (lora.hpp), or null
+    int terms;
 };
 
 // First row and length of group g.

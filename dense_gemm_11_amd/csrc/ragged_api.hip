@@ -324,9 +324,10 @@ size_t gemm_lora_workspace_bytes(int64_t M, int rank)
     using namespace dg;
     if (M <= 0 || rank <= 0) return 0;
     // rows of T's partial sums: at most 4 slices, and at most ceil(8192 / M)
-    // of them; or T and its bf16 terms (gemm_run_lora); does not decrease with M
+    // of them; or T and its bf16 terms, three of half the size (gemm_run_lora);
+    // does not decrease with M
     const int64_t pad = ceil_div(rank, LORA_PAD) * LORA_PAD;
-    return (size_t)(std::max<int64_t>(2 * M, std::min<int64_t>(4 * M, 8192 + M)) * pad) *
+    return (size_t)(std::max<int64_t>((5 * M + 1) / 2, std::min<int64_t>(4 * M, 8192 + M)) * pad) *
            sizeof(float);
 }
 
@@ -476,6 +477,7 @@ gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_
                                         K / (8 * 4 * ft.bk)});
     // the direct-to-LDS tiles want T whole, for their K-steps
     splits = t.stream ? std::max<int64_t>(1, splits) : 1;
+    a.terms = f.terms = dtype == GEMM_DTYPE_BF16_BF16 ? 2 : 3;
     if (!t.stream && dtype != GEMM_DTYPE_F32)
         a.t_terms = f.t_terms = reinterpret_cast<uint16_t*>(static_cast<float*>(ws) + M * a.rank_pad);
     f.k_slice = (int)(ceil_div(ceil_div(K, splits), ft.bk) * ft.bk);

@@ -414,9 +414,10 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_handle_t h, int64_t M, int64_t N, int6
  * hi: 2 rank columns, whose two products add up) they cost nothing to speak of.
  *
  * With bf16 operands the rows' products with down may enter the second product
- * as a sum of two bf16 terms (16 bits), by the tile that the call's sizes choose;
- * an infinity in up can then come out as NaN, in the rows of that adapter only,
- * and a product with down above bf16's largest value, 3.39e38, counts as infinite.
+ * as a sum of bf16 terms, by the tile that the call's sizes choose: two (16 bits)
+ * where D is bf16, three (24 bits) where it is fp32.  An infinity in up can then
+ * come out as NaN, in the rows of that adapter only, and a product with down
+ * above bf16's largest value, 3.39e38, counts as infinite.
  *
  * Without an adapter (rank, adapters or segments 0) the call is gemm_run's on a
  * handle without workspace or forced variant.

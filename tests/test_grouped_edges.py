@@ -172,6 +172,43 @@ def test_lora_without_adapters_is_planned_without_the_handle(kw, monkeypatch):
 
 
 @gpu
+@pytest.mark.parametrize("tile", [0, 16, 32, 64, 128, 192, 256])
+@pytest.mark.parametrize("up", ["N", "T"])
+@pytest.mark.parametrize("trans", ["N", "T"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_lora_keeps_24_bits_of_t_beside_an_fp32_d(dtype, trans, up, tile):
+    """Whole numbers of up to 21 bits in T, each picked out by a 1 in up: every sum is
+    exact in fp32, so D has to equal them, on tiles of one adapter and mixed ones."""
+    require_gpu()
+    announce("bits of T", dtype, trans, up, tile)
+    ti, R, K, N = TYPES[dtype][0], 24, 64, 136
+    sizes, ids = [300, 5, 70, 30], [1, 0, -1, 0]
+    M = sum(sizes)
+    gen = torch.Generator().manual_seed(1)
+    A = torch.randint(1, 256, (M, K), generator=gen).to(ti)
+    dn = torch.randint(1, 256, (2, R, K), generator=gen).to(ti)
+    u = torch.zeros(2, N, R, dtype=ti)
+    u[:, torch.arange(N), torch.arange(N) % R] = 1
+    want, at = torch.zeros(M, N, dtype=torch.float64), bounds_of(sizes)
+    for i, a in enumerate(ids):
+        if a >= 0:
+            want[at[i]:at[i + 1]] = (A[at[i]:at[i + 1]].double() @ dn[a].double().T)[:, torch.arange(N) % R]
+    assert want.max() < 2 ** 22 and (want.long() & 1).any()
+    h = handle(tile)
+    try:
+        D = torch.full((M, N), NAN, device="cuda")
+        B = torch.zeros(*((K, N) if trans == "N" else (N, K)), dtype=ti, device="cuda")
+        ws = g().lora_workspace(M, R)
+        ws.fill_(255)
+        u_ = u if up == "T" else u.transpose(1, 2).contiguous()
+        g().run_lora(h, A.cuda(), B, D, int32(at), dn.cuda(), u_.cuda(), ws, ids=int32(ids), transB=trans,
+                     transUp=up)
+        assert torch.equal(D.cpu().double(), want)
+    finally:
+        g().gemm_destroy(h)
+
+
+@gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "bf16_f32"])
 @pytest.mark.parametrize("rank", [8, 33, 64])
 def test_adapters_gradients_round_once(rank, dtype):
