@@ -7,8 +7,8 @@
 //    the waves splitting K into eight runs, so even a call of a few tiles has
 //    every wave of a compute unit loading;
 //  * operands go from memory straight into registers, four fragment steps of
-//    K at a time and, where the registers hold them, two such batches in flight; nothing is staged, so no
-//    barrier is met until the waves' sums are added;
+//    K at a time and, where the registers hold them, two such batches in flight;
+//    nothing is staged, so no barrier is met until the waves' sums are added;
 //  * the memory pipeline looks up the lines of four consecutive lanes at a
 //    time, so a k-contiguous operand is not read in the MFMA's lane order (16
 //    rows side by side: a line per lane; 64 rows of a 4096x4096 product took
@@ -32,8 +32,9 @@
 // blockIdx.y takes a slice of K each, whose sums go to a part of T of their
 // own.  RAG_LORA_ONE is RAG_LORA that forms its rows' T itself: every
 // workgroup reads the adapters' down again (from L2), which for one tile of
-// rows and one or two adapters costs less than a launch and T's way through
-// memory (one token, 2048x2048, rank 8: 12.6 -> 10.31 us).
+// rows, one or two blocks of 16 ranks and a K that is not too long costs less
+// than a launch and T's way through memory (one token, 2048x2048, rank 8: 12.6 ->
+// 10.31 us).
 #pragma once
 
 #include "lora.hpp"
