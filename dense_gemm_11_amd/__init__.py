@@ -612,7 +612,8 @@ def lora_workspace(rows: int, rank: int, device=None):
     import torch
 
     need = gemm_lora_workspace_bytes(rows, rank)
-    return torch.empty(max(need, 256), dtype=torch.uint8, device=device or "cuda")
+    return torch.empty(max(need, 256), dtype=torch.uint8,
+                       device="cuda" if device is None else device)
 
 
 def run_lora(h, A, B, D, offsets, down, up, workspace, ids=None, scales=None, C=None, transB="N",

@@ -333,3 +333,12 @@ def test_host_tensors_are_refused_on_a_given_stream(unlaunched):
     ws = ws[-ws.data_ptr() % 256:]
     with pytest.raises(ValueError, match="GPU"):
         g().run_lora(h, A, B[0], D, off, torch.zeros(2, 3, 6), torch.zeros(2, 5, 3), ws, stream=0)
+
+
+@pytest.mark.parametrize("device,on", [(None, "cuda"), (0, 0), ("cuda:1", "cuda:1")])
+def test_workspace_is_on_the_device_asked_for(device, on, monkeypatch):
+    """Device 0 by its number is not the current device."""
+    asked = []
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: asked.append(kw["device"]))
+    g().lora_workspace(4, 8, device)
+    assert asked == [on]
