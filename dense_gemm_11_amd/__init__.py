@@ -39,6 +39,10 @@ GEMM_NO_ALLOC_SCRATCH_BYTES = 16640 + (16 << 20)
 GEMM_ACT_NONE = 0
 GEMM_ACT_RELU = 1
 GEMM_ACT_GELU = 2
+GEMM_ACT_SILU = 3        # gemm_run_grouped_act and its gradient only
+GEMM_ACT_GELU_TANH = 4   # ... likewise
+GEMM_SCORES_SOFTMAX = 0
+GEMM_SCORES_SIGMOID = 1
 
 # Every function declared in include/dense_gemm.h.
 EXPORTS = ("gemm_create", "gemm_destroy", "gemm_run", "gemm_status_string",
@@ -50,7 +54,10 @@ EXPORTS = ("gemm_create", "gemm_destroy", "gemm_run", "gemm_status_string",
            "gemm_set_stream_k_poll_limit", "gemm_run_no_alloc", "gemm_set_planning_model",
            "gemm_run_grouped", "gemm_run_grouped_wgrad", "gemm_run_lora",
            "gemm_lora_workspace_bytes", "gemm_set_group_tile", "gemm_last_group_tile",
-           "gemm_set_group_tile_nth", "gemm_last_group_launch")
+           "gemm_set_group_tile_nth", "gemm_last_group_launch", "gemm_run_grouped_act",
+           "gemm_act_grad_workspace_bytes", "gemm_run_grouped_act_grad",
+           "gemm_route_workspace_bytes", "gemm_route", "gemm_route_grad", "gemm_gather_rows",
+           "gemm_combine_rows", "gemm_combine_rows_grad")
 
 
 class GemmEpilogue(ctypes.Structure):
@@ -76,6 +83,20 @@ class GemmLora(ctypes.Structure):
                 ("down", ctypes.c_void_p), ("ld_down", ctypes.c_int64),
                 ("stride_down", ctypes.c_int64), ("trans_up", ctypes.c_int),
                 ("up", ctypes.c_void_p), ("ld_up", ctypes.c_int64), ("stride_up", ctypes.c_int64)]
+
+
+class GemmAct(ctypes.Structure):
+    """gemm_act_t: activation, gate, bias, kept Z and residual (0/None for none)."""
+    _fields_ = [("activation", ctypes.c_int), ("gated", ctypes.c_int), ("bias", ctypes.c_void_p),
+                ("stride_bias", ctypes.c_int64), ("Z", ctypes.c_void_p), ("ldz", ctypes.c_int64),
+                ("R", ctypes.c_void_p), ("ldr", ctypes.c_int64)]
+
+
+class GemmRouting(ctypes.Structure):
+    """gemm_routing_t: how a router's logits choose experts."""
+    _fields_ = [("experts", ctypes.c_int), ("top", ctypes.c_int), ("scores", ctypes.c_int),
+                ("groups", ctypes.c_int), ("top_groups", ctypes.c_int), ("group_top", ctypes.c_int),
+                ("bias", ctypes.c_void_p), ("renormalize", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
 class GemmGroupLaunch(ctypes.Structure):
@@ -182,6 +203,29 @@ def _load():
     lib.gemm_set_group_tile_nth.restype = i32
     lib.gemm_last_group_launch.argtypes = [vp, ctypes.POINTER(GemmGroupLaunch)]
     lib.gemm_last_group_launch.restype = i32
+    sz, groups, routing = ctypes.c_size_t, ctypes.POINTER(GemmGroups), ctypes.POINTER(GemmRouting)
+    lib.gemm_run_grouped_act.argtypes = [vp, i32, i64, i64, i64, f32, vp, i64, vp, i64, i64, vp, i64,
+                                         i32, groups, ctypes.POINTER(GemmAct), vp]
+    lib.gemm_run_grouped_act.restype = i32
+    lib.gemm_act_grad_workspace_bytes.argtypes = [i64, i64, i32]
+    lib.gemm_act_grad_workspace_bytes.restype = sz
+    lib.gemm_run_grouped_act_grad.argtypes = [vp, i64, i64, i32, i32, vp, i64, vp, i64, vp, i64, vp,
+                                              i64, vp, i32, groups, vp, sz, vp]
+    lib.gemm_run_grouped_act_grad.restype = i32
+    lib.gemm_route_workspace_bytes.argtypes = [i64, i32]
+    lib.gemm_route_workspace_bytes.restype = sz
+    lib.gemm_route.argtypes = [vp, i64, vp, i64, i32, routing, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.gemm_route.restype = i32
+    lib.gemm_route_grad.argtypes = [vp, i64, vp, i64, i32, routing, vp, vp, vp, i64, vp]
+    lib.gemm_route_grad.restype = i32
+    lib.gemm_gather_rows.argtypes = [vp, i64, i64, i32, vp, i64, i64, vp, vp, vp, i64, i32, vp]
+    lib.gemm_gather_rows.restype = i32
+    lib.gemm_combine_rows.argtypes = [vp, i64, i64, i32, vp, i64, i64, vp, vp, f32, vp, i64, vp, i64,
+                                      i32, vp]
+    lib.gemm_combine_rows.restype = i32
+    lib.gemm_combine_rows_grad.argtypes = [vp, i64, i64, i32, vp, i64, i64, vp, vp, vp, i64, vp, i64,
+                                           vp, i32, vp]
+    lib.gemm_combine_rows_grad.restype = i32
     return lib
 
 
@@ -358,6 +402,70 @@ def gemm_last_group_launch(h) -> GemmGroupLaunch:
     if s != GEMM_OK:
         raise GemmError(s, "gemm_last_group_launch")
     return out
+
+
+def gemm_run_grouped_act(h, transB, M, N, K, alpha, A, lda, B, ldb, strideB, D, ldd, dtype, groups,
+                         act, stream) -> int:
+    """Raw call: pointers and the stream are integers (0/None for NULL); groups
+    is a GemmGroups or None, act a GemmAct or None."""
+    return lib.gemm_run_grouped_act(h, transB, M, N, K, alpha, A, lda, B, ldb, strideB, D, ldd, dtype,
+                                    None if groups is None else ctypes.byref(groups),
+                                    None if act is None else ctypes.byref(act), stream)
+
+
+def gemm_act_grad_workspace_bytes(M: int, width: int, groups: int) -> int:
+    return lib.gemm_act_grad_workspace_bytes(M, width, groups)
+
+
+def gemm_run_grouped_act_grad(h, M, N, activation, gated, Z, ldz, dD, lddd, dZ, lddz, H, ldh, dbias,
+                              dtype, groups, workspace, workspace_bytes, stream) -> int:
+    """Raw call: pointers and the stream are integers (0/None for NULL); groups
+    is a GemmGroups or None."""
+    return lib.gemm_run_grouped_act_grad(h, M, N, activation, gated, Z, ldz, dD, lddd, dZ, lddz, H,
+                                         ldh, dbias, dtype,
+                                         None if groups is None else ctypes.byref(groups), workspace,
+                                         workspace_bytes, stream)
+
+
+def gemm_route_workspace_bytes(tokens: int, experts: int) -> int:
+    return lib.gemm_route_workspace_bytes(tokens, experts)
+
+
+def gemm_route(h, tokens, logits, ld, dtype, routing, ids, weights, offsets, order, position,
+               workspace, workspace_bytes, stream) -> int:
+    """Raw call: pointers and the stream are integers (0/None for NULL); routing
+    is a GemmRouting or None."""
+    return lib.gemm_route(h, tokens, logits, ld, dtype,
+                          None if routing is None else ctypes.byref(routing), ids, weights, offsets,
+                          order, position, workspace, workspace_bytes, stream)
+
+
+def gemm_route_grad(h, tokens, logits, ld, dtype, routing, ids, dweights, dlogits, ldd, stream) -> int:
+    """Raw call: pointers and the stream are integers (0/None for NULL); routing
+    is a GemmRouting or None."""
+    return lib.gemm_route_grad(h, tokens, logits, ld, dtype,
+                               None if routing is None else ctypes.byref(routing), ids, dweights,
+                               dlogits, ldd, stream)
+
+
+def gemm_gather_rows(h, tokens, cols, top, X, ldx, rows, order, weights, D, ldd, dtype, stream) -> int:
+    """Raw call: pointers and the stream are integers (0/None for NULL)."""
+    return lib.gemm_gather_rows(h, tokens, cols, top, X, ldx, rows, order, weights, D, ldd, dtype,
+                                stream)
+
+
+def gemm_combine_rows(h, tokens, cols, top, Y, ldy, rows, position, weights, beta, C, ldc, D, ldd,
+                      dtype, stream) -> int:
+    """Raw call: pointers and the stream are integers (0/None for NULL)."""
+    return lib.gemm_combine_rows(h, tokens, cols, top, Y, ldy, rows, position, weights, beta, C, ldc,
+                                 D, ldd, dtype, stream)
+
+
+def gemm_combine_rows_grad(h, tokens, cols, top, Y, ldy, rows, position, weights, dD, lddd, dY, lddy,
+                           dweights, dtype, stream) -> int:
+    """Raw call: pointers and the stream are integers (0/None for NULL)."""
+    return lib.gemm_combine_rows_grad(h, tokens, cols, top, Y, ldy, rows, position, weights, dD, lddd,
+                                      dY, lddy, dweights, dtype, stream)
 
 
 def attach_workspace(h, nbytes=None, device=None):
@@ -669,3 +777,327 @@ def run_lora(h, A, B, D, offsets, down, up, workspace, ids=None, scales=None, C=
         B.data_ptr(), ldb, beta, c, ldc, D.data_ptr(), ldd, dtype, ctypes.byref(lo),
         workspace.data_ptr(), workspace.nbytes, _stream_on(device) if stream is None else stream)
     return _finish(s, check, "gemm_run_lora")
+
+
+# ---- what an expert layer needs around its products ---------------------------
+ACTIVATIONS = {"none": GEMM_ACT_NONE, "relu": GEMM_ACT_RELU, "gelu": GEMM_ACT_GELU,
+               "silu": GEMM_ACT_SILU, "gelu_tanh": GEMM_ACT_GELU_TANH}
+SCORES = {"softmax": GEMM_SCORES_SOFTMAX, "sigmoid": GEMM_SCORES_SIGMOID}
+
+
+def _named(table, name, what):
+    try:
+        return table[name]
+    except (KeyError, TypeError):
+        raise ValueError(f"{what} must be one of {', '.join(table)}") from None
+
+
+def _launch(device, fn, *args):
+    """fn(*args) with `device`, whose memory the arguments point to, current: the
+    default stream is that of the current device."""
+    import torch
+
+    if device == torch.cuda.current_device():
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
+
+
+def _stream_of(device, stream):
+    return _stream_on(device) if stream is None else stream
+
+
+def _table(t, dtype, rows, cols, device, what):
+    """Data pointer of a packed rows x cols tensor on device index `device`."""
+    if tuple(t.shape) != (rows, cols) or t.dtype is not dtype or t.get_device() != device or (
+            not t.is_contiguous()):
+        raise ValueError(f"{what} must be a contiguous {rows} x {cols} {dtype} tensor on the same device")
+    return t.data_ptr()
+
+
+def _logits(x):
+    """gemm_dtype_t, rows, columns and leading dimension of a router's logits."""
+    import torch
+
+    if x.dtype is torch.float32:
+        dtype = GEMM_DTYPE_F32
+    elif x.dtype is torch.bfloat16:
+        dtype = GEMM_DTYPE_BF16_BF16
+    else:
+        raise TypeError("logits must be float32 or bfloat16")
+    return (dtype, *_matrix(x))
+
+
+def route_workspace(tokens: int, experts: int, device=None):
+    """A workspace for run_route on up to `tokens` tokens of `experts` experts, as
+    a torch uint8 tensor on `device` (the current device by default); one per
+    concurrently used stream."""
+    import torch
+
+    return torch.empty(max(gemm_route_workspace_bytes(tokens, experts), 256), dtype=torch.uint8,
+                       device="cuda" if device is None else device)
+
+
+def run_route(h, logits, ids, weights, offsets=None, order=None, position=None, workspace=None,
+              scores="softmax", bias=None, groups=1, top_groups=1, group_top=1, renormalize=False,
+              scale=1.0, stream=None, check=True) -> int:
+    """gemm_route on torch tensors: each token's experts, their weights and the plan
+    of rows sorted by expert.
+
+    logits: tokens x experts, float32 or bfloat16; ids (int32) and weights
+    (float32): tokens x top.  The plan, all three int32 or none: offsets (experts +
+    1, as run_grouped takes them), order (tokens * top: the assignment t * top + j of
+    each row, -1 beyond the last) and position (tokens x top: the row of each
+    assignment, or -1), with a workspace from route_workspace for more than 16
+    tokens.  scores: "softmax" or "sigmoid"; bias: float32, experts, added to the
+    scores for the choice only; groups, top_groups, group_top: choose from the
+    top_groups best of `groups` runs of experts, by the sum of their group_top (1
+    or 2) best.  weights = scale * score, over the sum of the chosen scores with
+    renormalize.  Logits of -inf are never chosen: ids -1 and weight 0 where fewer
+    than top are left.
+    """
+    import torch
+
+    dtype, tokens, experts, ld = _logits(logits)
+    if ids.dim() != 2:
+        raise ValueError("ids must be tokens x top")
+    top = ids.shape[1]
+    device = _device_of(logits, ids, weights, offsets, order, position, workspace, bias)
+    i32 = torch.int32
+    plan = (None, None, None)
+    if offsets is not None or order is not None or position is not None:
+        if offsets is None or order is None or position is None:
+            raise ValueError("offsets, order and position come together")
+        plan = (_device_vector(offsets, i32, experts + 1, device, "offsets"),
+                _device_vector(order, i32, tokens * top, device, "order"),
+                _table(position, i32, tokens, top, device, "position"))
+    r = GemmRouting(experts, top, _named(SCORES, scores, "scores"), groups, top_groups, group_top,
+                    _device_vector(bias, torch.float32, experts, device, "bias"), int(renormalize),
+                    scale)
+    s = _launch(device, lib.gemm_route, h, tokens, logits.data_ptr(), ld, dtype, ctypes.byref(r),
+                _table(ids, i32, tokens, top, device, "ids"),
+                _table(weights, torch.float32, tokens, top, device, "weights"), *plan,
+                None if workspace is None else workspace.data_ptr(),
+                0 if workspace is None else workspace.nbytes, _stream_of(device, stream))
+    return _finish(s, check, "gemm_route")
+
+
+def run_route_grad(h, logits, ids, dweights, dlogits, scores="softmax", renormalize=False, scale=1.0,
+                   stream=None, check=True) -> int:
+    """gemm_route_grad on torch tensors: the logits' gradient (dlogits, of the
+    logits' type) from that of run_route's weights, for the experts it chose."""
+    import torch
+
+    dtype, tokens, experts, ld = _logits(logits)
+    rows, cols, ldd = _matrix(dlogits)
+    if dlogits.dtype is not logits.dtype or rows != tokens or cols != experts or ids.dim() != 2:
+        raise ValueError("dlogits must have the logits' dtype and shape, ids tokens x top")
+    top = ids.shape[1]
+    device = _device_of(logits, ids, dweights, dlogits)
+    r = GemmRouting(experts, top, _named(SCORES, scores, "scores"), 1, 1, 1, None, int(renormalize),
+                    scale)
+    s = _launch(device, lib.gemm_route_grad, h, tokens, logits.data_ptr(), ld, dtype, ctypes.byref(r),
+                _table(ids, torch.int32, tokens, top, device, "ids"),
+                _table(dweights, torch.float32, tokens, top, device, "dweights"), dlogits.data_ptr(),
+                ldd, _stream_of(device, stream))
+    return _finish(s, check, "gemm_route_grad")
+
+
+def run_gather_rows(h, X, D, order, top, weights=None, stream=None, check=True) -> int:
+    """gemm_gather_rows on torch tensors: D[r] = X[order[r] // top], times
+    weights.view(-1)[order[r]] where weights (tokens x top, float32) is given.
+
+    order: int32, one entry per row of D, from run_route; rows of a negative entry
+    keep their values.  X is float32 or bfloat16, D of X's dtype or float32.
+    """
+    import torch
+
+    dtype = _ragged_dtype(X, X, D, None)
+    tokens, cols, ldx = _matrix(X)
+    rows, Nd, ldd = _matrix(D)
+    if Nd != cols:
+        raise ValueError("X and D must have the same columns")
+    device = _device_of(D, X, order, weights)
+    s = _launch(device, lib.gemm_gather_rows, h, tokens, cols, top, X.data_ptr(), ldx, rows,
+                _device_vector(order, torch.int32, rows, device, "order"),
+                None if weights is None else _table(weights, torch.float32, tokens, top, device,
+                                                    "weights"),
+                D.data_ptr(), ldd, dtype, _stream_of(device, stream))
+    return _finish(s, check, "gemm_gather_rows")
+
+
+def run_combine_rows(h, Y, D, position, weights=None, C=None, beta=0.0, stream=None,
+                     check=True) -> int:
+    """gemm_combine_rows on torch tensors:
+    D[t] = sum_j weights[t, j] * Y[position[t, j]] + beta * C[t], with positions
+    outside Y's rows left out.
+
+    Y: rows x cols, float32 or bfloat16; C, D: tokens x cols, of Y's dtype or
+    float32 (D may be C); position: int32, tokens x top, from run_route; weights:
+    float32, tokens x top, or None (all 1).
+    """
+    import torch
+
+    dtype = _ragged_dtype(Y, Y, D, C)
+    rows, cols, ldy = _matrix(Y)
+    tokens, Nd, ldd = _matrix(D)
+    c, ldc = None, cols
+    if C is not None:
+        c = C.data_ptr()
+        Mc, Nc, ldc = _matrix(C)
+        if Mc != tokens or Nc != cols:
+            raise ValueError("C must have D's shape")
+    if Nd != cols or position.dim() != 2:
+        raise ValueError("Y and D must have the same columns, position tokens x top")
+    top = position.shape[1]
+    device = _device_of(D, Y, C, position, weights)
+    s = _launch(device, lib.gemm_combine_rows, h, tokens, cols, top, Y.data_ptr(), ldy, rows,
+                _table(position, torch.int32, tokens, top, device, "position"),
+                None if weights is None else _table(weights, torch.float32, tokens, top, device,
+                                                    "weights"),
+                beta, c, ldc, D.data_ptr(), ldd, dtype, _stream_of(device, stream))
+    return _finish(s, check, "gemm_combine_rows")
+
+
+def run_combine_rows_grad(h, Y, dD, dY, dweights, position, weights, stream=None, check=True) -> int:
+    """gemm_combine_rows_grad on torch tensors: dY[position[t, j]] = weights[t, j] *
+    dD[t] and dweights[t, j] = <Y[position[t, j]], dD[t]>.
+
+    Y, dY: rows x cols (dY may be Y); dD: tokens x cols, of Y's dtype or float32;
+    position (int32), weights and dweights (float32): tokens x top.
+    """
+    import torch
+
+    if dY.dtype is not Y.dtype:
+        raise TypeError("dY must have Y's dtype")
+    dtype = _ragged_dtype(Y, Y, dD, None)
+    rows, cols, ldy = _matrix(Y)
+    tokens, Nd, lddd = _matrix(dD)
+    rows_dy, cols_dy, lddy = _matrix(dY)
+    if Nd != cols or rows_dy != rows or cols_dy != cols or position.dim() != 2:
+        raise ValueError("inconsistent shapes of Y, dY, dD and position")
+    top = position.shape[1]
+    device = _device_of(dY, Y, dD, dweights, position, weights)
+    f32 = torch.float32
+    s = _launch(device, lib.gemm_combine_rows_grad, h, tokens, cols, top, Y.data_ptr(), ldy, rows,
+                _table(position, torch.int32, tokens, top, device, "position"),
+                _table(weights, f32, tokens, top, device, "weights"), dD.data_ptr(), lddd,
+                dY.data_ptr(), lddy, _table(dweights, f32, tokens, top, device, "dweights"), dtype,
+                _stream_of(device, stream))
+    return _finish(s, check, "gemm_combine_rows_grad")
+
+
+def run_grouped_act(h, A, B, D, offsets=None, activation="none", gated=False, bias=None, Z=None,
+                    R=None, transB="N", scales=None, alpha=1.0, stream=None, check=True) -> int:
+    """gemm_run_grouped_act on torch tensors: for each group g, with its rows
+    offsets[g] .. offsets[g+1]-1,
+    z = alpha * scales[g] * A[rows] @ op(B[g]) + bias[g]
+    D[rows] = act(z) + R[rows], or gated act(z[:, :N]) * z[:, N:] + R[rows].
+
+    A: M x K; B: groups x K x W ("N") or groups x W x K ("T"), W = N or gated 2 N;
+    D, R: M x N (D may be R); bias: groups x W of D's dtype, or W for all groups;
+    Z: M x W of D's dtype, which gets z; activation: "none", "relu", "gelu", "silu"
+    or "gelu_tanh".  offsets None: one dense product of all rows with B (K x W or
+    W x K, or a single group).  scales, dtypes and rows in no group as for
+    run_grouped.
+    """
+    import torch
+
+    dtype = _ragged_dtype(A, B, D, R)
+    if any(x is not None and x.dtype is not D.dtype for x in (Z, bias)):
+        raise TypeError("Z and bias must have D's dtype")
+    M, K, lda = _matrix(A)
+    if offsets is None and B.dim() == 2:
+        Kb, W, ldb = _matrix(B)
+        groups, stride_b = 1, 0
+    else:
+        groups, Kb, W, ldb, stride_b = _matrices(B)
+    if transB != "N":
+        Kb, W = W, Kb
+    Md, N, ldd = _matrix(D)
+    act = GemmAct(_named(ACTIVATIONS, activation, "activation"), int(bool(gated)))
+    if Kb != K or Md != M or W != (2 * N if gated else N) or (offsets is None and groups != 1):
+        raise ValueError("inconsistent grouped GEMM shapes")
+    if bias is not None:
+        if bias.dim() == 1:
+            shape, act.stride_bias = (W,), 0
+        else:
+            shape, act.stride_bias = (groups, W), bias.stride(0) if groups > 1 else 0
+        if tuple(bias.shape) != shape or (W > 1 and bias.stride(-1) != 1):
+            raise ValueError("bias must be groups x width, or width, with unit stride")
+        act.bias = bias.data_ptr()
+    if Z is not None:
+        Mz, Wz, act.ldz = _matrix(Z)
+        act.Z = Z.data_ptr()
+        if Mz != M or Wz != W:
+            raise ValueError("Z must be M x the products' columns")
+    if R is not None:
+        Mr, Nr, act.ldr = _matrix(R)
+        act.R = R.data_ptr()
+        if Mr != M or Nr != N:
+            raise ValueError("R must have D's shape")
+    device = _device_of(D, A, B, bias, Z, R)
+    gr = None
+    if offsets is not None:
+        gr = ctypes.byref(GemmGroups(
+            groups, _device_vector(offsets, torch.int32, groups + 1, device, "offsets"),
+            _device_vector(scales, torch.float32, groups, device, "scales")))
+    elif scales is not None:
+        raise ValueError("scales are the groups': without offsets, use alpha")
+    s = _launch(device, lib.gemm_run_grouped_act, h, GEMM_OP_N if transB == "N" else GEMM_OP_T, M, N, K,
+                alpha, A.data_ptr(), lda, B.data_ptr(), ldb, stride_b, D.data_ptr(), ldd, dtype, gr,
+                ctypes.byref(act), _stream_of(device, stream))
+    return _finish(s, check, "gemm_run_grouped_act")
+
+
+def act_grad_workspace(rows: int, width: int, groups: int, device=None):
+    """A workspace for run_grouped_act_grad with dbias on up to `rows` rows of
+    `groups` groups and a Z of `width` columns, as a torch uint8 tensor on `device`
+    (the current device by default); one per concurrently used stream."""
+    import torch
+
+    return torch.empty(max(gemm_act_grad_workspace_bytes(rows, width, groups), 256), dtype=torch.uint8,
+                       device="cuda" if device is None else device)
+
+
+def run_grouped_act_grad(h, Z, dD, dZ, offsets=None, activation="none", gated=False, H=None,
+                         dbias=None, workspace=None, stream=None, check=True) -> int:
+    """gemm_run_grouped_act_grad on torch tensors: the gradient of run_grouped_act's
+    epilogue from the Z it kept and D's gradient.
+    dZ = dD * act'(Z), or gated [dD * U * act'(G), dD * act(G)] of Z = [G U].
+
+    Z: M x W; dD: M x N (W = N or gated 2 N), of one dtype; dZ: M x W and H, if given,
+    M x N, of the operands' dtype, float32 or bfloat16 (dZ may be Z and H be dD): H
+    gets act(Z), or act(G) * U.  dbias, if given: float32, groups x W, the columns'
+    sums over each group's rows, with a workspace from act_grad_workspace.
+    offsets None: all rows are one group's.
+    """
+    import torch
+
+    dtype = _ragged_dtype(dZ, dZ if H is None else H, Z, dD)
+    M, W, ldz = _matrix(Z)
+    Md, N, lddd = _matrix(dD)
+    Mz, Wz, lddz = _matrix(dZ)
+    if Md != M or Mz != M or Wz != W or W != (2 * N if gated else N):
+        raise ValueError("inconsistent shapes of Z, dD and dZ")
+    hp, ldh = None, N
+    if H is not None:
+        hp = H.data_ptr()
+        Mh, Nh, ldh = _matrix(H)
+        if Mh != M or Nh != N:
+            raise ValueError("H must have dD's shape")
+    device = _device_of(dZ, Z, dD, H, dbias, workspace)
+    groups, gr = 1, None
+    if offsets is not None:
+        if offsets.dim() != 1 or offsets.shape[0] < 1:
+            raise ValueError("offsets must hold groups + 1 entries")
+        groups = offsets.shape[0] - 1
+        gr = ctypes.byref(GemmGroups(
+            groups, _device_vector(offsets, torch.int32, groups + 1, device, "offsets"), None))
+    s = _launch(device, lib.gemm_run_grouped_act_grad, h, M, N,
+                _named(ACTIVATIONS, activation, "activation"), int(bool(gated)), Z.data_ptr(), ldz,
+                dD.data_ptr(), lddd, dZ.data_ptr(), lddz, hp, ldh,
+                None if dbias is None else _table(dbias, torch.float32, groups, W, device, "dbias"),
+                dtype, gr, None if workspace is None else workspace.data_ptr(),
+                0 if workspace is None else workspace.nbytes, _stream_of(device, stream))
+    return _finish(s, check, "gemm_run_grouped_act_grad")

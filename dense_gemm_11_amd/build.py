@@ -32,7 +32,9 @@ SOURCES = ["api.hip", "inst_bf16.hip", "inst_bf16_dma.hip", "inst_bf16_dma_out.h
            "inst_rag_rows_bf16.hip", "inst_rag_lora_bf16.hip", "inst_rag_k_bf16.hip",
            "inst_rag_f32.hip", "inst_rag_stream_rows.hip",
            "inst_rag_stream_lora.hip", "inst_rag_stream_lora_one.hip",
-           "inst_rag_stream_shrink.hip", "inst_rag_stream_k.hip"]
+           "inst_rag_stream_shrink.hip", "inst_rag_stream_k.hip", "act_api.hip",
+           "inst_act_bf16.hip", "inst_gate_bf16.hip", "inst_act_f32.hip", "inst_act_stream.hip",
+           "route_api.hip", "inst_route_f32.hip", "inst_route_bf16.hip", "rows_api.hip"]
 
 
 def hipcc() -> str:

@@ -1,0 +1,8 @@
+// Routing from bf16 logits.
+#include "route_variants.hpp"
+
+namespace dg {
+
+RouteFn route_fn_bf16(bool lanes64, int v, bool wide) { return route_fn<bf16_t>(lanes64, v, wide); }
+
+}  // namespace dg

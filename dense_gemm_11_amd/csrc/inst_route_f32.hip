@@ -1,0 +1,8 @@
+// Routing from fp32 logits.
+#include "route_variants.hpp"
+
+namespace dg {
+
+RouteFn route_fn_f32(bool lanes64, int v, bool wide) { return route_fn<float>(lanes64, v, wide); }
+
+}  // namespace dg

@@ -52,6 +52,7 @@
 #include <type_traits>
 
 #include "common.hpp"
+#include "act.hpp"
 #include "mfma_gemm.hpp"
 #include "lora.hpp"
 #include "ragged.hpp"
@@ -327,7 +328,9 @@ __device__ __forceinline__ i32x4 buffer_rsrc(const void* base, uint32_t nrec)
 // PAIRED: the operand lives in pair buffers (k-contiguous only): a DMA copy
 // covers two K-steps, register-staged copies one step into half `half`.
 // WT, NWP: the wave tile's extent along mn and the wave positions along mn.
-template <class Cfg, int R, bool KC, bool ALIGNED, bool PAIRED, int WT, int NWP>
+// GATE (B of RAG_GATE): the tile is R / 2 of the matrix's first `split` columns
+// and the R / 2 that lie `split` further, half of each wave's tile of either.
+template <class Cfg, int R, bool KC, bool ALIGNED, bool PAIRED, int WT, int NWP, bool GATE = false>
 struct DmaOperand {
     static_assert(!PAIRED || KC, "only k-contiguous operands are paired");
     static constexpr int KD = PAIRED ? 2 * Cfg::BK : Cfg::BK;  // k per buffer
@@ -349,7 +352,19 @@ struct DmaOperand {
     // either way nothing reads them back.
     uint32_t voff[ND];
 
-    __device__ __forceinline__ void init(int wave, int lane, int64_t ld)
+    // Column i of the tile: which of its R / 2 pairs it belongs to, and where the
+    // matrix has it, from the panel's first.
+    static_assert(!GATE || (WT / 2) % 16 == 0, "whole chunks of either half");
+    __device__ static __forceinline__ int pair_of(int i)
+    {
+        return GATE ? i / WT * (WT / 2) + i % (WT / 2) : i;
+    }
+    __device__ static __forceinline__ int column_of(int i, int split)
+    {
+        return GATE && i % WT >= WT / 2 ? pair_of(i) + split : pair_of(i);
+    }
+
+    __device__ __forceinline__ void init(int wave, int lane, int64_t ld, int split = 0)
     {
 #pragma unroll
         for (int d = 0; d < ND; ++d) {
@@ -361,7 +376,9 @@ struct DmaOperand {
             if constexpr (KC) c = pc ^ L::kswz(row);
             else c = pc ^ L::mswz(row);
             const bool pad = KC ? row >= R : c * VEC >= R;
-            voff[d] = pad ? 0x80000000u : (uint32_t)(((int64_t)row * ld + c * VEC) * Cfg::ES);
+            voff[d] = pad ? 0x80000000u
+                      : KC ? (uint32_t)(((int64_t)column_of(row, split) * ld + c * VEC) * Cfg::ES)
+                           : (uint32_t)(((int64_t)row * ld + column_of(c * VEC, split)) * Cfg::ES);
         }
     }
 
@@ -411,7 +428,7 @@ struct DmaOperand {
     // Register-staged copy of the step at k0 with zero fill outside
     // [0, rlim) x [0, K), into half `half` of a pair buffer when PAIRED.
     __device__ __forceinline__ void guarded(const T* panel, int64_t ld, int rlim, int k0, int K,
-                                            char* lds, int tid, int half = 0) const
+                                            char* lds, int tid, int half = 0, int split = 0) const
     {
         // in batches of GB chunks per thread, which bounds the registers this
         // path adds on top of the accumulators and fragments
@@ -428,16 +445,17 @@ struct DmaOperand {
                 T e[VEC];
                 if constexpr (KC) {   // row = mn, elements along k
                     const int k = k0 + c * VEC;
-                    const T* src = panel + (int64_t)row * ld + k;
-                    if (ALIGNED && row < rlim && k + VEC <= K) {
+                    const T* src = panel + (int64_t)column_of(row, split) * ld + k;
+                    const int at = pair_of(row);
+                    if (ALIGNED && at < rlim && k + VEC <= K) {
                         v[b] = *reinterpret_cast<const u32x4_elem<T>*>(src);
                         continue;
                     }
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) e[j] = (row < rlim && k + j < K) ? src[j] : T(0);
+                    for (int j = 0; j < VEC; ++j) e[j] = (at < rlim && k + j < K) ? src[j] : T(0);
                 } else {              // row = k, elements along mn
-                    const int k = k0 + row, mn = c * VEC;
-                    const T* src = panel + (int64_t)k * ld + mn;
+                    const int k = k0 + row, mn = pair_of(c * VEC);
+                    const T* src = panel + (int64_t)k * ld + column_of(c * VEC, split);
                     if (ALIGNED && k < K && mn + VEC <= rlim) {
                         v[b] = *reinterpret_cast<const u32x4_elem<T>*>(src);
                         continue;
@@ -601,7 +619,8 @@ __device__ __forceinline__ void barrier_only() { asm volatile("s_barrier" ::: "m
 //
 // RAG (ragged.hpp): the workgroup first narrows p to its group of rows, or
 // (RAG_LORA) adds its rows' low-rank products, as more of K where the tile has
-// one adapter and in the epilogue where it has several.
+// one adapter and in the epilogue where it has several.  RAG_ACT and RAG_GATE
+// have an epilogue of their own (act.hpp).
 template <class Cfg, bool A_KC, bool B_KC, bool ALIGNED, bool SK, bool OUT_T, bool OUT_BF16, bool EPI,
           int RAG, class Args>
 __device__ __forceinline__ void dma_gemm_body(Args p)
@@ -615,7 +634,10 @@ __device__ __forceinline__ void dma_gemm_body(Args p)
     constexpr bool PAIRED = PA || PB;
     constexpr int NP = Cfg::NP;
     using OpA = DmaOperand<Cfg, BM, A_KC, ALIGNED, PA, Cfg::WTM, Cfg::WM>;
-    using OpB = DmaOperand<Cfg, BN, B_KC, ALIGNED, PB, Cfg::WTN, Cfg::WN>;
+    // RAG_GATE: B has 2 p.N columns, of which a tile takes BN, for BN / 2 outputs
+    constexpr bool GATE = RAG == RAG_GATE, ACTED = GATE || RAG == RAG_ACT;
+    constexpr int BNO = GATE ? BN / 2 : BN;
+    using OpB = DmaOperand<Cfg, BN, B_KC, ALIGNED, PB, Cfg::WTN, Cfg::WN, GATE>;
     constexpr int A_ST = PA ? 0 : OpA::BYTES, ST_BYTES = A_ST + (PB ? 0 : OpB::BYTES);
     constexpr int A_PR = PA ? OpA::BYTES : 0, PR_BYTES = A_PR + (PB ? OpB::BYTES : 0);
     constexpr int ST_DECL = ST_BYTES > 0 ? ST_BYTES : 16, PR_DECL = PR_BYTES > 0 ? PR_BYTES : 16;
@@ -672,20 +694,23 @@ __device__ __forceinline__ void dma_gemm_body(Args p)
     if constexpr (RAG == RAG_ROWS || RAG == RAG_K)
         if (!narrow_to_group<RAG, BM, T, std::conditional_t<OUT_BF16, bf16_t, float>>(p, tm_g, tn_g))
             return;
+    if constexpr (ACTED)
+        if (!narrow_act<BM, T, std::conditional_t<OUT_BF16, bf16_t, float>>(p, tm_g, tn_g)) return;
     const T* A = static_cast<const T*>(p.A);
     const T* B = static_cast<const T*>(p.B);
 
     OpA oa;
     OpB ob;
     oa.init(wave, lane, p.lda);
-    ob.init(wave, lane, p.ldb);
+    ob.init(wave, lane, p.ldb, GATE ? p.N : 0);
     oa.init_frags(lane, wave_m0);
     ob.init_frags(lane, wave_n0);
     // end of each stored matrix: A is M x K (k-contiguous) or K x M, B likewise
     const char* end_a = reinterpret_cast<const char*>(
         A + (A_KC ? (int64_t)(p.M - 1) * p.lda + p.K : (int64_t)(p.K - 1) * p.lda + p.M));
     const char* end_b = reinterpret_cast<const char*>(
-        B + (B_KC ? (int64_t)(p.N - 1) * p.ldb + p.K : (int64_t)(p.K - 1) * p.ldb + p.N));
+        B + (B_KC ? ((int64_t)p.N * (GATE ? 2 : 1) - 1) * p.ldb + p.K
+                  : (int64_t)(p.K - 1) * p.ldb + (int64_t)p.N * (GATE ? 2 : 1)));
     const int nk_all = (p.K + BK - 1) / BK;  // K-steps of a whole tile
     const bool k_ragged = (p.K % BK) != 0;
     // RAG_K: the rows of a group are the product's K, and only the device
@@ -732,9 +757,9 @@ __device__ __forceinline__ void dma_gemm_body(Args p)
     // The K-steps [k_lo, k_hi) of output tile (tm, tn), accumulated into acc
     // from zero.  Every wave enters with the LDS stages free.
     auto tile_work = [&](int tm, int tn, int k_lo, int k_hi) __attribute__((always_inline)) {
-    const int m0 = tm * BM, n0 = tn * BN;
+    const int m0 = tm * BM, n0 = tn * BNO;
     const int rlim_a = p.M - m0, rlim_b = p.N - n0;
-    const bool edge = rlim_a < BM || rlim_b < BN;
+    const bool edge = rlim_a < BM || rlim_b < BNO;
     const T* panel_a = A_KC ? A + (int64_t)m0 * p.lda : A + m0;
     const T* panel_b = B_KC ? B + (int64_t)n0 * p.ldb : B + n0;
     const i32x4 rsrc_a = OpA::panel_rsrc(panel_a, end_a);
@@ -768,7 +793,8 @@ __device__ __forceinline__ void dma_gemm_body(Args p)
             if constexpr (!PB) ob.dma(rsrc_b, OpB::step_bytes(k0, p.ldb), base + A_ST, wave);
         } else {
             if constexpr (!PA) oa.guarded(panel_a, p.lda, rlim_a, k0, p.K, base, tid);
-            if constexpr (!PB) ob.guarded(panel_b, p.ldb, rlim_b, k0, p.K, base + A_ST, tid);
+            if constexpr (!PB)
+                ob.guarded(panel_b, p.ldb, rlim_b, k0, p.K, base + A_ST, tid, 0, GATE ? p.N : 0);
         }
     };
     // steps 2q and 2q+1 of the paired operands into a pair buffer (one DMA
@@ -783,7 +809,8 @@ __device__ __forceinline__ void dma_gemm_body(Args p)
             for (int h = 0; h < 2 && 2 * q + h < nk; ++h) {
                 if constexpr (PA) oa.guarded(panel_a, p.lda, rlim_a, k0 + h * BK, p.K, base, tid, h);
                 if constexpr (PB)
-                    ob.guarded(panel_b, p.ldb, rlim_b, k0 + h * BK, p.K, base + A_PR, tid, h);
+                    ob.guarded(panel_b, p.ldb, rlim_b, k0 + h * BK, p.K, base + A_PR, tid, h,
+                               GATE ? p.N : 0);
             }
         }
     };
@@ -1334,7 +1361,69 @@ __device__ __forceinline__ void dma_gemm_body(Args p)
     });
     };  // epilogue
 
-    if constexpr (RAG == RAG_ROWS || RAG == RAG_K) {
+    // ---- epilogue of RAG_ACT and RAG_GATE.  As above a fragment goes through LDS
+    // to come out row by row, here one fragment of 32 columns at a time, or a
+    // gate's and its partner's: 4 KiB each per wave, side by side in the stage
+    // arrays.  Rows of D and Z are written 32 columns at a time, so their stores
+    // are ordinary ones, which the L2 puts together to lines.
+    auto act_epilogue = [&](int tm, int tn) __attribute__((always_inline)) {
+    if constexpr (ACTED) {
+        constexpr int NFH = GATE ? NF / 2 : NF, HALVES = GATE ? 2 : 1;
+        constexpr int CH = FM / 4, RPI = 64 / CH, NT = FM / RPI, UNIT = FM * FM * 4;
+        constexpr bool USE_PR = PR_BYTES > ST_BYTES;
+        constexpr int PER = (USE_PR ? PR_BYTES : ST_BYTES) / UNIT;  // fragments an array holds
+        constexpr int ARRAYS = (HALVES * Cfg::WAVES + PER - 1) / PER;
+        static_assert(FM == 32 && !OUT_T && (!GATE || NF % 2 == 0), "fragments");
+        static_assert(ARRAYS <= (USE_PR ? 2 : S < 3 ? S : 3), "staging space");
+        const int wv = __builtin_amdgcn_readfirstlane(wave);
+        auto unit = [&](int half) __attribute__((always_inline)) -> char* {
+            const int u = wv * HALVES + half, a = u / PER;
+            char* base = USE_PR ? pr0 : st0;
+            if constexpr (ARRAYS > 1) base = a == 1 ? (USE_PR ? pr1 : st1) : base;
+            if constexpr (ARRAYS > 2) base = a == 2 ? st2 : base;
+            return base + u % PER * UNIT;
+        };
+        char* const region[2] = {unit(0), unit(HALVES - 1)};
+        auto slot = [&](int half, int r, int chunk) __attribute__((always_inline)) -> f32x4* {
+            return reinterpret_cast<f32x4*>(region[half] + r * (FM * 4) + ((chunk ^ (r & (CH - 1))) * 16));
+        };
+        const int row0 = tm * BM + wave_m0 + lane / CH;
+        const int col0 = tn * BNO + wave_n0 / HALVES + 4 * (lane % CH);
+        f32x4 bias_g[NFH], bias_u[NFH];
+#pragma unroll
+        for (int j = 0; j < NFH; ++j) {
+            const int col = col0 + j * FM;
+            bias_g[j] = act_bias<OutT>(p, col, p.N - col);
+            bias_u[j] = GATE ? act_bias<OutT>(p, p.N + col, p.N - col) : f32x4{};
+        }
+        __syncthreads();  // every wave is done reading operands from the stage arrays
+        static_for<MF * NFH>([&](auto x_c) __attribute__((always_inline)) {
+            constexpr int i = decltype(x_c)::value / NFH, j = decltype(x_c)::value % NFH;
+#pragma unroll
+            for (int half = 0; half < HALVES; ++half)
+#pragma unroll
+                for (int vg = 0; vg < Cfg::ACC / 4; ++vg) {
+                    const Acc& a = acc[i][j + half * NFH];
+                    *slot(half, lane % FM, 2 * vg + (lane >> 5)) =
+                        f32x4{a[4 * vg], a[4 * vg + 1], a[4 * vg + 2], a[4 * vg + 3]};
+                }
+            const int col = col0 + j * FM;
+#pragma unroll 1
+            for (int t = 0; t < NT; ++t) {
+                const int r = t * RPI + lane / CH, row = row0 + i * FM + t * RPI;
+                const f32x4 g = *slot(0, r, lane % CH);
+                const f32x4 u = GATE ? *slot(1, r, lane % CH) : f32x4{};
+                if (row < p.M && col < p.N)
+                    act_outputs<GATE, OutT>(p, row, col, p.N - col, g, u, bias_g[j], bias_u[j]);
+            }
+        });
+    }
+    };
+
+    if constexpr (ACTED) {
+        tile_work(tm_g, tn_g, 0, nk_all);
+        act_epilogue(tm_g, tn_g);
+    } else if constexpr (RAG == RAG_ROWS || RAG == RAG_K) {
         tile_work(tm_g, tn_g, 0, nk_all);  // an empty K leaves zero accumulators
         epilogue(tm_g, tn_g, 0, 0);
     } else if constexpr (!SK) {
@@ -1462,6 +1551,14 @@ __global__ __launch_bounds__(Cfg::THREADS) __attribute__((amdgpu_waves_per_eu(Cf
 void dma_ragged_kernel(RaggedArgs p)
 {
     dma_gemm_body<Cfg, A_KC, B_KC, true, false, false, OUT_BF16, false, RAG>(p);
+}
+
+// ... with bias, activation and residual (RAG_ACT) or a gate as well (RAG_GATE).
+template <class Cfg, bool B_KC, bool OUT_BF16, int RAG>
+__global__ __launch_bounds__(Cfg::THREADS) __attribute__((amdgpu_waves_per_eu(Cfg::WPE)))
+void dma_act_kernel(ActArgs p)
+{
+    dma_gemm_body<Cfg, true, B_KC, true, false, false, OUT_BF16, false, RAG>(p);
 }
 
 }  // namespace dg

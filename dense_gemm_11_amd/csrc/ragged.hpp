@@ -20,8 +20,19 @@ namespace dg {
 //            with their segment's adapter, already scaled (lora.hpp);
 //  RAG_SHRINK: those products, T[rows of s] = s_a A[rows of s] op(down_a)
 //            (stream.hpp);
-//  RAG_LORA_ONE: RAG_LORA and RAG_SHRINK in one launch, for one tile of rows.
-enum : int { RAG_NONE = 0, RAG_ROWS = 1, RAG_K = 2, RAG_LORA = 3, RAG_SHRINK = 4, RAG_LORA_ONE = 5 };
+//  RAG_LORA_ONE: RAG_LORA and RAG_SHRINK in one launch, for one tile of rows;
+//  RAG_ACT, RAG_GATE: the products of RAG_ROWS with bias, activation and, RAG_GATE,
+//            a gate (act.hpp).
+enum : int {
+    RAG_NONE = 0,
+    RAG_ROWS = 1,
+    RAG_K = 2,
+    RAG_LORA = 3,
+    RAG_SHRINK = 4,
+    RAG_LORA_ONE = 5,
+    RAG_ACT = 6,
+    RAG_GATE = 7
+};
 
 struct RaggedArgs : GemmArgs {
     const int32_t* offsets;  // groups + 1
@@ -71,9 +82,10 @@ __device__ __forceinline__ int wave_scan(int x)
 }
 
 // A workgroup's output tile of the row-ragged product: tile (tm, tn) of group
-// `group`, which holds rows start .. start+size-1 in tiles_m tiles of BM.
+// `group`, which holds rows start .. start+size-1 in tiles_m tiles of BM; the
+// groups before it have `first` rows of tiles.
 struct RowTile {
-    int group, start, size, tiles_m, in_group;
+    int group, start, size, tiles_m, in_group, first;
 };
 
 // Number of the tile that workgroup w takes: workgroups go round the 8 XCDs, and
@@ -125,7 +137,8 @@ __device__ __forceinline__ bool find_row_tile(const RaggedArgs& p, int w, int ti
             t.start = __builtin_amdgcn_readlane(start, src);
             t.size = __builtin_amdgcn_readlane(size, src);
             t.tiles_m = __builtin_amdgcn_readlane(cnt, src);
-            t.in_group = w - __builtin_amdgcn_readlane(ex, src) * tiles_n;
+            t.first = __builtin_amdgcn_readlane(ex, src);
+            t.in_group = w - t.first * tiles_n;
             return true;
         }
         base += __builtin_amdgcn_readlane(incl, 63);

@@ -4,19 +4,11 @@
 #include <climits>
 #include <cstdio>
 
-#include "handle.hpp"
-#include "ragged_variants.hpp"
+#include "tile_choice.hpp"
 #include "lora.hpp"
 
 namespace dg {
 namespace {
-
-constexpr int MAX_GROUPS = 1 << 16;
-
-// The kernels form row, column and step numbers in 32 bits up to a tile or a
-// batch of steps past the end (a last tile of 192 rows would pass 2^31 from M =
-// 2^31 - 128), and twice the padded rank.
-constexpr int64_t MAX_EXTENT = INT_MAX - 512;
 
 // The layout, type and size checks that the three calls share.
 gemm_status_t check_common(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_t N, int64_t K,
@@ -30,90 +22,8 @@ gemm_status_t check_common(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_t
     return GEMM_OK;
 }
 
-// Byte offsets inside a panel of `rows` rows of `ld` elements and `cols` more
-// stay below 2^32.
-bool panel_fits(int64_t rows, int64_t ld, int64_t cols, int64_t es)
-{
-    return (rows * ld + cols) * es < ((int64_t)1 << 32) - 64;
-}
-
-// A launch has fewer than 2^32 threads along its first axis.
-bool grid_fits(int64_t grid, int threads) { return grid * threads < (int64_t)1 << 32; }
-
-// C against D: the same matrix with the same strides, or disjoint.
-bool c_d_ok(const void* C, int64_t span_c, const void* D, int64_t span_d, bool same_strides)
-{
-    return C == D ? same_strides : !ranges_overlap(C, span_c, D, span_d);
-}
-
-// A call's tiles, tallest first: the direct-to-LDS ones, then the streaming
-// ones.
-struct TileList {
-    const RaggedTile* dma;
-    const RaggedTile* stream;
-    int n_dma, n;
-    const RaggedTile& operator[](int i) const { return i < n_dma ? dma[i] : stream[i - n_dma]; }
-};
-typedef const RaggedTile* (*TileTable)(int* count);
-TileList tile_list(TileTable dma, TileTable stream)
-{
-    TileList l{};
-    int n_stream = 0;
-    l.dma = dma(&l.n_dma);
-    l.stream = stream(&n_stream);
-    l.n = l.n_dma + n_stream;
-    return l;
-}
-
-// Number of tile i among those of its height.
-int nth_of_height(const TileList& t, int i)
-{
-    int n = 0;
-    for (int j = 0; j < i; ++j) n += t[j].bm == t[i].bm;
-    return n;
-}
-
-// The forced tile (gemm_set_group_tile_nth), else the one of least expected
-// time among those whose grid fits; tiles(t) is the number of output tiles of t a
-// call has, or expects, grid(t) its workgroups, and `bytes` what it reads and
-// writes at the least.
-template <class F, class G>
-const RaggedTile& pick_tile(gemm_handle_t h, const TileList& t, bool b_kc, int64_t K, double bytes,
-                            F tiles, G grid)
-{
-    int best = t.n - 1;
-    if (h->forced_rows > 0) {
-        int height = t[best].bm;
-        for (int i = 0; i < t.n; ++i)
-            if (t[i].bm <= h->forced_rows && t[i].bm > height) height = t[i].bm;
-        for (int i = 0; i < t.n; ++i)
-            if (t[i].bm == height) {
-                best = i;
-                if (nth_of_height(t, i) == h->forced_nth) break;
-            }
-        return t[best];
-    }
-    double best_us = 0.0;
-    for (int i = 0; i < t.n; ++i) {
-        if (!grid_fits(grid(t[i]), t[i].threads)) continue;
-        const double us = expected_us(t[i], b_kc, (double)tiles(t[i]), (double)K, bytes, device_cus());
-        if (best_us == 0.0 || us < best_us) {
-            best = i;
-            best_us = us;
-        }
-    }
-    return t[best];
-}
-
-// Rows of tiles of height bm in `busy` groups of avg rows on average: the last
-// tile of a group is half full.
-double row_tiles(double busy, double avg, int bm)
-{
-    return busy * std::max(1.0, avg / bm + 0.5);
-}
-
 // Notes and logs the launch of tile t.
-void note_call(gemm_handle_t h, const char* what, const RaggedArgs& a, const TileList& tiles,
+void note_call(gemm_handle_t h, const char* what, const RaggedArgs& a, const TileList<RaggedTile>& tiles,
                const RaggedTile& t, int bn, int64_t grid, int launches = 1)
 {
     int i = 0;
@@ -206,8 +116,8 @@ gemm_status_t gemm_run_grouped(gemm_handle_t h, gemm_op_t transB, int64_t M, int
     // a group holds M / groups rows on average, and the host knows no more
     const int64_t busy = std::min<int64_t>(groups->groups, M);
     const double bytes = (double)es * K * ((double)busy * N + M) + (double)eo * M * N;
-    const TileList tiles = dtype == GEMM_DTYPE_F32 ? tile_list(ragged_rows_f32, stream_rows_f32)
-                                                   : tile_list(ragged_rows_bf16, stream_rows_bf16);
+    const auto tiles = dtype == GEMM_DTYPE_F32 ? tile_list(ragged_rows_f32, stream_rows_f32)
+                                              : tile_list(ragged_rows_bf16, stream_rows_bf16);
     // the most tile-rows any split into groups needs
     auto grid_of = [&](const RaggedTile& x) {
         return (M + busy * (x.bm - 1)) / x.bm * ceil_div(N, x.bn[b_kc]);
@@ -291,7 +201,7 @@ gemm_status_t gemm_run_grouped_wgrad(gemm_handle_t h, int64_t M, int64_t N, int6
     a.rows = reads_ab ? (int)rows : 0;  // no rows: D_g = beta * C_g
     a.stride_c = strideC;
     a.stride_d = strideD;
-    const TileList tiles =
+    const auto tiles =
         dtype == GEMM_DTYPE_F32 ? tile_list(ragged_k_f32, stream_k_f32)
                                 : tile_list(ragged_k_bf16, stream_k_bf16);
     auto tiles_of = [&](const RaggedTile& x) { return G * ceil_div(M, x.bm) * ceil_div(N, x.bn[0]); };
@@ -411,8 +321,8 @@ gemm_status_t gemm_run_lora(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_
     a.stride_up = lora->stride_up;
     a.up_kc = up_kc;
     const double bytes = (double)es * K * (N + M) + (double)eo * M * N;
-    const TileList tiles = dtype == GEMM_DTYPE_F32 ? tile_list(ragged_lora_f32, stream_lora_f32)
-                                                   : tile_list(ragged_lora_bf16, stream_lora_bf16);
+    const auto tiles = dtype == GEMM_DTYPE_F32 ? tile_list(ragged_lora_f32, stream_lora_f32)
+                                              : tile_list(ragged_lora_bf16, stream_lora_bf16);
     auto grid_of = [&](const RaggedTile& x) { return ceil_div(M, x.bm) * ceil_div(N, x.bn[b_kc]); };
     const RaggedTile& t = pick_tile(h, tiles, b_kc, K, bytes, grid_of, grid_of);
     const int bn = t.bn[b_kc];

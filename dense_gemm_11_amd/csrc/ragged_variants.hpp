@@ -14,12 +14,14 @@ struct TileCost {
     float alone, alone_k, each, each_k;
 };
 
-struct RaggedTile {
+template <class Fn>
+struct TileOf {
     int bm, bn[2], bk, threads;  // bn of either layout of B
-    RaggedFn fn[2][2];  // [B k-contiguous][bf16 output] (RAG_K: [0] only)
+    Fn fn[2][2];        // [B k-contiguous][bf16 output] (RAG_K: [0] only)
     bool stream;        // a streaming tile
     TileCost cost;
 };
+using RaggedTile = TileOf<RaggedFn>;
 
 // Expected time of `tiles` tiles of t.  The costs are least-squares fits of
 // this form to timings of every tile on random calls of each kind (80 to 170
@@ -34,7 +36,8 @@ struct RaggedTile {
 // suits the row-ragged calls, whose tiles are a guess, and now and then costs the
 // others, whose tiles are known (276 tiles of 192x256 on 256 units, counted as
 // one round: 0.298 ms where 184 of 256x256 take 0.193).
-inline double expected_us(const RaggedTile& t, bool b_kc, double tiles, double K, double bytes, int cus)
+template <class Tile>
+double expected_us(const Tile& t, bool b_kc, double tiles, double K, double bytes, int cus)
 {
     const double n = tiles > cus ? tiles / cus : 1.0, k = K / 1000.0;
     const double alone = t.cost.alone + k * t.cost.alone_k;

@@ -35,8 +35,12 @@
 // rows, one or two blocks of 16 ranks and a K that is not too long costs less
 // than a launch and T's way through memory (one token, 2048x2048, rank 8: 12.6 ->
 // 10.31 us).
+//
+// RAG_GATE (act.hpp) takes NF / 2 fragments of a gate's columns and as many of
+// their partners'.
 #pragma once
 
+#include "act.hpp"
 #include "lora.hpp"
 #include "ragged.hpp"
 
@@ -108,7 +112,7 @@ __device__ __forceinline__ void quad_turn(u32x4 (&x)[4], int lane)
 // VEC rows of k, `bytes` apart, of NF adjacent columns per lane (lane % 16 the
 // columns' place, lane / 16 the rows'), `off` the lane's place in them.
 template <typename T, int NF>
-__device__ __forceinline__ void load_rows(uint32_t (&x)[NF * 4], const T* row, int64_t ld, uint32_t off)
+__device__ __forceinline__ void load_rows(uint32_t* x, const T* row, int64_t ld, uint32_t off)
 {
     constexpr int VEC = 16 / sizeof(T), W = NF * sizeof(T) / 4;  // words per row of k
     using V = typename RawLoad<4 * W>::T;
@@ -122,7 +126,7 @@ __device__ __forceinline__ void load_rows(uint32_t (&x)[NF * 4], const T* row, i
 
 // Fragment j of them (columns j, j + NF, ...) as the MFMA operand.
 template <typename T, int NF>
-__device__ __forceinline__ u32x4 rows_fragment(const uint32_t (&x)[NF * 4], int j)
+__device__ __forceinline__ u32x4 rows_fragment(const uint32_t* x, int j)
 {
     u32x4 r;
     if constexpr (sizeof(T) == 4) {      // row k: words NF*k .. of the columns
@@ -140,15 +144,19 @@ __device__ __forceinline__ u32x4 rows_fragment(const uint32_t (&x)[NF * 4], int 
 
 // This wave's part of a tile's product, added to acc: `rows` rows of A (at least
 // one) and `cols` columns of B, from the tile's first, by all of K.  meanwhile()
-// runs once, while the first loads are under way.
-template <class S, class F>
+// runs once, while the first loads are under way.  GATE: the tile's columns are
+// twice `cols`, the second half of its fragments `split` columns further.
+template <class S, bool GATE = false, class F>
 __device__ __forceinline__ void stream_product(const typename S::T* A, int64_t lda, int rows,
                                                const typename S::T* B, int64_t ldb, int cols, int K,
                                                int wave, int lane, f32x4 (&acc)[S::RF][S::NF],
-                                               F meanwhile)
+                                               F meanwhile, int64_t split = 0)
 {
     using T = typename S::T;
     constexpr int RF = S::RF, NF = S::NF, KSTEP = S::KSTEP, VEC = S::VEC, ES = S::ES;
+    // fragments of one half, and of what an n-contiguous B's rows are read in
+    constexpr int HALVES = GATE ? 2 : 1, NH = NF / HALVES;
+    static_assert(!GATE || NF % 2 == 0, "halves");
     // the row (of A, or of a k-contiguous B) and chunk of 16 bytes that load t of
     // a batch takes within a fragment of 16 rows
     const int q_row = 4 * ((lane >> 2) & 3), q_chunk = 4 * (lane >> 4) + (lane & 3);
@@ -164,12 +172,12 @@ __device__ __forceinline__ void stream_product(const typename S::T* A, int64_t l
         for (int j = 0; j < NF; ++j)
 #pragma unroll
             for (int t = 0; t < 4; ++t)
-                off_b[j][t] = (uint32_t)(((int64_t)last(j * 16 + q_row + t, cols) * ldb +
+                off_b[j][t] = (uint32_t)(((last(j % NH * 16 + q_row + t, cols) + j / NH * split) * ldb +
                                           VEC * q_chunk) * ES);
     } else {
-        const int c = NF * (lane % 16);
+        const int c = NH * (lane % 16);
         off_b[0][0] = (uint32_t)(((int64_t)4 * VEC * (lane / 16) * ldb +
-                                  (c < cols ? c : cols - NF)) * ES);
+                                  (c < cols ? c : cols - NH)) * ES);
     }
     auto load = [&](StreamBatch<S>& x, int batch) __attribute__((always_inline)) {
         const int k = batch * 4 * KSTEP;
@@ -189,7 +197,10 @@ __device__ __forceinline__ void stream_product(const typename S::T* A, int64_t l
         } else {
 #pragma unroll
             for (int t = 0; t < 4; ++t)
-                load_rows<T, NF>(x.r[t], B + (int64_t)(k + VEC * t) * ldb, ldb, off_b[0][0]);
+#pragma unroll
+                for (int half = 0; half < HALVES; ++half)
+                    load_rows<T, NH>(x.r[t] + half * NH * 4,
+                                     B + (int64_t)(k + VEC * t) * ldb + half * split, ldb, off_b[0][0]);
         }
     };
     auto multiply = [&](StreamBatch<S>& x) __attribute__((always_inline)) {
@@ -204,13 +215,13 @@ __device__ __forceinline__ void stream_product(const typename S::T* A, int64_t l
             for (int j = 0; j < NF; ++j) {
                 u32x4 b;
                 if constexpr (S::KC) b = x.b[j][t];
-                else b = rows_fragment<T, NF>(x.r[t], j);
+                else b = rows_fragment<T, NH>(x.r[t] + j / NH * NH * 4, j % NH);
 #pragma unroll
                 for (int i = 0; i < RF; ++i) mfma16<T>(x.a[i][t], b, acc[i][j]);
             }
     };
     // whole batches of K, split evenly over the waves
-    const bool narrow = !S::KC && cols < S::BN && cols % NF != 0;
+    const bool narrow = !S::KC && cols < S::BN / HALVES && cols % NH != 0;
     const int steps = narrow ? 0 : K / KSTEP, batches = steps / 4;
     const int b_lo = (int)((int64_t)batches * wave / S::WAVES);
     const int b_hi = (int)((int64_t)batches * (wave + 1) / S::WAVES);
@@ -257,8 +268,10 @@ __device__ __forceinline__ void stream_product(const typename S::T* A, int64_t l
         uint32_t br[S::KC ? 1 : NF * 4];
         if constexpr (!S::KC)
             if (whole)
-                load_rows<T, NF>(br, B + (int64_t)t * KSTEP * ldb, ldb,
-                          off_b[0][0] - (uint32_t)((int64_t)3 * VEC * (lane / 16) * ldb * ES));
+#pragma unroll
+                for (int half = 0; half < HALVES; ++half)
+                    load_rows<T, NH>(br + half * NH * 4, B + (int64_t)t * KSTEP * ldb + half * split, ldb,
+                                     off_b[0][0] - (uint32_t)((int64_t)3 * VEC * (lane / 16) * ldb * ES));
 #pragma unroll
         for (int i = 0; i < RF; ++i) {
             const T* row = A + (int64_t)last(i * 16 + lane % 16, rows) * lda;
@@ -267,14 +280,17 @@ __device__ __forceinline__ void stream_product(const typename S::T* A, int64_t l
         }
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
-            const int c = last(S::column(j, lane % 16), cols);
+            const int c = last(GATE ? StreamConfig<T, S::KC, RF, NH>::column(j % NH, lane % 16)
+                                    : S::column(j, lane % 16), cols);
+            const int64_t far = j / NH * split;  // to the half of fragment j
             u32x4 fb;
             if constexpr (S::KC) {
-                const T* row = B + (int64_t)c * ldb;
+                const T* row = B + (c + far) * ldb;
                 fb = whole ? *reinterpret_cast<const u32x4_elem<T>*>(row + k)
                            : clamped_chunk<T>(row, 1, k, K);
             } else {
-                fb = whole ? rows_fragment<T, NF>(br, j) : clamped_chunk<T>(B + c, ldb, k, K);
+                fb = whole ? rows_fragment<T, NH>(br + j / NH * NH * 4, j % NH)
+                           : clamped_chunk<T>(B + c + far, ldb, k, K);
             }
 #pragma unroll
             for (int i = 0; i < RF; ++i) mfma16<T>(fa[i], fb, acc[i][j]);
@@ -479,6 +495,68 @@ __global__ __launch_bounds__(S::THREADS) void stream_kernel(RaggedArgs p)
                 continue;
             }
             store_piece(d, c, v, p.beta, col, n0, p.N);
+        }
+    });
+}
+
+// RAG_ACT and RAG_GATE: the same product, whose sums go through act_outputs.
+template <class S, typename OutT, bool GATE>
+__global__ __launch_bounds__(S::THREADS) void stream_act_kernel(ActArgs p)
+{
+    using T = typename S::T;
+    constexpr int RF = S::RF, HALVES = GATE ? 2 : 1, NH = S::NF / HALVES, BNO = 16 * NH;
+    using H = StreamConfig<T, S::KC, RF, NH>;  // one half's columns
+    constexpr int ITEMS = S::PF * NH * 64, IPT = (ITEMS + S::THREADS - 1) / S::THREADS;
+    __shared__ f32x4 part[S::WAVES][S::SLOTS][64];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int tm, tn;
+    if (!narrow_act<S::BM, T, OutT>(p, tm, tn)) return;
+    const int r0 = tm * S::BM, n0 = tn * BNO;
+    // with an n-contiguous B the last tile of a row moves back to end at column N
+    const int nb = S::KC || n0 + BNO <= p.N ? n0 : (p.N >= BNO ? p.N - BNO : 0);
+    const T* A = static_cast<const T*>(p.A) + (int64_t)r0 * p.lda;
+    const T* B = static_cast<const T*>(p.B) + (S::KC ? (int64_t)nb * p.ldb : nb);
+    const int rows = p.M - r0;
+
+    f32x4 acc[RF][S::NF] = {};
+    stream_product<S, GATE>(A, p.lda, rows, B, p.ldb, p.N - nb, p.K, wave, lane, acc, [] {},
+                            GATE ? p.N : 0);
+
+    static_for<S::PASSES>([&](auto pass_c) __attribute__((always_inline)) {
+        constexpr int pass = decltype(pass_c)::value;
+        if constexpr (pass > 0) __syncthreads();
+        static_for<S::SLOTS>([&](auto q_c) __attribute__((always_inline)) {
+            constexpr int slot = decltype(q_c)::value, i = pass * S::PF + slot / S::NF;
+            constexpr int half = slot % S::NF / NH, q = slot % NH;
+            f32x4 v;
+            if constexpr (S::KC) v = acc[i][half * NH + q];
+            else
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = acc[i][half * NH + (4 * q + e) % NH][(4 * q + e) / NH];
+            part[wave][slot][lane] = v;
+        });
+        __syncthreads();
+#pragma unroll
+        for (int h = 0; h < IPT; ++h) {
+            const int item = tid + h * S::THREADS, l = item & 63;
+            if (item >= ITEMS) break;
+            const int f = item / 64 / NH, q = item / 64 % NH, slot = f * S::NF + q;
+            const int row = (pass * S::PF + f) * 16 + l % 16, col = nb + H::slot_column(q, l);
+            if (row >= rows || col >= p.N) continue;
+            f32x4 g = part[0][slot][l], u{};
+#pragma unroll
+            for (int w = 1; w < S::WAVES; ++w) g += part[w][slot][l];
+            if constexpr (GATE) {
+                u = part[0][slot + NH][l];
+#pragma unroll
+                for (int w = 1; w < S::WAVES; ++w) u += part[w][slot + NH][l];
+            }
+            // (a tile that moved back computes its neighbour's columns again:
+            // those are not stored twice, since D may be R)
+            const int n = p.N - col, skip = n0 - col;
+            act_outputs<GATE, OutT>(p, r0 + row, col, n, g, u, act_bias<OutT>(p, col, n),
+                                    GATE ? act_bias<OutT>(p, p.N + col, n) : f32x4{}, skip);
         }
     });
 }

@@ -136,7 +136,8 @@ gemm_status_t gemm_run(gemm_handle_t h, gemm_op_t transA, gemm_op_t transB,
  *                aligned (GEMM_ERR_NOT_SUPPORTED otherwise).
  *   activation : GEMM_ACT_NONE; GEMM_ACT_RELU max(x, 0); GEMM_ACT_GELU
  *                x*Phi(x) = x/2 * (1 + erf(x/sqrt(2))) (the erf form).  Any
- *                other value: GEMM_ERR_INVALID_VALUE.
+ *                other value: GEMM_ERR_INVALID_VALUE (the activations beyond
+ *                these are gemm_run_grouped_act's).
  *   clamp      : nonzero clamps to [clamp_lo, clamp_hi]; clamp_lo > clamp_hi
  *                or a NaN bound: GEMM_ERR_INVALID_VALUE.
  * A NULL epilogue (or one with no bias, no activation and no clamp) is
@@ -151,7 +152,9 @@ gemm_status_t gemm_run(gemm_handle_t h, gemm_op_t transA, gemm_op_t transB,
 typedef enum {
     GEMM_ACT_NONE = 0,
     GEMM_ACT_RELU = 1,
-    GEMM_ACT_GELU = 2
+    GEMM_ACT_GELU = 2,
+    GEMM_ACT_SILU = 3,     /* gemm_run_grouped_act and its gradient only */
+    GEMM_ACT_GELU_TANH = 4 /* ... likewise */
 } gemm_activation_t;
 
 typedef struct {
@@ -472,6 +475,184 @@ typedef struct {
                                                   * of A op(down), and slices of K (else 0) */
 } gemm_group_launch_t;
 gemm_status_t gemm_last_group_launch(gemm_handle_t h, gemm_group_launch_t* out);
+
+/* ---- products with bias, activation, gate and residual --------------------
+ * What an expert's or a dense layer's product is followed by, in the product's
+ * epilogue, for the ragged groups of gemm_run_grouped, or with groups == NULL
+ * for one matrix and all M rows:
+ *     Z = alpha s_g A[rows of g] op(B_g) + bias_g
+ *     D[rows of g] = act(Z) + R               (Z, bias_g and op(B_g) of N columns)
+ * or, gated, with Z, bias_g and op(B_g) of 2 N columns, the gate's N before its
+ * partner's,
+ *     D[rows of g] = act(Z[:, :N]) * Z[:, N:] + R.
+ * All of it is formed in fp32 from the fp32 sums; D and Z are rounded once each,
+ * D from the unrounded Z.
+ *   activation : GEMM_ACT_NONE; RELU max(x, 0); GELU x Phi(x); SILU x s(x) with
+ *                s(x) = 1 / (1 + e^-x); GELU_TANH x s(2 sqrt(2/pi) (x + 0.044715
+ *                x^3)), which is x/2 (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))).
+ *   bias       : D's element type, group g's at g*stride_bias elements (>= 0; 0
+ *                shares one); or NULL.
+ *   Z          : M rows of ldz elements of D's type, for the backward pass; or NULL.
+ *   R          : M x N of D's type, the residual; or NULL.  D may be R (ldd == ldr);
+ *                any other overlap of D, Z, R and bias that something is written
+ *                to is rejected.
+ * An infinite or NaN Z gives what these formulas give: SILU of -inf is NaN.
+ * K == 0 or alpha == 0: Z = bias, and A and B are not read.  Rows in no group are
+ * not written.  Otherwise as gemm_run_grouped, with N up to 2^30 - 257, and gated
+ * B's panel of both halves below 4 GiB; D, Z, R and bias must be element-aligned
+ * (GEMM_ERR_NOT_SUPPORTED).  gemm_set_group_tile and gemm_last_group_launch serve
+ * this call too; a gated tile's columns are counted as D's. */
+typedef struct {
+    gemm_activation_t activation;
+    int gated;
+    const void* bias;
+    int64_t stride_bias;
+    void* Z;
+    int64_t ldz;
+    const void* R;
+    int64_t ldr;
+} gemm_act_t;
+
+gemm_status_t gemm_run_grouped_act(gemm_handle_t h, gemm_op_t transB, int64_t M, int64_t N, int64_t K,
+                                   float alpha, const void* A, int64_t lda, const void* B, int64_t ldb,
+                                   int64_t strideB, void* D, int64_t ldd, gemm_dtype_t dtype,
+                                   const gemm_groups_t* groups, const gemm_act_t* act,
+                                   hipStream_t stream);
+
+/* Its gradient, from the Z that it stored and D's gradient dD (both of D's type):
+ *     dZ = dD * act'(Z),                                   H = act(Z)
+ * or, gated, with Z = [G U] of 2 N columns,
+ *     dZ = [dD * U * act'(G), dD * act(G)],                H = act(G) * U.
+ * dZ and H (the product's result without R again, or NULL) have the operands'
+ * type, for the products that follow: gemm_run_grouped on dZ with the other
+ * transB is A's gradient, gemm_run_grouped_wgrad on A and dZ that of the B_g, and
+ * R's gradient is dD.  (relu' is 0 at 0.)  dbias, groups x the width of Z in
+ * fp32, not NULL: the sums of dZ's columns over each group's rows, formed from
+ * the unrounded dZ; an empty group's are 0.  It needs `workspace`, device memory
+ * of gemm_act_grad_workspace_bytes(M, width of Z, groups) bytes, 256-byte
+ * aligned (GEMM_ERR_INVALID_VALUE otherwise), which needs no clearing; calls that
+ * may overlap in time need one each.  dZ may be Z, and H may be dD, where they
+ * have one type and leading dimension; any other overlap of what is written is
+ * rejected.  Rows in no group are not written.  Results are bitwise reproducible. */
+size_t gemm_act_grad_workspace_bytes(int64_t M, int64_t width, int groups);
+
+gemm_status_t gemm_run_grouped_act_grad(gemm_handle_t h, int64_t M, int64_t N,
+                                        gemm_activation_t activation, int gated, const void* Z,
+                                        int64_t ldz, const void* dD, int64_t lddd, void* dZ,
+                                        int64_t lddz, void* H, int64_t ldh, float* dbias,
+                                        gemm_dtype_t dtype, const gemm_groups_t* groups, void* workspace,
+                                        size_t workspace_bytes, hipStream_t stream);
+
+/* ---- routing to experts -----------------------------------------------------
+ * From a router's logits x (tokens x experts) each token's `top` experts, their
+ * weights, and the plan of rows sorted by expert that the ragged products take.
+ *
+ * Scores are s = softmax(x) over the token's experts, or s = 1 / (1 + e^-x) each;
+ * the choice is by c = s + bias (fp32, experts entries on the device, or NULL:
+ * c = s), which balances the experts and has no part in the weights.  With groups
+ * > 1 the experts are `groups` runs of experts / groups neighbours, a group's score
+ * is its largest c (group_top 1) or the sum of its two largest (group_top 2; of
+ * its one where it has no second), and only the top_groups best groups' experts
+ * are chosen from; groups 0 or 1: no such step.  The `top` largest c are taken in
+ * descending order; of equals, also of groups, the lower index comes first.
+ * Scores next to each other decide, so c is compared in 64 bits; without a bias
+ * and with group_top 1 (or no groups) the logits themselves are, in whose order
+ * the scores are.
+ * The weights are scale * s, or with renormalize scale * s / (sum of the chosen s),
+ * in fp32 and formed so that no underflow of s spoils the ratio.
+ *
+ * An expert whose logit, or c, is NaN or -inf is not chosen; where fewer than
+ * `top` are left (none in a row of -inf that pads a batch), ids is -1 and the
+ * weight 0 in the places left.  Logits of +inf share a softmax among themselves.
+ *
+ * Logits are fp32, or bfloat16 with GEMM_DTYPE_BF16_BF16 (the type of D that
+ * `dtype` names), rows ld >= experts apart.  ids and weights: tokens x top, packed.
+ * The plan, NULL all three if not wanted: offsets (experts + 1) as gemm_groups_t
+ * takes them, order (tokens*top): row r of expert e, offsets[e] <= r <
+ * offsets[e+1], has assignment order[r] = t*top + j, an expert's in ascending order;
+ * -1 from offsets[experts] on; position (tokens*top): the row of each assignment,
+ * -1 where there is none.  It is formed with integers alone and in a fixed order.
+ *
+ * workspace: gemm_route_workspace_bytes(tokens, experts) bytes, 256-byte aligned, no
+ * clearing needed; calls that may overlap in time need one each.  It is needed
+ * with a plan of more than 16 tokens only.  None of these calls allocates or
+ * waits, and all can be captured.
+ *
+ * GEMM_ERR_INVALID_VALUE: a NULL that is needed, negative sizes, ld < experts,
+ * experts or top < 1, top > experts or than the kept groups hold, groups that do not
+ * divide experts, top_groups outside [1, groups], group_top other than 1 and 2, a
+ * scale that is not finite, part of a plan, too small a workspace.
+ * GEMM_ERR_NOT_SUPPORTED: experts > 1024, top > 32, groups > 64, tokens above 2^26 -
+ * 64, ld above 2^31 - 1, pointers that are not element-aligned. */
+typedef enum { GEMM_SCORES_SOFTMAX = 0, GEMM_SCORES_SIGMOID = 1 } gemm_scores_t;
+
+typedef struct {
+    int experts, top;
+    gemm_scores_t scores;
+    int groups, top_groups, group_top;
+    const float* bias; /* device, experts; or NULL */
+    int renormalize;
+    float scale;
+} gemm_routing_t;
+
+size_t gemm_route_workspace_bytes(int64_t tokens, int experts);
+
+gemm_status_t gemm_route(gemm_handle_t h, int64_t tokens, const void* logits, int64_t ld,
+                         gemm_dtype_t dtype, const gemm_routing_t* routing, int32_t* ids, float* weights,
+                         int32_t* offsets, int32_t* order, int32_t* position, void* workspace,
+                         size_t workspace_bytes, hipStream_t stream);
+
+/* The weights' gradient carried back to the logits, for the experts in ids (the
+ * choice itself has no gradient): with g the gradient of the weights, c the scale
+ *     softmax                dx_e = c s_e (g_e - sum_j g_j s_j)      (g_e 0 unless chosen)
+ *     softmax, renormalised  dx_j = c q_j (g_j - sum_l g_l q_l),  q_j = s_j / sum_l s_l
+ *     sigmoid                dx_j = c s_j (1 - s_j) g_j
+ *     sigmoid, renormalised  dx_j = c q_j (1 - s_j) (g_j - sum_l g_l q_l)
+ * and 0 for the others.  Of `routing` experts, top, scores, renormalize and scale
+ * are read.  dlogits (rows ldd >= experts apart) has the logits' type and may not
+ * overlap them; every one of its tokens x experts elements is written.  ids outside
+ * [0, experts) have no part; an expert named twice gets the sum. */
+gemm_status_t gemm_route_grad(gemm_handle_t h, int64_t tokens, const void* logits, int64_t ld,
+                              gemm_dtype_t dtype, const gemm_routing_t* routing, const int32_t* ids,
+                              const float* dweights, void* dlogits, int64_t ldd, hipStream_t stream);
+
+/* ---- rows to their experts and back ----------------------------------------
+ * By the plan of gemm_route, with `rows` rows sorted by expert (up to tokens*top)
+ * of `cols` columns.  dtype names the types of operands (X, Y, dY) and outputs (D,
+ * C, dD) as for gemm_run; sums are fp32 and rounded once.
+ *   gemm_gather_rows       : D[r] = X[order[r] / top], times weights[order[r]]
+ *                            unless weights (tokens*top) is NULL.  A row whose order
+ *                            lies outside [0, tokens*top) is left as it was.
+ *   gemm_combine_rows      : D[t] = sum_j weights[t,j] Y[position[t,j]] + beta C[t]
+ *                            (weights NULL: 1), the sum in the order of j.  C is as
+ *                            in gemm_run: not read with beta == 0, and D may be C.
+ *   gemm_combine_rows_grad : dY[position[t,j]] = weights[t,j] dD[t] and
+ *                            dweights[t,j] = <Y[position[t,j]], dD[t]>; rows of dY
+ *                            that no position names are left as they were.  dY may be
+ *                            Y (one leading dimension).  C's gradient is beta dD.
+ * A position outside [0, rows) has no part and a dweights of 0, whatever the rows
+ * hold; a row that several positions name is summed from each, and its dY is
+ * undefined.  The gradient of gather is combine without weights (and gather of dD
+ * with weights is the dY above).
+ * GEMM_ERR_INVALID_VALUE: negative sizes, top < 1, leading dimensions below cols,
+ * a NULL that is needed, outputs that overlap operands otherwise than said.
+ * GEMM_ERR_NOT_SUPPORTED: tokens or rows of 2^24 or more, tokens*top above 2^31 - 1,
+ * cols above 65535 * 1024, pointers that are not element-aligned.
+ * Results are bitwise reproducible; nothing is allocated or waited for. */
+gemm_status_t gemm_gather_rows(gemm_handle_t h, int64_t tokens, int64_t cols, int top, const void* X,
+                               int64_t ldx, int64_t rows, const int32_t* order, const float* weights,
+                               void* D, int64_t ldd, gemm_dtype_t dtype, hipStream_t stream);
+
+gemm_status_t gemm_combine_rows(gemm_handle_t h, int64_t tokens, int64_t cols, int top, const void* Y,
+                                int64_t ldy, int64_t rows, const int32_t* position,
+                                const float* weights, float beta, const void* C, int64_t ldc, void* D,
+                                int64_t ldd, gemm_dtype_t dtype, hipStream_t stream);
+
+gemm_status_t gemm_combine_rows_grad(gemm_handle_t h, int64_t tokens, int64_t cols, int top,
+                                     const void* Y, int64_t ldy, int64_t rows, const int32_t* position,
+                                     const float* weights, const void* dD, int64_t lddd, void* dY,
+                                     int64_t lddy, float* dweights, gemm_dtype_t dtype,
+                                     hipStream_t stream);
 
 #ifdef __cplusplus
 }
