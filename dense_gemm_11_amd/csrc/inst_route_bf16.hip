@@ -3,6 +3,6 @@
 
 namespace dg {
 
-RouteFn route_fn_bf16(bool lanes64, int v, bool wide) { return route_fn<bf16_t>(lanes64, v, wide); }
+RouteFn route_fn_bf16(bool lanes64, int v, bool bias) { return route_fn<bf16_t>(lanes64, v, bias); }
 
 }  // namespace dg

@@ -3,6 +3,6 @@
 
 namespace dg {
 
-RouteFn route_fn_f32(bool lanes64, int v, bool wide) { return route_fn<float>(lanes64, v, wide); }
+RouteFn route_fn_f32(bool lanes64, int v, bool bias) { return route_fn<float>(lanes64, v, bias); }
 
 }  // namespace dg

@@ -6,17 +6,26 @@
 // weights are scale * s, or scale * s over the sum of the chosen s.
 //
 // Scores next to each other decide what is chosen, so c is compared in 64 bits;
-// without a bias (and without sums of two scores) the logits themselves are
-// compared, whose order is that of the scores.  The weights are formed in fp32
-// from the logits of the chosen.  A logit (or c) of -inf or NaN is never chosen;
-// of +inf the softmax is its limit.
+// without a bias the logits themselves are compared, whose order is that of the
+// scores.  The weights are formed in fp32 from the logits of the chosen.  A logit
+// (or c) of -inf or NaN is never chosen; of +inf the softmax is its limit.
 //
-// L lanes hold a token, V experts each, in the experts' order, so the lowest
-// index among equals is that of the lowest lane.  Each of the `top` rounds takes
-// the largest of the lanes' maxima (4 exchanges within 16 lanes) and only then
-// does the lane that held it look for its next.  Four tokens to a wave (L = 16)
-// take a quarter of the rounds' instructions; a wave to a token (L = 64) is
-// quicker where there are few tokens.
+// L lanes hold a token, V experts each, in the experts' order.  Each of the `top`
+// rounds takes the largest of the lanes' maxima (4 exchanges within 16 lanes) and
+// strikes it out.  Four tokens to a wave (L = 16) share the rounds' instructions,
+// which are what bounds the launch (16384 tokens of 256 experts, in groups and with
+// a bias, top 8: 1340 a wave, 18.7 us; the bytes alone would take 3.5).
+//
+// route_quick does so on 32-bit integers in the order of the values with the
+// expert's place in their low bits, so that no two are equal, striking out takes a
+// compare and a select for each, and every lane knows the expert.  bf16 logits
+// leave 16 bits free; of others the places take the last 8 or so.  Where two
+// neighbours among the chosen (or the last of them and the next) are closer than
+// what is cut off, or scores closer than their fp32 errors, the token's candidates,
+// one to a lane, are compared for certain (route_rank).  A token for which that is
+// not enough (three so close, sums of groups, a softmax with a bias) is chosen for
+// again in 64 bits by a wave of its own once its workgroup is done with the others
+// (route_exact).
 #pragma once
 
 #include "common.hpp"
@@ -27,6 +36,7 @@ namespace dg {
 
 constexpr int ROUTE_MAX_EXPERTS = 1024, ROUTE_MAX_TOP = 32;
 constexpr int ROUTE_CHUNK = 64;    // tokens whose experts are counted together, at most
+constexpr int ROUTE_ONE = 128;     // ... by a single workgroup, which makes the plan
 constexpr int ROUTE_SUPER = 256;   // chunks whose counts are added up for the others
 
 struct RouteArgs {
@@ -119,87 +129,348 @@ __device__ __forceinline__ void wave_sync()
 __device__ __forceinline__ float exp_below(float x, float m) { return x == m ? 1.0f : expf(x - m); }
 __device__ __forceinline__ double exp_below(double x, double m) { return x == m ? 1.0 : exp(x - m); }
 
+// V values from x, `count` of them (V: as vectors), the others `rest`.
+template <int V, typename X>
+__device__ __forceinline__ void load_part(float (&v)[V], const X* x, int count, float rest)
+{
+    if (count == V && V >= 4) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            if constexpr (sizeof(X) == 4) {
+                const f32x4 r = *reinterpret_cast<const f32x4_a4*>(x + i);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (i + q < V) v[i + q] = r[q];
+            } else {
+                const u16x4 r = *reinterpret_cast<const u16x4_a2*>(x + i);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (i + q < V) v[i + q] = to_f32((bf16_t)r[q]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = i < count ? to_f32(x[i]) : rest;
+    }
+}
+
+// A lane's part of a token: V experts from e0, `count` of them, and their logits
+// (-inf beyond, and for NaN, which is as little a choice).
+template <typename X, int L, int V>
+struct TokenPart {
+    int e0, count, group;
+    float x[V];
+
+    __device__ __forceinline__ TokenPart(const RouteArgs& p, int group_lanes, int t, bool live)
+    {
+        const int sub = threadIdx.x & (L - 1);
+        const int log = __builtin_ctz(group_lanes), part = sub & (group_lanes - 1);
+        group = sub >> log;
+        e0 = group * p.group_size + part * V;
+        count = group < p.groups && live ? p.group_size - part * V : 0;
+        count = count < 0 ? 0 : count > V ? V : count;
+        load_part(x, static_cast<const X*>(p.logits) + (int64_t)(live ? t : 0) * p.ld + (count > 0 ? e0 : 0),
+                  count, -__builtin_inff());
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = fmaxf(x[i], -__builtin_inff());
+    }
+    // The expert in place n = V * lane + i of the token's lanes.
+    __device__ static __forceinline__ int expert_at(const RouteArgs& p, int group_lanes, int n)
+    {
+        const int lane = n / V, log = __builtin_ctz(group_lanes);
+        return (lane >> log) * p.group_size + (lane & (group_lanes - 1)) * V + n % V;
+    }
+    // The token's largest logit, and the sum of e^(x - most) where weights need it.
+    __device__ __forceinline__ void sums(const RouteArgs& p, float& most, float& total) const;
+};
+
+// An unsigned integer in the order of x, and back.  Below LEAST: -inf, or nothing.
+__device__ __forceinline__ uint32_t order_key(float x)
+{
+    const int i = __float_as_int(x);
+    return (uint32_t)i ^ ((uint32_t)(i >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k)
+{
+    return __uint_as_float(k ^ (~(uint32_t)((int)k >> 31) | 0x80000000u));
+}
+constexpr uint32_t LEAST = 0x00800000u;
+
+__device__ __forceinline__ uint32_t least_of(uint32_t a, uint32_t b) { return a < b ? a : b; }
+__device__ __forceinline__ uint32_t most_of(uint32_t a, uint32_t b) { return a > b ? a : b; }
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t x)
+{
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xf, 0xf, true);
+}
+
+// op (least_of or most_of) over the lane's L lanes.
+template <int L, class F>
+__device__ __forceinline__ uint32_t lanes_pick(uint32_t k, F op)
+{
+    k = op(k, dpp<0xB1>(k));
+    k = op(k, dpp<0x4E>(k));
+    k = op(k, dpp<0x141>(k));
+    k = op(k, dpp<0x140>(k));
+    if constexpr (L == 64)
+        k = op(op((uint32_t)__builtin_amdgcn_readlane((int)k, 0), (uint32_t)__builtin_amdgcn_readlane((int)k, 16)),
+               op((uint32_t)__builtin_amdgcn_readlane((int)k, 32), (uint32_t)__builtin_amdgcn_readlane((int)k, 48)));
+    return k;
+}
+template <int L>
+__device__ __forceinline__ uint32_t lanes_most(uint32_t k)
+{
+    return lanes_pick<L>(k, [](uint32_t a, uint32_t b) { return most_of(a, b); });
+}
+
+// The second of three where a >= b are two of them: of a, b and c.
+__device__ __forceinline__ uint32_t second_of(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t r;
+    asm("v_med3_u32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+
+// The lane's L lanes' part of a mask over the wave.
+template <int L>
+__device__ __forceinline__ uint64_t lanes_mask(uint64_t m, int lane)
+{
+    return L == 64 ? m : m >> (lane & 48) & 0xFFFFu;
+}
+
+// The largest two of a group's keys, from its lanes' (a >= b).
+__device__ __forceinline__ void group_two(int lanes, uint32_t& a, uint32_t& b)
+{
+    auto join = [&](uint32_t a2, uint32_t b2) __attribute__((always_inline)) {
+        b = most_of(least_of(a, a2), most_of(b, b2));
+        a = most_of(a, a2);
+    };
+    if (lanes > 1) join(dpp<0xB1>(a), dpp<0xB1>(b));
+    if (lanes > 2) join(dpp<0x4E>(a), dpp<0x4E>(b));
+    if (lanes > 4) join(dpp<0x141>(a), dpp<0x141>(b));
+    if (lanes > 8) join(dpp<0x140>(a), dpp<0x140>(b));
+    if (lanes > 16) join(__shfl_xor(a, 16), __shfl_xor(b, 16));
+    if (lanes > 32) join(__shfl_xor(a, 32), __shfl_xor(b, 32));
+}
+
+__device__ __forceinline__ float quick_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
+// 1 / (1 + e^-x)
+__device__ __forceinline__ float quick_sigmoid(float x)
+{
+    return __builtin_amdgcn_rcpf(1.0f + quick_exp(-x));
+}
+__device__ __forceinline__ float quick_exp_below(float x, float m) { return x == m ? 1.0f : quick_exp(x - m); }
+
+template <typename X, int L, int V>
+__device__ __forceinline__ void TokenPart<X, L, V>::sums(const RouteArgs& p, float& most, float& total) const
+{
+    most = x[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) most = x[i] > most ? x[i] : most;
+    most = key_value(lanes_most<L>(order_key(most)));
+    total = 1.0f;
+    if (!p.sigmoid && !p.renormalize) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) s += x[i] > -__builtin_inff() ? quick_exp_below(x[i], most) : 0.0f;
+        total = lanes_sum<L>(s);
+    }
+}
+
 // A token's chosen logit as a score: softmax over all (e^(x - m) / sum), or with
 // renormalised weights a number in proportion to it, of which the largest is
 // about 1 (m the largest chosen logit): e^(x - m); e^(x - m) / (1 + e^x) for the
 // sigmoid of logits below zero, whose own value may be too small for fp32.
 __device__ __forceinline__ float chosen_score(const RouteArgs& p, float x, float m)
 {
-    if (!p.sigmoid) return exp_below(x, m);
-    if (!p.renormalize || x > 0.0f) return 1.0f / (1.0f + expf(-x));
-    return expf(x - fminf(m, 0.0f)) / (1.0f + expf(x));
+    if (!p.sigmoid) return quick_exp_below(x, m);
+    if (!p.renormalize || x > 0.0f) return quick_sigmoid(x);
+    return quick_exp(x - fminf(m, 0.0f)) * __builtin_amdgcn_rcpf(1.0f + quick_exp(x));
 }
 
-// Tokens t0 .. of the workgroup's pass, one per L lanes: chooses their experts
-// into picked[token of the pass][j] and writes ids and weights.
-template <typename X, int L, int V, typename K>
-__device__ __forceinline__ void route_token(const RouteArgs& p, int t, bool live,
-                                            int32_t* picked)
+// How far a token's choice is certain.
+enum : int { ROUTE_SURE = 0, ROUTE_RANK = 1, ROUTE_AGAIN = 2 };
+
+// Chooses a token's experts: the j-th of them, and the one after the last, to lane
+// j of its L lanes (-1: none), and returns how certain that is, in every lane.
+// BIAS: by scores with a bias, which it forms in fp32.  In units u of 2^-24 a
+// sigmoid is off by 4 at most and the sum c with the bias by |c| more, so two
+// choices may be in the wrong order up to 8 + 2 |c| apart.  A softmax is off by
+// |x - m| e^(x - m) <= 0.37 for its argument and 4 p for its exponential and
+// products, and its sum by 49 of itself at most (of which 38 are additions), which
+// shifts two choices against each other by 49 of the largest p: 0.8 + 57 p + 2 |c|.
+// `close` times 1 + |c| is more than that, and twice it more than what sums of two
+// choices are off by.
+template <typename X, int L, int V, bool BIAS>
+__device__ __forceinline__ int route_quick(const RouteArgs& p, const TokenPart<X, L, V>& in, float most,
+                                           int& expert)
 {
+    constexpr int BITS = sizeof(X) == 2 && !BIAS ? 16 : __builtin_ctz(L * V);
+    constexpr uint32_t PLACES = (1u << BITS) - 1u;
+    constexpr bool WHOLE = BITS == 16;  // nothing of the value is cut off
     const int lane = threadIdx.x & 63, sub = lane & (L - 1);
-    const X* row = static_cast<const X*>(p.logits) + (int64_t)(live ? t : 0) * p.ld;
-    // the lane's experts
-    const int group = sub / p.lanes_per_group, part = sub % p.lanes_per_group;
-    const int e0 = group * p.group_size + part * V;
-    int count = group < p.groups && live ? p.group_size - part * V : 0;
-    count = count < 0 ? 0 : count > V ? V : count;
-    float x[V];
-    if (count == V && V >= 4) {
+    float close = 0x1p-20f;
+    auto apart = [&](float a, float b, float times) __attribute__((always_inline)) {
+        return a - b > times * close * (1.0f + fmaxf(fabsf(a), fabsf(b)));
+    };
+    bool again = false;
+    uint32_t c[V];
+    if constexpr (BIAS) {
+        float s[V], b[V];
+        load_part(b, p.bias + (in.count > 0 ? in.e0 : 0), in.count, 0.0f);
+        if (p.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < V; i += 4) {
-            if constexpr (sizeof(X) == 4) {
-                const f32x4 v = *reinterpret_cast<const f32x4_a4*>(row + e0 + i);
+            for (int i = 0; i < V; ++i) s[i] = quick_sigmoid(in.x[i]);
+        } else {
+            float sum = 0.0f;
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (i + q < V) x[i + q] = v[q];
-            } else {
-                const u16x4 v = *reinterpret_cast<const u16x4_a2*>(row + e0 + i);
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (i + q < V) x[i + q] = to_f32((bf16_t)v[q]);
+            for (int i = 0; i < V; ++i) {
+                s[i] = in.x[i] > -__builtin_inff() ? quick_exp_below(in.x[i], most) : 0.0f;
+                sum += s[i];
             }
-        }
-    } else {
+            sum = 1.0f / lanes_sum<L>(sum);  // the largest p
+            close = 0x1p-24f * (2.0f + 64.0f * sum);
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = i < count ? to_f32(row[e0 + i]) : -__builtin_inff();
-    }
-    // NaN is as little a choice as -inf
-    float most = -__builtin_inff();
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        x[i] = x[i] > -__builtin_inff() ? x[i] : -__builtin_inff();
-        most = fmaxf(most, x[i]);
-    }
-    most = lanes_max<L>(most);
-    float total = 1.0f;
-    if (!p.sigmoid && !p.renormalize) {
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) s += x[i] > -__builtin_inff() ? exp_below(x[i], most) : 0.0f;
-        total = lanes_sum<L>(s);
-    }
-    K c[V];
-    if constexpr (sizeof(K) == 4) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) c[i] = x[i];
-    } else {
-        double sum = 1.0;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            c[i] = p.sigmoid ? 1.0 / (1.0 + exp(-(double)x[i]))
-                   : x[i] > -__builtin_inff() ? exp_below((double)x[i], (double)most) : 0.0;
-        if (!p.sigmoid) {
-            sum = 0.0;
-#pragma unroll
-            for (int i = 0; i < V; ++i) sum += c[i];
-            sum = lanes_sum<L>(sum);
+            for (int i = 0; i < V; ++i) s[i] *= sum;
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if (!p.sigmoid) c[i] /= sum;
-            if (p.bias) c[i] += i < count ? (double)p.bias[e0 + i] : 0.0;
-            c[i] = x[i] > -__builtin_inff() && c[i] > key_low<K>() ? c[i] : key_low<K>();
+            // (0 + -0 is 0; a NaN becomes -inf)
+            const float v = in.x[i] > -__builtin_inff() ? s[i] + b[i] : -__builtin_inff();
+            c[i] = order_key(fmaxf(v, -__builtin_inff()));
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) c[i] = order_key(in.x[i] + 0.0f);  // -0 is 0
+    }
+    if (p.groups > 1) {
+        uint32_t a = c[0], b = 0;
+#pragma unroll
+        for (int i = 1; i < V; ++i) {
+            b = second_of(a, b, c[i]);
+            a = most_of(a, c[i]);
+        }
+        group_two(p.lanes_per_group, a, b);
+        const bool sums = p.group_top > 1;
+        uint32_t score = a;
+        if (sums && a >= LEAST) {
+            // (without a bias: of the two logits' scores, a softmax's up to its sum)
+            float f = key_value(a), g = key_value(b);
+            if constexpr (!BIAS) {
+                f = p.sigmoid ? quick_sigmoid(f) : quick_exp_below(f, most);
+                g = p.sigmoid ? quick_sigmoid(g) : quick_exp_below(g, most);
+            }
+            score = order_key(b >= LEAST ? f + g : f);
+        }
+        bool kept = false;
+        uint32_t m = 0;
+        for (int j = 0; j < p.top_groups; ++j) {
+            m = lanes_most<L>(kept ? 0u : score);
+            kept |= score == m && m >= LEAST;
+        }
+        // equal scores went in together; where that is too many, and where rounded
+        // ones are as good as equal, 64 bits or the groups' order decide
+        again = __popcll(lanes_mask<L>(__ballot(kept), lane)) > p.top_groups * p.lanes_per_group;
+        if (BIAS || sums) {
+            const uint32_t next = lanes_most<L>(kept ? 0u : score);
+            again |= next >= LEAST && !apart(key_value(m), key_value(next), 2.0f);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) c[i] = kept ? c[i] : 0u;
+    }
+    // the places, and the keys' distance below each choice: those not below it wrap
+    // round to large numbers, so the least is the next choice's
+    const uint32_t place = PLACES - V * sub;
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = (c[i] & ~PLACES) + (place - i);
+    uint32_t m = 0, mine = 0, chosen_last = 0;
+    bool rank = false;
+    const int rounds = p.top + (WHOLE ? 0 : 2);
+    for (int j = 0; j < rounds; ++j) {
+        const uint32_t last = m;
+        uint32_t d = last - 1u - c[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) d = least_of(d, last - 1u - c[i]);
+        m = last - 1u - lanes_pick<L>(d, [](uint32_t a, uint32_t b) { return least_of(a, b); });
+        mine = sub == j ? m : mine;
+        if constexpr (!WHOLE) {
+            // what the one before is at the least and this one at the most
+            auto sure = [&](uint32_t hi) __attribute__((always_inline)) {
+                if constexpr (BIAS) return apart(key_value(hi & ~PLACES), key_value(m | PLACES), 1.0f);
+                else return (hi & ~PLACES) > (m | PLACES);
+            };
+            if (j <= p.top) rank |= j > 0 && m >= LEAST && !sure(last);
+            else again |= rank && m >= LEAST && !sure(chosen_last);
+            chosen_last = j == p.top - 1 ? m : chosen_last;
+        }
+    }
+    if (BIAS && !p.sigmoid) again |= rank;
+    expert = mine < LEAST ? -1 : TokenPart<X, L, V>::expert_at(p, p.lanes_per_group, PLACES - (mine & PLACES));
+    return again ? ROUTE_AGAIN : rank ? ROUTE_RANK : ROUTE_SURE;
+}
+
+// Puts the candidates of lanes 0 .. top (one more than are chosen) in their order,
+// of logits or of sigmoids with a bias in 64 bits; c: the lane's.
+template <int L>
+__device__ __forceinline__ int route_rank(const RouteArgs& p, int expert, double c, int32_t* picked)
+{
+    const int lane = threadIdx.x & 63, sub = lane & (L - 1);
+    const bool in = sub <= p.top && expert >= 0;
+    c = in ? c : key_low<double>();
+    const int e = in ? expert : 0x7FFFFFFF;
+    int before = 0;  // candidates ahead of the lane's
+    auto meet = [&](double c2, int e2) __attribute__((always_inline)) {
+        before += c2 > c || (c2 == c && e2 < e);
+    };
+    if constexpr (L == 16) {
+        static_for<15>([&](auto q_c) __attribute__((always_inline)) {
+            constexpr int ROR = 0x121 + decltype(q_c)::value;  // row_ror: 1 to 15
+            meet(dpp<ROR>(c), __builtin_amdgcn_mov_dpp(e, ROR, 0xf, 0xf, true));
+        });
+    } else {
+        for (int q = 0; q <= p.top; ++q)
+            meet(__hiloint2double(__builtin_amdgcn_readlane(__double2hiint(c), q),
+                                  __builtin_amdgcn_readlane(__double2loint(c), q)),
+                 __builtin_amdgcn_readlane(e, q));
+    }
+    if (sub < p.top) picked[sub] = -1;
+    wave_sync();
+    if (in && before < p.top) picked[before] = expert;
+    wave_sync();
+    return sub < p.top ? picked[sub] : -1;
+}
+
+// The same, certain of every case: scores with a bias and groups' sums in 64 bits,
+// the lowest number first among equals.
+template <typename X, int L, int V, bool BIAS>
+__device__ __forceinline__ void route_exact(const RouteArgs& p, int group_lanes,
+                                            const TokenPart<X, L, V>& in, float most, int32_t* picked)
+{
+    using K = std::conditional_t<BIAS, double, float>;
+    const int lane = threadIdx.x & 63;
+    // 1 / (1 + e^-x), or e^(x - most)
+    auto score_of = [&](float x) __attribute__((always_inline)) -> double {
+        return p.sigmoid ? 1.0 / (1.0 + exp(-(double)x))
+               : x > -__builtin_inff() ? exp_below((double)x, (double)most) : 0.0;
+    };
+    K c[V];
+    if constexpr (BIAS) {
+        double sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            c[i] = score_of(in.x[i]);
+            sum += c[i];
+        }
+        if (!p.sigmoid) sum = lanes_sum<L>(sum);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (!p.sigmoid) c[i] /= sum;
+            c[i] += i < in.count ? (double)p.bias[in.e0 + i] : 0.0;
+            c[i] = in.x[i] > -__builtin_inff() && c[i] > key_low<K>() ? c[i] : key_low<K>();
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) c[i] = in.x[i];
     }
     if (p.groups > 1) {
         K a = key_low<K>(), b = key_low<K>();  // the group's two largest
@@ -208,17 +479,22 @@ __device__ __forceinline__ void route_token(const RouteArgs& p, int t, bool live
             b = max_of(b, c[i] < a ? c[i] : a);
             a = max_of(a, c[i]);
         }
-        for (int d = 1; d < p.lanes_per_group; d *= 2) {
+        for (int d = 1; d < group_lanes; d *= 2) {
             const K a2 = __shfl_xor(a, d), b2 = __shfl_xor(b, d);
             b = max_of(a < a2 ? a : a2, max_of(b, b2));
             a = max_of(a, a2);
         }
-        K score = p.group_top > 1 && b > key_low<K>() ? a + b : a;
+        double score = a;
+        if (p.group_top > 1 && a > key_low<K>()) {
+            // (without a bias: of logits' scores, a softmax's up to its sum)
+            score = BIAS ? (double)a : score_of((float)a);
+            if (b > key_low<K>()) score += BIAS ? (double)b : score_of((float)b);
+        }
         bool kept = false;
         for (int j = 0; j < p.top_groups; ++j) {
-            const K best = lanes_max<L>(kept ? key_low<K>() : score);
+            const double best = lanes_max<L>(kept ? key_low<double>() : score);
             const int first = first_lane<L>(!kept && score == best, lane);
-            kept |= group == (first & (L - 1)) / p.lanes_per_group && first < 64;
+            kept |= in.group == (first & (L - 1)) / group_lanes && first < 64;
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) c[i] = kept ? c[i] : key_low<K>();
@@ -241,43 +517,55 @@ __device__ __forceinline__ void route_token(const RouteArgs& p, int t, bool live
         const int first = first_lane<L>(best == m, lane);
         if (lane == first) {
             const bool any = m > key_low<K>();
-            picked[j] = any ? e0 + at : -1;
+            picked[j] = any ? in.e0 + at : -1;
 #pragma unroll
             for (int i = 0; i < V; ++i) c[i] = any && i == at ? key_low<K>() : c[i];
             look();
         }
     }
-    wave_sync();
-    // the weights, one per lane
-    const int e = sub < p.top ? picked[sub] : -1;
-    const float xe = e >= 0 ? to_f32(row[e]) : -__builtin_inff();
-    const float m = p.renormalize ? lanes_max<L>(xe) : most;
-    float w = e >= 0 ? chosen_score(p, xe, m) : 0.0f;
-    if (p.renormalize) total = lanes_sum<L>(w);
-    if (live && sub < p.top) {
-        const int64_t o = (int64_t)t * p.top + sub;
-        p.ids[o] = e;
-        p.weights[o] = e >= 0 ? w / total * p.scale : 0.0f;
-    }
 }
 
 // Which of a chunk's tokens chose an expert, as bits.
-struct ChosenBits {
-    uint32_t w[ROUTE_MAX_EXPERTS][2];
+struct __attribute__((aligned(16))) ChosenBits {
+    uint32_t w[ROUTE_MAX_EXPERTS][ROUTE_ONE / 32];
 };
 __device__ __forceinline__ void clear_bits(ChosenBits& b, int experts)
 {
-    for (int e = threadIdx.x; e < experts; e += blockDim.x) b.w[e][0] = b.w[e][1] = 0;
+    for (int e = threadIdx.x; e < experts; e += blockDim.x) *reinterpret_cast<u32x4*>(b.w[e]) = u32x4{};
 }
 __device__ __forceinline__ int count_bits(const ChosenBits& b, int e)
 {
-    return __popc(b.w[e][0]) + __popc(b.w[e][1]);
+    const u32x4 w = *reinterpret_cast<const u32x4*>(b.w[e]);
+    return __popc(w[0]) + __popc(w[1]) + __popc(w[2]) + __popc(w[3]);
 }
 // ... of those before token t of the chunk.
 __device__ __forceinline__ int rank_bits(const ChosenBits& b, int e, int t)
 {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(b.w[e]);
     const uint32_t below = (1u << (t & 31)) - 1u;
-    return t < 32 ? __popc(b.w[e][0] & below) : __popc(b.w[e][0]) + __popc(b.w[e][1] & below);
+    int n = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) n += __popc(t >= 32 * (q + 1) ? w[q] : t >= 32 * q ? w[q] & below : 0u);
+    return n;
+}
+
+// Writes ids and weights of token t (i of its chunk), lane j of its L lanes those of
+// choice j, `expert`, and notes them in `bits` for a plan.
+template <typename X, int L>
+__device__ __forceinline__ void route_finish(const RouteArgs& p, int t, int i, bool live, float most,
+                                             float total, int expert, ChosenBits& bits)
+{
+    const int sub = threadIdx.x & (L - 1);
+    const int e = live && sub < p.top ? expert : -1;
+    const float x = e >= 0 ? to_f32(static_cast<const X*>(p.logits)[(int64_t)t * p.ld + e]) : -__builtin_inff();
+    const float m = p.renormalize ? lanes_max<L>(x) : most;
+    const float w = e >= 0 ? chosen_score(p, x, m) : 0.0f;
+    if (p.renormalize) total = lanes_sum<L>(w);
+    if (!live || sub >= p.top) return;
+    const int64_t o = (int64_t)t * p.top + sub;
+    p.ids[o] = e;
+    p.weights[o] = e >= 0 ? w * __builtin_amdgcn_rcpf(total) * p.scale : 0.0f;
+    if (p.order && e >= 0) atomicOr(&bits.w[e][i >> 5], 1u << (i & 31));
 }
 
 // Exclusive sum of n[0 .. experts) in place, the total to *total; ends with a
@@ -304,43 +592,68 @@ __device__ __forceinline__ void scan_experts(int* n, int experts, int* wave_sum,
     __syncthreads();
 }
 
-// Rows of the chunk's assignments: expert e's begin at start[e].
-__device__ __forceinline__ void place_rows(const RouteArgs& p, int t0, int tokens, const ChosenBits& bits,
-                                           const int* start)
+// The row of the chunk's assignment i, of expert e, whose rows begin at start[e].
+__device__ __forceinline__ void place_row(const RouteArgs& p, int t0, int i, int e, const ChosenBits& bits,
+                                          const int* start)
 {
-    for (int i = threadIdx.x; i < tokens * p.top; i += blockDim.x) {
-        const int64_t a = (int64_t)t0 * p.top + i;
-        const int e = p.ids[a];
-        const int r = e >= 0 ? start[e] + rank_bits(bits, e, i / p.top) : -1;
-        p.position[a] = r;
-        if (e >= 0) p.order[r] = (int32_t)a;
-    }
+    const int64_t a = (int64_t)t0 * p.top + i;
+    const int r = e >= 0 ? start[e] + rank_bits(bits, e, i / p.top) : -1;
+    p.position[a] = r;
+    if (e >= 0) p.order[r] = (int32_t)a;
 }
 
-// Chooses the experts of `chunk` tokens per workgroup.  PLAN: counts them by
+// Chooses the experts of `chunk` tokens per workgroup.  With a plan: counts them by
 // expert for route_place, or (a single workgroup) makes the plan at once.
-template <typename X, int L, int V, typename K>
+template <typename X, int L, int V, bool BIAS>
 __global__ __launch_bounds__(1024) void route_kernel(RouteArgs p)
 {
-    const int threads = blockDim.x, pass = threads / L;  // tokens at a time
+    constexpr int VX = V * L >= 4 * 64 ? V * L / 64 : V * L >= 2 * 64 ? 2 : 1;  // a wave to a token
+    const int threads = blockDim.x, pass = threads / L;                         // tokens at a time
     __shared__ int32_t picked[1024 / L][ROUTE_MAX_TOP];
     __shared__ ChosenBits bits;
     __shared__ int start[ROUTE_MAX_EXPERTS];
-    __shared__ int wave_sum[16], total;
+    __shared__ int wave_sum[16], total_rows;
+    __shared__ int again[ROUTE_ONE], again_count;
     const bool plan = p.order != nullptr;
     const int t0 = blockIdx.x * p.chunk;
     const int tokens = p.tokens - t0 < p.chunk ? p.tokens - t0 : p.chunk;
-    if (plan) {
-        clear_bits(bits, p.experts);
-        __syncthreads();
-    }
-    const int slot = threadIdx.x / L, sub = threadIdx.x & (L - 1);
+    if (threadIdx.x == 0) again_count = 0;
+    if (plan) clear_bits(bits, p.experts);
+    const int lane = threadIdx.x & 63, slot = threadIdx.x / L;
     for (int i = slot; i - slot < tokens; i += pass) {
-        route_token<X, L, V, K>(p, t0 + i, i < tokens, picked[slot]);
-        if (plan && i < tokens && sub < p.top) {
-            const int e = picked[slot][sub];
-            if (e >= 0) atomicOr(&bits.w[e][i >> 5], 1u << (i & 31));
+        bool live = i < tokens;
+        const TokenPart<X, L, V> in(p, p.lanes_per_group, t0 + i, live);
+        float most, total;
+        in.sums(p, most, total);
+        int expert;
+        const int certain = route_quick<X, L, V, BIAS>(p, in, most, expert);
+        if (__any(certain == ROUTE_RANK)) {
+            double c = 0.0;
+            if (live && expert >= 0) {
+                c = to_f32(static_cast<const X*>(p.logits)[(int64_t)(t0 + i) * p.ld + expert]);
+                if constexpr (BIAS) c = 1.0 / (1.0 + exp(-c)) + p.bias[expert];
+            }
+            const int ranked = route_rank<L>(p, expert, c, picked[slot]);
+            expert = certain == ROUTE_RANK ? ranked : expert;
         }
+        // (the first logits were asked for before the workgroup meets)
+        if (i == slot) __syncthreads();
+        if (certain == ROUTE_AGAIN && live) {
+            if ((lane & (L - 1)) == 0) again[atomicAdd(&again_count, 1)] = i;
+            live = false;
+        }
+        route_finish<X, L>(p, t0 + i, i, live, most, total, expert, bits);
+    }
+    __syncthreads();  // (no tokens: the first)
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (int q = wave; q < again_count; q += threads / 64) {
+        const int i = __builtin_amdgcn_readfirstlane(again[q]), group_lanes = p.lanes_per_group * (64 / L);
+        const TokenPart<X, 64, VX> in(p, group_lanes, t0 + i, true);
+        float most, total;
+        in.sums(p, most, total);
+        route_exact<X, 64, VX, BIAS>(p, group_lanes, in, most, picked[wave]);
+        wave_sync();
+        route_finish<X, 64>(p, t0 + i, i, true, most, total, lane < p.top ? picked[wave][lane] : -1, bits);
         wave_sync();
     }
     if (!plan) return;
@@ -352,11 +665,12 @@ __global__ __launch_bounds__(1024) void route_kernel(RouteArgs p)
     }
     for (int e = threadIdx.x; e < p.experts; e += threads) start[e] = count_bits(bits, e);
     __syncthreads();
-    scan_experts(start, p.experts, wave_sum, &total);
-    place_rows(p, t0, tokens, bits, start);
+    scan_experts(start, p.experts, wave_sum, &total_rows);
+    for (int i = threadIdx.x; i < tokens * p.top; i += threads)
+        place_row(p, t0, i, p.ids[(int64_t)t0 * p.top + i], bits, start);
     for (int e = threadIdx.x; e <= p.experts; e += threads)
-        p.offsets[e] = e < p.experts ? start[e] : total;
-    for (int r = total + threadIdx.x; r < p.tokens * p.top; r += threads) p.order[r] = -1;
+        p.offsets[e] = e < p.experts ? start[e] : total_rows;
+    for (int r = total_rows + threadIdx.x; r < p.tokens * p.top; r += threads) p.order[r] = -1;
 }
 
 }  // namespace dg

@@ -17,11 +17,12 @@ namespace {
 constexpr int64_t MAX_TOKENS = ((int64_t)1 << 26) - 64;
 static_assert(MAX_TOKENS * ROUTE_MAX_TOP <= INT_MAX, "32-bit assignments");
 
-// Tokens that share a count by expert: as few as make at most ROUTE_SUPER
-// chunks, so the second launch needs no sums of sums, and 64 beyond.
+// Tokens that share a count by expert, where one workgroup does not take them all:
+// as few as make at most ROUTE_SUPER chunks, so the second launch needs no sums of
+// sums, and 64 beyond.
 int route_chunk(int64_t tokens)
 {
-    return tokens <= 16 ? 16 : tokens <= 4 * ROUTE_SUPER ? 4 : tokens <= 16 * ROUTE_SUPER ? 16 : ROUTE_CHUNK;
+    return tokens <= 4 * ROUTE_SUPER ? 4 : tokens <= 16 * ROUTE_SUPER ? 16 : ROUTE_CHUNK;
 }
 
 bool ints_ok(const void* p) { return aligned_to(p, 4); }
@@ -99,17 +100,29 @@ gemm_status_t gemm_route(gemm_handle_t h, int64_t tokens, const void* logits, in
     a.sigmoid = r.scores == GEMM_SCORES_SIGMOID;
     a.renormalize = r.renormalize != 0;
     a.scale = r.scale;
-    const bool wide = r.bias || (groups > 1 && r.group_top == 2);
-    // 16 lanes to a token where there are tokens enough to fill the card with
-    // them, and room in 16 lanes (32 doubles to a lane spill)
+    // 16 lanes to a token where they have room (for a candidate more than are chosen,
+    // too; 32 scores and biases to a lane spill): few lanes to a token take fewer
+    // instructions, but a single token, or a token to each SIMD and no more, is
+    // sooner done in 64 (one of 64 experts 3.9 us, 17 of them 4.6 in 16 lanes each
+    // and 16 of them 5.6 in 64; 256 tokens of 256 experts 9.6 us in 64).
     int padded = 1;
     while (padded < groups) padded *= 2;
-    const bool fits16 = padded <= 16 && r.top <= 16 && ceil_div(a.group_size, 16 / padded) <= (wide ? 16 : 32);
-    const bool lanes64 = !fits16 || tokens <= 4 * ROUTE_SUPER;
+    auto per_lane = [&](int lanes) {  // log2 of the experts to a lane
+        int v = 0;
+        while ((1 << v) * (lanes / padded) < a.group_size) ++v;
+        return v;
+    };
+    const bool fits16 = padded <= 16 && r.top < 16 && per_lane(16) <= (r.bias ? 4 : 5);
+    // One workgroup makes the plan with the choice (a launch less: 2.5 us for the
+    // host) until its passes take longer than that: 96 tokens of 64 experts 7.6 us
+    // either way, of 256 experts 12.8 against 9.1, 64 of those 8.1 against 8.9, 32 of
+    // 256 with a bias and groups 8.6 against 10.1 and 64 of them 12.6 against 10.4.
+    const bool one = fits16 ? tokens <= ROUTE_ONE && tokens << per_lane(16) <= (r.bias ? 512 : 1024)
+                            : tokens <= 16;
+    const bool lanes64 = !fits16 || tokens <= 4 || (!one && tokens <= 4 * ROUTE_SUPER);
     a.lanes_per_group = (lanes64 ? 64 : 16) / padded;
-    int v = 0;
-    while ((1 << v) * a.lanes_per_group < a.group_size) ++v;
-    a.chunk = route_chunk(tokens);
+    const int v = per_lane(lanes64 ? 64 : 16);
+    a.chunk = one ? ROUTE_ONE : route_chunk(tokens);
     a.chunks = (int)std::max<int64_t>(1, ceil_div(tokens, a.chunk));
     a.count_ld = (int)ceil_div(r.experts, 4) * 4;
     if (plan && a.chunks > 1) {
@@ -122,8 +135,9 @@ gemm_status_t gemm_route(gemm_handle_t h, int64_t tokens, const void* logits, in
     if (v > 5) return GEMM_ERR_NOT_SUPPORTED;  // (not reached: 1024 experts in 64 groups are 16 a lane)
     if (h->fail_launch) return GEMM_ERR_HIP;
     // a workgroup's threads: its chunk at once, or in passes of 16 waves
-    const int threads = std::min(1024, a.chunk * (lanes64 ? 64 : 16));
-    const RouteFn fn = bf16 ? route_fn_bf16(lanes64, v, wide) : route_fn_f32(lanes64, v, wide);
+    const int threads = (int)std::min<int64_t>(1024, std::max<int64_t>(1, std::min<int64_t>(tokens, a.chunk)) *
+                                                         (lanes64 ? 64 : 16) + 63) / 64 * 64;
+    const RouteFn fn = bf16 ? route_fn_bf16(lanes64, v, r.bias) : route_fn_f32(lanes64, v, r.bias);
     void* args[] = {&a};
     if (hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3(a.chunks), dim3(threads), args, 0, stream) !=
         hipSuccess)

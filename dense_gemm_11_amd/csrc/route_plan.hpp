@@ -10,7 +10,8 @@ namespace dg {
 // the chunk is below `below` and to all[].
 __device__ __forceinline__ void add_counts(const RouteArgs& p, int lo, int hi, int below, int* n, int* all)
 {
-    const int quads = p.count_ld / 4, segs = blockDim.x / quads < 1 ? 1 : blockDim.x / quads;
+    // (with few experts no more than 16 parts: they meet in one sum each)
+    const int quads = p.count_ld / 4, segs = quads > 64 ? 1024 / quads : 16;
     const int q = threadIdx.x % quads, seg = threadIdx.x / quads;
     if (seg >= segs) return;
     // even and odd bytes as 16-bit sums: at most ROUTE_SUPER * ROUTE_CHUNK each
@@ -59,6 +60,14 @@ __global__ __launch_bounds__(1024) void route_place(RouteArgs p)
     __shared__ int wave_sum[16], total;
     const int b = blockIdx.x, t0 = b * p.chunk;
     const int tokens = p.tokens - t0 < p.chunk ? p.tokens - t0 : p.chunk;
+    // the chunk's assignments, up to two to a thread, asked for before all else
+    constexpr int OWN = ROUTE_CHUNK * ROUTE_MAX_TOP / 1024;
+    int own[OWN];
+#pragma unroll
+    for (int q = 0; q < OWN; ++q) {
+        const int i = threadIdx.x + 1024 * q;
+        own[q] = i < tokens * p.top ? p.ids[(int64_t)t0 * p.top + i] : -1;
+    }
     clear_bits(bits, p.experts);
     for (int e = threadIdx.x; e < p.experts; e += 1024) start[e] = all[e] = 0;
     __syncthreads();
@@ -80,15 +89,20 @@ __global__ __launch_bounds__(1024) void route_place(RouteArgs p)
             atomicAdd(&all[e], sum);
         }
     }
-    for (int i = threadIdx.x; i < tokens * p.top; i += 1024) {
-        const int e = p.ids[(int64_t)t0 * p.top + i], t = i / p.top;
-        if (e >= 0) atomicOr(&bits.w[e][t >> 5], 1u << (t & 31));
+#pragma unroll
+    for (int q = 0; q < OWN; ++q) {
+        const int t = ((int)threadIdx.x + 1024 * q) / p.top;
+        if (own[q] >= 0) atomicOr(&bits.w[own[q]][t >> 5], 1u << (t & 31));
     }
     __syncthreads();
     scan_experts(all, p.experts, wave_sum, &total);
     for (int e = threadIdx.x; e < p.experts; e += 1024) start[e] += all[e];
     __syncthreads();
-    place_rows(p, t0, tokens, bits, start);
+#pragma unroll
+    for (int q = 0; q < OWN; ++q) {
+        const int i = threadIdx.x + 1024 * q;
+        if (i < tokens * p.top) place_row(p, t0, i, own[q], bits, start);
+    }
     if (b == 0)
         for (int e = threadIdx.x; e <= p.experts; e += 1024)
             p.offsets[e] = e < p.experts ? all[e] : total;

@@ -9,28 +9,28 @@ namespace dg {
 typedef void (*RouteFn)(RouteArgs);
 
 // Kernels of L lanes to a token and 1 << v experts to a lane (v 0 to 5), by
-// whether the choice is compared in 64 bits.
-RouteFn route_fn_f32(bool lanes64, int v, bool wide);
-RouteFn route_fn_bf16(bool lanes64, int v, bool wide);
+// whether there is a bias.
+RouteFn route_fn_f32(bool lanes64, int v, bool bias);
+RouteFn route_fn_bf16(bool lanes64, int v, bool bias);
 
-template <typename X, int L, typename K>
+template <typename X, int L, bool BIAS>
 RouteFn route_fn_of(int v)
 {
     switch (v) {
-    case 0: return route_kernel<X, L, 1, K>;
-    case 1: return route_kernel<X, L, 2, K>;
-    case 2: return route_kernel<X, L, 4, K>;
-    case 3: return route_kernel<X, L, 8, K>;
-    case 4: return route_kernel<X, L, 16, K>;
-    default: return route_kernel<X, L, 32, K>;
+    case 0: return route_kernel<X, L, 1, BIAS>;
+    case 1: return route_kernel<X, L, 2, BIAS>;
+    case 2: return route_kernel<X, L, 4, BIAS>;
+    case 3: return route_kernel<X, L, 8, BIAS>;
+    case 4: return route_kernel<X, L, 16, BIAS>;
+    default: return route_kernel<X, L, 32, BIAS>;
     }
 }
 
 template <typename X>
-RouteFn route_fn(bool lanes64, int v, bool wide)
+RouteFn route_fn(bool lanes64, int v, bool bias)
 {
-    if (lanes64) return wide ? route_fn_of<X, 64, double>(v) : route_fn_of<X, 64, float>(v);
-    return wide ? route_fn_of<X, 16, double>(v) : route_fn_of<X, 16, float>(v);
+    if (lanes64) return bias ? route_fn_of<X, 64, true>(v) : route_fn_of<X, 64, false>(v);
+    return bias ? route_fn_of<X, 16, true>(v) : route_fn_of<X, 16, false>(v);
 }
 
 }  // namespace dg

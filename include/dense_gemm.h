@@ -555,9 +555,9 @@ gemm_status_t gemm_run_grouped_act_grad(gemm_handle_t h, int64_t M, int64_t N,
  * its one where it has no second), and only the top_groups best groups' experts
  * are chosen from; groups 0 or 1: no such step.  The `top` largest c are taken in
  * descending order; of equals, also of groups, the lower index comes first.
- * Scores next to each other decide, so c is compared in 64 bits; without a bias
- * and with group_top 1 (or no groups) the logits themselves are, in whose order
- * the scores are.
+ * Scores next to each other decide, so c and the groups' sums are compared in 64
+ * bits; without a bias the logits themselves are compared, in whose order the
+ * scores are.
  * The weights are scale * s, or with renormalize scale * s / (sum of the chosen s),
  * in fp32 and formed so that no underflow of s spoils the ratio.
  *
