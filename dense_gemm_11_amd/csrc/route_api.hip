@@ -125,7 +125,8 @@ gemm_status_t gemm_route(gemm_handle_t h, int64_t tokens, const void* logits, in
     a.chunk = one ? ROUTE_ONE : route_chunk(tokens);
     a.chunks = (int)std::max<int64_t>(1, ceil_div(tokens, a.chunk));
     a.count_ld = (int)ceil_div(r.experts, 4) * 4;
-    if (plan && a.chunks > 1) {
+    // (by the tokens alone, so that a call's needs do not turn on the choice above)
+    if (plan && tokens > 16) {
         if (!ws || !aligned_to(ws, 256) || ws_bytes < gemm_route_workspace_bytes(tokens, r.experts))
             return GEMM_ERR_INVALID_VALUE;
         a.counts = static_cast<uint8_t*>(ws);
