@@ -4,11 +4,14 @@
 // and the bias's, the sums of dZ's columns over each group's rows, taken before
 // dZ is rounded.
 //
-// One pass, bound by the bytes: a workgroup takes 64 rows of one group by 64
-// vectors of columns, its waves every fourth row.  A lane sums its columns down
-// its rows in registers, the waves' sums meet in LDS, and each tile's go to a row
-// of the workspace that a second, small launch adds up in order: no atomics, so
-// the sums repeat exactly.
+// One pass, bound by the bytes: a workgroup takes 16 rows of one group by 64
+// vectors of columns, its waves every fourth row, all asked for at once.  A lane
+// sums its columns down its rows in registers, the waves' sums meet in LDS, and
+// each tile's go to a row of the workspace that a second, small launch adds up in
+// order: no atomics, so the sums repeat exactly.  16 rows, since the fewer the more
+// workgroups there are to share the card out evenly (8192 rows, 2 x 5632 columns of
+// 16 groups, gated bf16 with H and dbias, 64, 32, 16 and 8 rows: 118, 112, 107 and
+// 116 us, 5.2 TB/s with 16, where the sums' way through memory begins to tell).
 #pragma once
 
 #include "act.hpp"
@@ -16,7 +19,7 @@
 
 namespace dg {
 
-constexpr int ACT_GRAD_ROWS = 64;
+constexpr int ACT_GRAD_ROWS = 16;
 
 struct ActGradArgs : RaggedArgs {
     const void* Z;
@@ -33,7 +36,7 @@ struct ActGradArgs : RaggedArgs {
 template <typename T, typename OutT, bool GATE>
 __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs p)
 {
-    constexpr int VEC = 16 / sizeof(T), COLS = 64 * VEC, WAVES = 4, U = 2;
+    constexpr int VEC = 16 / sizeof(T), COLS = 64 * VEC, WAVES = 4, U = 4;
     constexpr bool PRECISE = sizeof(T) == 4;
     constexpr int HALVES = GATE ? 2 : 1;
     __shared__ float part[WAVES - 1][HALVES * VEC][64];

@@ -107,7 +107,7 @@ gemm_status_t gemm_route(gemm_handle_t h, int64_t tokens, const void* logits, in
     // and 16 of them 5.6 in 64; 256 tokens of 256 experts 9.6 us in 64).
     int padded = 1;
     while (padded < groups) padded *= 2;
-    auto per_lane = [&](int lanes) {  // log2 of the experts to a lane
+    auto per_lane = [&](int lanes) {  // log2 of the experts to a lane (in 64 lanes: 5 at most)
         int v = 0;
         while ((1 << v) * (lanes / padded) < a.group_size) ++v;
         return v;
@@ -133,7 +133,6 @@ gemm_status_t gemm_route(gemm_handle_t h, int64_t tokens, const void* logits, in
         a.supers = reinterpret_cast<int32_t*>(a.counts +
                                               ceil_div((int64_t)a.chunks * a.count_ld, 256) * 256);
     }
-    if (v > 5) return GEMM_ERR_NOT_SUPPORTED;  // (not reached: 1024 experts in 64 groups are 16 a lane)
     if (h->fail_launch) return GEMM_ERR_HIP;
     // a workgroup's threads: its chunk at once, or in passes of 16 waves
     const int threads = (int)std::min<int64_t>(1024, std::max<int64_t>(1, std::min<int64_t>(tokens, a.chunk)) *

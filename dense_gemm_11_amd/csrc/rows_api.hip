@@ -55,26 +55,39 @@ hipError_t launch_move(MoveFn fn, const RowsArgs& a, int64_t rows, int vec, hipS
                            dim3(256), args, 0, stream);
 }
 
-template <template <typename, typename> class F>
-auto pick_type(gemm_dtype_t t) -> decltype(F<float, float>::fn())
+// Rows of a token to take at a time, 1 to 4: those with the fewest too many (one too
+// many rather than each alone), of these the most.
+int pick_batch(int top)
 {
-    return t == GEMM_DTYPE_F32       ? F<float, float>::fn()
-           : t == GEMM_DTYPE_BF16_F32 ? F<bf16_t, float>::fn()
-                                      : F<bf16_t, bf16_t>::fn();
+    int best = 1;
+    for (int b = 2; b <= 4; ++b)
+        if (ceil_div(top, b) * b <= ceil_div(top, best) * best + (best == 1 && top > 4 ? 1 : 0)) best = b;
+    return best;
+}
+
+MoveFn gather_fn(gemm_dtype_t t)
+{
+    return t == GEMM_DTYPE_F32        ? gather_rows_kernel<float, float>
+           : t == GEMM_DTYPE_BF16_F32 ? gather_rows_kernel<bf16_t, float>
+                                      : gather_rows_kernel<bf16_t, bf16_t>;
 }
 template <typename T, typename O>
-struct Gather {
-    static MoveFn fn() { return gather_rows_kernel<T, O>; }
-};
-template <typename T, typename O>
-struct Combine {
-    static MoveFn fn() { return combine_rows_kernel<T, O>; }
-};
+MoveFn combine_fn(int batch)
+{
+    return batch == 1   ? combine_rows_kernel<T, O, 1>
+           : batch == 2 ? combine_rows_kernel<T, O, 2>
+           : batch == 3 ? combine_rows_kernel<T, O, 3>
+                        : combine_rows_kernel<T, O, 4>;
+}
 typedef void (*GradFn)(RowsArgs);
 template <typename T, typename O>
-struct CombineGrad {
-    static GradFn fn() { return combine_rows_grad_kernel<T, O>; }
-};
+GradFn combine_grad_fn(int batch)
+{
+    return batch == 1   ? combine_rows_grad_kernel<T, O, 1>
+           : batch == 2 ? combine_rows_grad_kernel<T, O, 2>
+           : batch == 3 ? combine_rows_grad_kernel<T, O, 3>
+                        : combine_rows_grad_kernel<T, O, 4>;
+}
 
 }  // namespace
 }  // namespace dg
@@ -109,7 +122,7 @@ gemm_status_t gemm_gather_rows(gemm_handle_t h, int64_t tokens, int64_t cols, in
     a.top = top;
     a.rows = (int)rows;
     if (h->fail_launch) return GEMM_ERR_HIP;
-    if (launch_move(pick_type<Gather>(dtype), a, rows, (int)(16 / es), stream) != hipSuccess)
+    if (launch_move(gather_fn(dtype), a, rows, (int)(16 / es), stream) != hipSuccess)
         return GEMM_ERR_HIP;
     if (h->log)
         std::fprintf(stderr, "gemm: gather rows=%d tokens=%d cols=%d\n", a.rows, a.tokens, a.cols);
@@ -153,7 +166,11 @@ gemm_status_t gemm_combine_rows(gemm_handle_t h, int64_t tokens, int64_t cols, i
     a.rows = (int)rows;
     a.beta = beta;
     if (h->fail_launch) return GEMM_ERR_HIP;
-    if (launch_move(pick_type<Combine>(dtype), a, tokens, (int)(16 / es), stream) != hipSuccess)
+    const int batch = pick_batch(top);
+    const MoveFn fn = dtype == GEMM_DTYPE_F32        ? combine_fn<float, float>(batch)
+                      : dtype == GEMM_DTYPE_BF16_F32 ? combine_fn<bf16_t, float>(batch)
+                                                     : combine_fn<bf16_t, bf16_t>(batch);
+    if (launch_move(fn, a, tokens, (int)(16 / es), stream) != hipSuccess)
         return GEMM_ERR_HIP;
     if (h->log)
         std::fprintf(stderr, "gemm: combine rows=%d tokens=%d cols=%d\n", a.rows, a.tokens, a.cols);
@@ -199,8 +216,12 @@ gemm_status_t gemm_combine_rows_grad(gemm_handle_t h, int64_t tokens, int64_t co
     a.top = top;
     a.rows = (int)rows;
     if (h->fail_launch) return GEMM_ERR_HIP;
+    const int batch = pick_batch(top);
+    const GradFn fn = dtype == GEMM_DTYPE_F32        ? combine_grad_fn<float, float>(batch)
+                      : dtype == GEMM_DTYPE_BF16_F32 ? combine_grad_fn<bf16_t, float>(batch)
+                                                     : combine_grad_fn<bf16_t, bf16_t>(batch);
     void* args[] = {&a};
-    if (hipLaunchKernel(reinterpret_cast<const void*>(pick_type<CombineGrad>(dtype)), dim3((unsigned)tokens),
+    if (hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3((unsigned)tokens),
                         dim3(256), args, 0, stream) != hipSuccess)
         return GEMM_ERR_HIP;
     if (h->log)
