@@ -1,6 +1,15 @@
 // Launch tables of the products with bias, activation, gate and residual
 // (act.hpp): one tile configuration each, for both layouts of B and both output
 // types.  bn counts B's columns: gated, twice the outputs'.
+//
+// The costs of the gated tiles and of those of fp32 operands are fits of their
+// own for either layout of B (100 random calls of each kind: 1 to 16384 rows, 1 to
+// 128 groups, K 128 to 8192, N 128 to 14336), the others are gemm_run_grouped's.
+// On 50 other calls of each kind the tile chosen took 1.02 to 1.06 times the
+// fastest one's time on average, and up to 1.7 times; with gemm_run_grouped's costs
+// throughout 1.26 on average where a gated bf16 B is n-contiguous (a row piece is
+// half as long there, and streaming tiles half as fast) and 1.13 where a gated fp32
+// one is not.
 #pragma once
 
 #include "act.hpp"

@@ -20,6 +20,9 @@ struct TileOf {
     Fn fn[2][2];        // [B k-contiguous][bf16 output] (RAG_K: [0] only)
     bool stream;        // a streaming tile
     TileCost cost;
+    TileCost cost_kc;   // with a k-contiguous B, where it is another (alone > 0)
+
+    const TileCost& cost_of(bool b_kc) const { return b_kc && cost_kc.alone > 0.0f ? cost_kc : cost; }
 };
 using RaggedTile = TileOf<RaggedFn>;
 
@@ -40,13 +43,14 @@ template <class Tile>
 double expected_us(const Tile& t, bool b_kc, double tiles, double K, double bytes, int cus)
 {
     const double n = tiles > cus ? tiles / cus : 1.0, k = K / 1000.0;
-    const double alone = t.cost.alone + k * t.cost.alone_k;
+    const TileCost& cost = t.cost_of(b_kc);
+    const double alone = cost.alone + k * cost.alone_k;
     // tiles that have a unit to themselves come in whole rounds, the others
     // leave a part of one
     const double rounds = t.stream || t.bm * t.bn[0] >= 192 * 256 ? (double)(int64_t)(n + 0.9)
                           : n > 1.0                               ? n + 0.4
                                                                   : 1.0;
-    const double full = rounds * (t.cost.each + k * t.cost.each_k);
+    const double full = rounds * (cost.each + k * cost.each_k);
     const double us = alone > full ? alone : full;
     const double floor_us = bytes / 5.2e6 * (t.bn[b_kc] < 64 ? 1.15 : 1.0);
     return (us > floor_us ? us : floor_us) + 0.01 * us;
