@@ -18,7 +18,7 @@ the runtime torch already loaded instead of loading a second one.
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.util
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -786,17 +786,18 @@ ACTIVATIONS = {"none": GEMM_ACT_NONE, "relu": GEMM_ACT_RELU, "gelu": GEMM_ACT_GE
 SCORES = {"softmax": GEMM_SCORES_SOFTMAX, "sigmoid": GEMM_SCORES_SIGMOID}
 
 
-# These calls too are made per token by a decoding loop, where their kernels take a
-# few microseconds: torch's modules are looked up once, every tensor is asked for a
-# property once, and the structures that hold no pointer are kept by their values.
+# Their tensors are checked natively, positionally; what is left here are names,
+# defaults and the stream.
 try:
     import torch as _torch
-    _i32, _f32, _bf16 = _torch.int32, _torch.float32, _torch.bfloat16
+    from . import _bind  # (the library above is loaded already)
     _current_device = getattr(_torch._C, "_cuda_getDevice", None) or _torch.cuda.current_device
     _raw_stream = getattr(_torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda device: _torch.cuda.current_stream(device).cuda_stream)
-except ImportError:  # the raw calls need no torch
-    _torch = None
+except ImportError:
+    if importlib.util.find_spec("torch") is not None:
+        raise  # built without its native part, or against another torch
+    # without torch there are no tensors: the raw calls are all there is
 
 
 def _named(table, name, what):
@@ -806,94 +807,18 @@ def _named(table, name, what):
         raise ValueError(f"{what} must be one of {', '.join(table)}") from None
 
 
-def _gpu_of(t):
-    """Device index of the tensor that the others of a call are compared with."""
+def _call(fn, what, t, stream, check, *args):
+    """fn(stream, *args) with the device of tensor t current, whose memory the
+    arguments point to: the default stream is that of the current device."""
     device = t.get_device()
-    if device < 0:
-        raise ValueError("the tensors must be on a GPU")
-    return device
-
-
-def _launch(device, stream, fn, *args):
-    """fn(*args, stream), the device's current stream by default, with `device`,
-    whose memory the arguments point to, current: the default stream is that of the
-    current device."""
-    if device == _current_device():
-        return fn(*args, _raw_stream(device) if stream is None else stream)
-    with _torch.cuda.device(device):
-        return fn(*args, _raw_stream(device) if stream is None else stream)
-
-
-def _table(t, dtype, rows, cols, device, what):
-    """Data pointer of a packed rows x cols tensor on device index `device` (None
-    stays None)."""
-    if t is None:
-        return None
-    if t.shape != (rows, cols) or t.dtype is not dtype or t.get_device() != device or (
-            not t.is_contiguous()):
-        raise ValueError(f"{what} must be a contiguous {rows} x {cols} {dtype} tensor on the same device")
-    return t.data_ptr()
-
-
-def _vector(t, dtype, length, device, what):
-    """... of a packed vector."""
-    if t is None:
-        return None
-    if t.shape != (length,) or t.dtype is not dtype or t.get_device() != device or (
-            not t.is_contiguous()):
-        raise ValueError(f"{what} must be a contiguous length-{length} {dtype} tensor on the same device")
-    return t.data_ptr()
-
-
-def _strided(t, dtype, rows, cols, device, what):
-    """Data pointer and leading dimension of a rows x cols matrix on device index
-    `device` (None stays None)."""
-    if t is None:
-        return None, cols
-    if t.shape != (rows, cols) or t.dtype is not dtype or t.get_device() != device:
-        raise ValueError(f"{what} must be a {rows} x {cols} {dtype} tensor on the same device")
-    s = t.stride()
-    if s[1] != 1 and cols > 1:
-        raise ValueError(f"{what} must have unit stride in its last axis")
-    return t.data_ptr(), s[0] if rows > 1 else max(cols, 1)
-
-
-def _workspace(t, device):
-    if t is None:
-        return None, 0
-    if t.get_device() != device:
-        raise ValueError("the workspace must be on the same device")
-    return t.data_ptr(), t.nbytes
-
-
-def _two_types(ti, to):
-    """gemm_dtype_t of operands and outputs."""
-    if ti is _bf16:
-        if to is _bf16:
-            return GEMM_DTYPE_BF16_BF16
-        if to is _f32:
-            return GEMM_DTYPE_BF16_F32
-    elif ti is _f32 and to is _f32:
-        return GEMM_DTYPE_F32
-    raise TypeError("operands must be float32, or bfloat16 with float32 or bfloat16 outputs")
-
-
-def _logits(x):
-    """gemm_dtype_t, rows, columns and leading dimension of a router's logits."""
-    if x.dtype is _f32:
-        dtype = GEMM_DTYPE_F32
-    elif x.dtype is _bf16:
-        dtype = GEMM_DTYPE_BF16_BF16
+    if device < 0 or device == _current_device():
+        s = fn(_raw_stream(device) if stream is None and device >= 0 else stream, *args)
     else:
-        raise TypeError("logits must be float32 or bfloat16")
-    return (dtype, *_matrix(x))
-
-
-@functools.lru_cache(maxsize=256)
-def _routing(experts, top, scores, groups, top_groups, group_top, renormalize, scale):
-    """A routing without a bias, whose structure holds no pointer."""
-    return ctypes.byref(GemmRouting(experts, top, _named(SCORES, scores, "scores"), groups, top_groups,
-                                    group_top, None, int(renormalize), scale))
+        with _torch.cuda.device(device):
+            s = fn(_raw_stream(device) if stream is None else stream, *args)
+    if check and s != GEMM_OK:
+        raise GemmError(s, what)
+    return s
 
 
 def route_workspace(tokens: int, experts: int, device=None):
@@ -924,43 +849,17 @@ def run_route(h, logits, ids, weights, offsets=None, order=None, position=None, 
     renormalize.  Logits of -inf are never chosen: ids -1 and weight 0 where fewer
     than top are left.
     """
-    dtype, tokens, experts, ld = _logits(logits)
-    if ids.dim() != 2:
-        raise ValueError("ids must be tokens x top")
-    top = ids.shape[1]
-    device = _gpu_of(logits)
-    if (offsets is None) != (order is None) or (order is None) != (position is None):
-        raise ValueError("offsets, order and position come together")
-    if bias is None:
-        r = _routing(experts, top, scores, groups, top_groups, group_top, renormalize, scale)
-    else:
-        r = ctypes.byref(GemmRouting(experts, top, _named(SCORES, scores, "scores"), groups, top_groups,
-                                     group_top, _vector(bias, _f32, experts, device, "bias"),
-                                     int(renormalize), scale))
-    s = _launch(device, stream, lib.gemm_route, h, tokens, logits.data_ptr(), ld, dtype, r,
-                _table(ids, _i32, tokens, top, device, "ids"),
-                _table(weights, _f32, tokens, top, device, "weights"),
-                _vector(offsets, _i32, experts + 1, device, "offsets"),
-                _vector(order, _i32, tokens * top, device, "order"),
-                _table(position, _i32, tokens, top, device, "position"), *_workspace(workspace, device))
-    return _finish(s, check, "gemm_route")
+    return _call(_bind.route, "gemm_route", logits, stream, check, h, logits, ids, weights, offsets,
+                 order, position, workspace, _named(SCORES, scores, "scores"), bias, groups, top_groups,
+                 group_top, renormalize, scale)
 
 
 def run_route_grad(h, logits, ids, dweights, dlogits, scores="softmax", renormalize=False, scale=1.0,
                    stream=None, check=True) -> int:
     """gemm_route_grad on torch tensors: the logits' gradient (dlogits, of the
     logits' type) from that of run_route's weights, for the experts it chose."""
-    dtype, tokens, experts, ld = _logits(logits)
-    if ids.dim() != 2:
-        raise ValueError("ids must be tokens x top")
-    top = ids.shape[1]
-    device = _gpu_of(logits)
-    s = _launch(device, stream, lib.gemm_route_grad, h, tokens, logits.data_ptr(), ld, dtype,
-                _routing(experts, top, scores, 1, 1, 1, renormalize, scale),
-                _table(ids, _i32, tokens, top, device, "ids"),
-                _table(dweights, _f32, tokens, top, device, "dweights"),
-                *_strided(dlogits, logits.dtype, tokens, experts, device, "dlogits"))
-    return _finish(s, check, "gemm_route_grad")
+    return _call(_bind.route_grad, "gemm_route_grad", logits, stream, check, h, logits, ids, dweights,
+                 dlogits, _named(SCORES, scores, "scores"), renormalize, scale)
 
 
 def run_gather_rows(h, X, D, order, top, weights=None, stream=None, check=True) -> int:
@@ -970,18 +869,7 @@ def run_gather_rows(h, X, D, order, top, weights=None, stream=None, check=True) 
     order: int32, one entry per row of D, from run_route; rows of a negative entry
     keep their values.  X is float32 or bfloat16, D of X's dtype or float32.
     """
-    dtype = _two_types(X.dtype, D.dtype)
-    tokens, cols, ldx = _matrix(X)
-    rows, Nd, ldd = _matrix(D)
-    if Nd != cols:
-        raise ValueError("X and D must have the same columns")
-    device = _gpu_of(D)
-    if X.get_device() != device:
-        raise ValueError("every tensor must be on D's device")
-    s = _launch(device, stream, lib.gemm_gather_rows, h, tokens, cols, top, X.data_ptr(), ldx, rows,
-                _vector(order, _i32, rows, device, "order"),
-                _table(weights, _f32, tokens, top, device, "weights"), D.data_ptr(), ldd, dtype)
-    return _finish(s, check, "gemm_gather_rows")
+    return _call(_bind.gather_rows, "gemm_gather_rows", D, stream, check, h, X, D, order, top, weights)
 
 
 def run_combine_rows(h, Y, D, position, weights=None, C=None, beta=0.0, stream=None,
@@ -994,20 +882,8 @@ def run_combine_rows(h, Y, D, position, weights=None, C=None, beta=0.0, stream=N
     float32 (D may be C); position: int32, tokens x top, from run_route; weights:
     float32, tokens x top, or None (all 1).
     """
-    dtype = _two_types(Y.dtype, D.dtype)
-    rows, cols, ldy = _matrix(Y)
-    tokens, Nd, ldd = _matrix(D)
-    if Nd != cols or position.dim() != 2:
-        raise ValueError("Y and D must have the same columns, position tokens x top")
-    top = position.shape[1]
-    device = _gpu_of(D)
-    if Y.get_device() != device:
-        raise ValueError("every tensor must be on D's device")
-    s = _launch(device, stream, lib.gemm_combine_rows, h, tokens, cols, top, Y.data_ptr(), ldy, rows,
-                _table(position, _i32, tokens, top, device, "position"),
-                _table(weights, _f32, tokens, top, device, "weights"), beta,
-                *_strided(C, D.dtype, tokens, cols, device, "C"), D.data_ptr(), ldd, dtype)
-    return _finish(s, check, "gemm_combine_rows")
+    return _call(_bind.combine_rows, "gemm_combine_rows", D, stream, check, h, Y, D, position, weights,
+                 C, beta)
 
 
 def run_combine_rows_grad(h, Y, dD, dY, dweights, position, weights, stream=None, check=True) -> int:
@@ -1017,23 +893,8 @@ def run_combine_rows_grad(h, Y, dD, dY, dweights, position, weights, stream=None
     Y, dY: rows x cols (dY may be Y); dD: tokens x cols, of Y's dtype or float32;
     position (int32), weights and dweights (float32): tokens x top.
     """
-    if dY.dtype is not Y.dtype:
-        raise TypeError("dY must have Y's dtype")
-    dtype = _two_types(Y.dtype, dD.dtype)
-    rows, cols, ldy = _matrix(Y)
-    tokens, Nd, lddd = _matrix(dD)
-    if Nd != cols or position.dim() != 2:
-        raise ValueError("Y and dD must have the same columns, position tokens x top")
-    top = position.shape[1]
-    device = _gpu_of(Y)
-    if dD.get_device() != device:
-        raise ValueError("every tensor must be on Y's device")
-    s = _launch(device, stream, lib.gemm_combine_rows_grad, h, tokens, cols, top, Y.data_ptr(), ldy, rows,
-                _table(position, _i32, tokens, top, device, "position"),
-                _table(weights, _f32, tokens, top, device, "weights"), dD.data_ptr(), lddd,
-                *_strided(dY, Y.dtype, rows, cols, device, "dY"),
-                _table(dweights, _f32, tokens, top, device, "dweights"), dtype)
-    return _finish(s, check, "gemm_combine_rows_grad")
+    return _call(_bind.combine_rows_grad, "gemm_combine_rows_grad", Y, stream, check, h, Y, dD, dY,
+                 dweights, position, weights)
 
 
 def run_grouped_act(h, A, B, D, offsets=None, activation="none", gated=False, bias=None, Z=None,
@@ -1050,47 +911,9 @@ def run_grouped_act(h, A, B, D, offsets=None, activation="none", gated=False, bi
     W x K, or a single group).  scales, dtypes and rows in no group as for
     run_grouped.
     """
-    ta, to = A.dtype, D.dtype
-    if B.dtype is not ta or (Z is not None and Z.dtype is not to) or (
-            R is not None and R.dtype is not to) or (bias is not None and bias.dtype is not to):
-        raise TypeError("A and B, and D, Z, R and bias, must have one dtype each")
-    dtype = _two_types(ta, to)
-    M, K, lda = _matrix(A)
-    if offsets is None and B.dim() == 2:
-        Kb, W, ldb = _matrix(B)
-        groups, stride_b = 1, 0
-    else:
-        groups, Kb, W, ldb, stride_b = _matrices(B)
-    if transB != "N":
-        Kb, W = W, Kb
-    Md, N, ldd = _matrix(D)
-    if Kb != K or Md != M or W != (2 * N if gated else N) or (offsets is None and groups != 1):
-        raise ValueError("inconsistent grouped GEMM shapes")
-    device = _gpu_of(D)
-    if A.get_device() != device or B.get_device() != device:
-        raise ValueError("every tensor must be on D's device")
-    act = GemmAct(_named(ACTIVATIONS, activation, "activation"), bool(gated))
-    if bias is not None:
-        shape = bias.shape
-        if (shape != (W,) and shape != (groups, W)) or bias.get_device() != device or (
-                W > 1 and bias.stride(-1) != 1):
-            raise ValueError("bias must be groups x width, or width, with unit stride, on D's device")
-        act.bias = bias.data_ptr()
-        act.stride_bias = bias.stride(0) if len(shape) == 2 and groups > 1 else 0
-    if Z is not None:
-        act.Z, act.ldz = _strided(Z, to, M, W, device, "Z")
-    if R is not None:
-        act.R, act.ldr = _strided(R, to, M, N, device, "R")
-    gr = None
-    if offsets is not None:
-        gr = ctypes.byref(GemmGroups(groups, _vector(offsets, _i32, groups + 1, device, "offsets"),
-                                     _vector(scales, _f32, groups, device, "scales")))
-    elif scales is not None:
-        raise ValueError("scales are the groups': without offsets, use alpha")
-    s = _launch(device, stream, lib.gemm_run_grouped_act, h, GEMM_OP_N if transB == "N" else GEMM_OP_T,
-                M, N, K, alpha, A.data_ptr(), lda, B.data_ptr(), ldb, stride_b, D.data_ptr(), ldd, dtype,
-                gr, ctypes.byref(act))
-    return _finish(s, check, "gemm_run_grouped_act")
+    return _call(_bind.grouped_act, "gemm_run_grouped_act", D, stream, check, h, A, B, D, offsets,
+                 _named(ACTIVATIONS, activation, "activation"), gated, bias, Z, R, transB == "N", scales,
+                 alpha)
 
 
 def act_grad_workspace(rows: int, width: int, groups: int, device=None):
@@ -1115,27 +938,5 @@ def run_grouped_act_grad(h, Z, dD, dZ, offsets=None, activation="none", gated=Fa
     sums over each group's rows, with a workspace from act_grad_workspace.
     offsets None: all rows are one group's.
     """
-    ti, to = dZ.dtype, Z.dtype
-    if dD.dtype is not to or (H is not None and H.dtype is not ti):
-        raise TypeError("Z and dD, and dZ and H, must have one dtype each")
-    dtype = _two_types(ti, to)
-    M, W, ldz = _matrix(Z)
-    Md, N, lddd = _matrix(dD)
-    if Md != M or W != (2 * N if gated else N):
-        raise ValueError("inconsistent shapes of Z and dD")
-    device = _gpu_of(Z)
-    if dD.get_device() != device:
-        raise ValueError("every tensor must be on Z's device")
-    groups, gr = 1, None
-    if offsets is not None:
-        if offsets.dim() != 1 or offsets.shape[0] < 1:
-            raise ValueError("offsets must hold groups + 1 entries")
-        groups = offsets.shape[0] - 1
-        gr = ctypes.byref(GemmGroups(groups, _vector(offsets, _i32, groups + 1, device, "offsets"), None))
-    s = _launch(device, stream, lib.gemm_run_grouped_act_grad, h, M, N,
-                _named(ACTIVATIONS, activation, "activation"), bool(gated), Z.data_ptr(), ldz,
-                dD.data_ptr(), lddd, *_strided(dZ, ti, M, W, device, "dZ"),
-                *_strided(H, ti, M, N, device, "H"),
-                _table(dbias, _f32, groups, W, device, "dbias"), dtype, gr,
-                *_workspace(workspace, device))
-    return _finish(s, check, "gemm_run_grouped_act_grad")
+    return _call(_bind.grouped_act_grad, "gemm_run_grouped_act_grad", Z, stream, check, h, Z, dD, dZ,
+                 offsets, _named(ACTIVATIONS, activation, "activation"), gated, H, dbias, workspace)

@@ -1,7 +1,8 @@
 """Build the gfx950 HIP library libdense_gemm.so in this package directory.
 
 Each source in csrc/ is compiled to an object under _build/ (in parallel),
-then the objects are linked into one shared library.  Every HIP compile uses
+then the objects are linked into one shared library.  csrc/bind.cpp, the native
+part of the Python binding, becomes the extension module _bind beside it.  Every HIP compile uses
 -Xclang -target-feature -Xclang -packed-fp32-ops, which keeps the compiler
 from emitting packed FP32 instructions.
 """
@@ -19,6 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libdense_gemm.so")
+BIND = os.path.join(HERE, "_bind.so")
 ARCH = "gfx950"
 
 SOURCES = ["api.hip", "inst_bf16.hip", "inst_bf16_dma.hip", "inst_bf16_dma_out.hip",
@@ -63,15 +65,51 @@ def _compile(src: str, extra) -> str:
     return obj
 
 
+def _compile_bind() -> str:
+    """Object of the extension module: host code against torch's headers."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
+    obj = os.path.join(BUILD, "bind.o")
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w",
+           "-D__HIP_PLATFORM_AMD__=1", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", INCLUDE, "-isystem", os.path.join(rocm, "include"),
+           "-isystem", sysconfig.get_paths()["include"]]
+    for path in cpp_extension.include_paths():
+        cmd += ["-isystem", path]
+    cmd += ["-c", os.path.join(CSRC, "bind.cpp"), "-o", obj]
+    proc = subprocess.run(cmd, capture_output=True, text=True)
+    if proc.returncode != 0:
+        raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{proc.stdout}\n{proc.stderr}")
+    return obj
+
+
+def _link_bind(obj: str) -> None:
+    from torch.utils import cpp_extension
+
+    tmp = BIND + ".tmp"
+    cmd = [shutil.which("g++") or "c++", "-shared", obj, "-L", HERE, "-l:libdense_gemm.so",
+           "-Wl,-rpath,$ORIGIN"]
+    for path in cpp_extension.library_paths():
+        cmd += ["-L", path]
+    subprocess.run(cmd + ["-lc10", "-ltorch_cpu", "-ltorch_python", "-o", tmp], check=True)
+    os.replace(tmp, BIND)
+
+
 def build(extra_flags=(), jobs: int = 0) -> str:
     os.makedirs(BUILD, exist_ok=True)
     jobs = jobs or min(len(SOURCES), os.cpu_count() or 4)
     with concurrent.futures.ThreadPoolExecutor(jobs) as ex:
+        bind = ex.submit(_compile_bind)
         objs = list(ex.map(lambda s: _compile(s, extra_flags), SOURCES))
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    _link_bind(bind.result())
     return LIB
 
 

@@ -83,9 +83,10 @@ const Tile& pick_tile(gemm_handle_t h, const TileList<Tile>& t, bool b_kc, int64
         return t[best];
     }
     double best_us = 0.0;
+    const int cus = device_cus();
     for (int i = 0; i < t.n; ++i) {
         if (!grid_fits(grid(t[i]), t[i].threads)) continue;
-        const double us = expected_us(t[i], b_kc, (double)tiles(t[i]), (double)K, bytes, device_cus());
+        const double us = expected_us(t[i], b_kc, (double)tiles(t[i]), (double)K, bytes, cus);
         if (best_us == 0.0 || us < best_us) {
             best = i;
             best_us = us;
