@@ -383,25 +383,33 @@ __device__ __forceinline__ int route_quick(const RouteArgs& p, const TokenPart<X
     const uint32_t place = PLACES - V * sub;
 #pragma unroll
     for (int i = 0; i < V; ++i) c[i] = (c[i] & ~PLACES) + (place - i);
-    uint32_t m = 0, mine = 0, chosen_last = 0;
+    uint32_t m = 0, mine = 0, last = 0;  // this choice, lane j's, the last that counts
     bool rank = false;
-    const int rounds = p.top + (WHOLE ? 0 : 2);
-    for (int j = 0; j < rounds; ++j) {
-        const uint32_t last = m;
-        uint32_t d = last - 1u - c[0];
+    auto next = [&]() __attribute__((always_inline)) {
+        uint32_t d = m - 1u - c[0];
 #pragma unroll
-        for (int i = 1; i < V; ++i) d = least_of(d, last - 1u - c[i]);
-        m = last - 1u - lanes_pick<L>(d, [](uint32_t a, uint32_t b) { return least_of(a, b); });
+        for (int i = 1; i < V; ++i) d = least_of(d, m - 1u - c[i]);
+        m = m - 1u - lanes_pick<L>(d, [](uint32_t a, uint32_t b) { return least_of(a, b); });
+    };
+    // whether hi, at the least, is above m at the most
+    auto sure = [&](uint32_t hi) __attribute__((always_inline)) {
+        if constexpr (BIAS) return apart(key_value(hi & ~PLACES), key_value(m | PLACES), 1.0f);
+        else return (hi & ~PLACES) > (m | PLACES);
+    };
+    for (int j = 0; j < p.top; ++j) {
+        last = m;
+        next();
         mine = sub == j ? m : mine;
-        if constexpr (!WHOLE) {
-            // what the one before is at the least and this one at the most
-            auto sure = [&](uint32_t hi) __attribute__((always_inline)) {
-                if constexpr (BIAS) return apart(key_value(hi & ~PLACES), key_value(m | PLACES), 1.0f);
-                else return (hi & ~PLACES) > (m | PLACES);
-            };
-            if (j <= p.top) rank |= j > 0 && m >= LEAST && !sure(last);
-            else again |= rank && m >= LEAST && !sure(chosen_last);
-            chosen_last = j == p.top - 1 ? m : chosen_last;
+        if constexpr (!WHOLE) rank |= j > 0 && m >= LEAST && !sure(last);
+    }
+    if constexpr (!WHOLE) {
+        last = m;
+        next();
+        mine = sub == p.top ? m : mine;
+        rank |= m >= LEAST && !sure(last);
+        if (__any(rank)) {
+            next();  // has to be below the last for certain
+            again |= rank && m >= LEAST && !sure(last);
         }
     }
     if (BIAS && !p.sigmoid) again |= rank;
