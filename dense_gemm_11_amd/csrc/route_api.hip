@@ -27,6 +27,19 @@ int route_chunk(int64_t tokens)
 
 bool ints_ok(const void* p) { return aligned_to(p, 4); }
 
+// The gradient's kernel: one quad of experts to a lane, or four.
+typedef void (*GradFn)(RouteGradArgs);
+template <typename X>
+GradFn grad_fn(bool lanes64, int experts, bool dense)
+{
+    if (lanes64) {
+        if (experts <= 256) return dense ? route_grad_kernel<X, 64, 1, true> : route_grad_kernel<X, 64, 1, false>;
+        return dense ? route_grad_kernel<X, 64, 4, true> : route_grad_kernel<X, 64, 4, false>;
+    }
+    if (experts <= 64) return dense ? route_grad_kernel<X, 16, 1, true> : route_grad_kernel<X, 16, 1, false>;
+    return dense ? route_grad_kernel<X, 16, 4, true> : route_grad_kernel<X, 16, 4, false>;
+}
+
 gemm_status_t check_routing(const gemm_routing_t* r)
 {
     if (!r || (r->scores != GEMM_SCORES_SOFTMAX && r->scores != GEMM_SCORES_SIGMOID))
@@ -178,17 +191,17 @@ gemm_status_t gemm_route_grad(gemm_handle_t h, int64_t tokens, const void* logit
         return GEMM_ERR_INVALID_VALUE;
     if (!aligned_to(logits, es) || !aligned_to(dlogits, es) || !ints_ok(ids) || !ints_ok(dweights))
         return GEMM_ERR_NOT_SUPPORTED;
-    RouteGradArgs a{logits, ids, dweights, dlogits, ld, ldd, (int)tokens, r.experts, r.top,
+    const int row = (int)ceil_div(r.experts, 4) * 4;
+    RouteGradArgs a{logits, ids, dweights, dlogits, ld, ldd, (int)tokens, r.experts, r.top, row,
                     r.scores == GEMM_SCORES_SIGMOID, r.renormalize != 0, r.scale};
-    const bool lanes64 = r.top > 16 || r.experts > 512 || tokens <= 4 * ROUTE_SUPER;
+    const bool lanes64 = r.top > 16 || r.experts > 256 || tokens <= 4 * ROUTE_SUPER;
     const int per = lanes64 ? 4 : 16;
+    const bool dense = !a.sigmoid && !a.renormalize;
     if (h->fail_launch) return GEMM_ERR_HIP;
-    typedef void (*Fn)(RouteGradArgs);
-    const Fn fn = es == 2 ? (lanes64 ? (Fn)route_grad_kernel<bf16_t, 64> : (Fn)route_grad_kernel<bf16_t, 16>)
-                          : (lanes64 ? (Fn)route_grad_kernel<float, 64> : (Fn)route_grad_kernel<float, 16>);
+    const GradFn fn = es == 2 ? grad_fn<bf16_t>(lanes64, r.experts, dense) : grad_fn<float>(lanes64, r.experts, dense);
     void* args[] = {&a};
     if (hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3((unsigned)ceil_div(tokens, per)), dim3(256),
-                        args, (size_t)per * r.experts * 4, stream) != hipSuccess)
+                        args, (size_t)per * row * 4, stream) != hipSuccess)
         return GEMM_ERR_HIP;
     if (h->log)
         std::fprintf(stderr, "gemm: route grad tokens=%d experts=%d top=%d\n", a.tokens, a.experts, a.top);

@@ -2,6 +2,7 @@
 // and the gradient.
 #pragma once
 
+#include "act.hpp"
 #include "route.hpp"
 
 namespace dg {
@@ -117,68 +118,79 @@ __global__ __launch_bounds__(1024) void route_place(RouteArgs p)
 //   sigmoid          dx_j = scale s_j (1 - s_j) g_j
 //   ... renormalised dx_j = scale q_j (1 - s_j) (g_j - sum_l g_l q_l)
 // with g_e = 0 for experts that were not chosen.  What the chosen get goes
-// through LDS to the lanes that write the row.  Bound by reading and writing the
-// logits (only writing where nothing but the chosen count).
+// through LDS to the lanes that write the row, NQ quads of neighbouring experts
+// each.  DENSE, the first form, needs every logit, which its lanes hold (read three
+// times over instead, 16384 rows of 256 fp32 took 14.9 us; 8.3).  Bound by reading
+// and writing the logits, of the other forms only by writing.
 struct RouteGradArgs {
     const void* logits;
     const int32_t* ids;
     const float* dweights;
     void* dlogits;
     int64_t ld, ldd;
-    int tokens, experts, top;
+    int tokens, experts, top, row;  // row: experts padded to whole quads
     int sigmoid, renormalize;
     float scale;
 };
 
-template <typename X, int L>
+template <typename X, int L, int NQ, bool DENSE>
 __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p)
 {
-    extern __shared__ float chosen[];  // a row of experts per token
+    extern __shared__ f32x4 quads[];  // a row of experts per token
     const int lane = threadIdx.x & 63, sub = lane & (L - 1), slot = threadIdx.x / L;
     const int t = blockIdx.x * (256 / L) + slot;
-    if (t >= p.tokens) return;  // (whole waves are not needed: nothing below crosses the L lanes)
+    if (t >= p.tokens) return;  // (no exchange below leaves a token's L lanes)
     const X* row = static_cast<const X*>(p.logits) + (int64_t)t * p.ld;
     X* out = static_cast<X*>(p.dlogits) + (int64_t)t * p.ldd;
-    float* mine = chosen + slot * p.experts;
-    const int E = p.experts;
-    for (int e = sub; e < E; e += L) mine[e] = 0.0f;
-    const bool dense = !p.sigmoid && !p.renormalize;
+    f32x4* mine = quads + slot * (p.row / 4);
     const float low = -__builtin_inff();
-    const int e = sub < p.top ? p.ids[(int64_t)t * p.top + sub] : -1;
-    const bool live = e >= 0 && e < E;
-    float x = live ? to_f32(row[e]) : low;
-    x = x > low ? x : low;
-    float g = live ? p.dweights[(int64_t)t * p.top + sub] : 0.0f;
-    float m, total = 1.0f;
-    if (dense) {
-        m = low;
-        for (int i = sub; i < E; i += L) m = fmaxf(m, to_f32(row[i]));
-        m = lanes_max<L>(m);
-        float s = 0.0f;
-        for (int i = sub; i < E; i += L) {
-            const float v = to_f32(row[i]);
-            s += v > low ? exp_below(v, m) : 0.0f;
+    float x[DENSE ? NQ : 1][4];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+        const int e = 4 * (sub + i * L);
+        if (e < p.experts) mine[e / 4] = f32x4{};
+        if constexpr (DENSE) {
+            load_part<4>(x[i], row + (e < p.experts ? e : 0), e + 4 <= p.experts ? 4 : p.experts - e, low);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[i][q] = fmaxf(x[i][q], low);  // a NaN is as -inf
         }
+    }
+    const int e = sub < p.top ? p.ids[(int64_t)t * p.top + sub] : -1;
+    const bool live = e >= 0 && e < p.experts;
+    const float xe = live ? fmaxf(to_f32(row[e]), low) : low;
+    const float g = live ? p.dweights[(int64_t)t * p.top + sub] : 0.0f;
+    float m = xe, total = 1.0f;
+    if constexpr (DENSE) {
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) m = fmaxf(m, x[i][q]);
+    }
+    m = lanes_max<L>(m);
+    if constexpr (DENSE) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                x[i][q] = x[i][q] > low ? quick_exp_below(x[i][q], m) : 0.0f;
+                s += x[i][q];
+            }
         total = lanes_sum<L>(s);
-        total = total > 0.0f ? total : 1.0f;
-    } else {
-        m = lanes_max<L>(x);
     }
     // p_j, or in proportion to it (chosen_score), and q_j
-    float q = x > low ? exp_below(x, p.sigmoid ? fminf(m, 0.0f) : m) : 0.0f, rest = 1.0f;
-    if (p.sigmoid && x > low) {
-        const float up = 1.0f / (1.0f + expf(-fabsf(x)));  // the larger of s and 1 - s
-        const float dn = expf(-fabsf(x)) * up;
-        rest = x > 0.0f ? dn : up;
-        q = x > 0.0f ? up : p.renormalize ? expf(x - fminf(m, 0.0f)) * up : dn;
+    float q = xe > low ? quick_exp_below(xe, m) : 0.0f, rest = 1.0f;
+    if (p.sigmoid && xe > low) {
+        const float tail = quick_exp(-fabsf(xe));
+        const float up = __builtin_amdgcn_rcpf(1.0f + tail), dn = tail * up;  // the larger of s and 1 - s
+        rest = xe > 0.0f ? dn : up;
+        q = xe > 0.0f ? up : p.renormalize ? quick_exp(xe - fminf(m, 0.0f)) * up : dn;
     }
-    if (p.renormalize) {
-        total = lanes_sum<L>(q);
-        total = total > 0.0f ? total : 1.0f;
-    }
-    q /= total;
-    const float mean = p.renormalize || dense ? lanes_sum<L>(q * g) : 0.0f;
-    float d = p.scale * q * rest * (p.renormalize ? g - mean : g);
+    if (p.renormalize) total = lanes_sum<L>(q);
+    const float share = total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
+    q *= share;
+    const float mean = DENSE || p.renormalize ? lanes_sum<L>(q * g) : 0.0f;
+    const float d = p.scale * q * rest * (p.renormalize ? g - mean : g);
     // an expert named more than once gets the sum
     float sum = 0.0f;
     for (int j = 0; j < p.top; ++j) {
@@ -188,15 +200,17 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs p)
         sum += live && ej == e ? dj : 0.0f;
     }
     wave_sync();
-    if (live) mine[e] = sum;
+    if (live) reinterpret_cast<float*>(mine)[e] = sum;
     wave_sync();
-    for (int i = sub; i < E; i += L) {
-        float v = mine[i];
-        if (dense) {
-            const float xi = to_f32(row[i]);
-            if (xi > low) v -= p.scale * (exp_below(xi, m) / total) * mean;
-        }
-        out[i] = from_f32<X>(v);
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+        const int at = 4 * (sub + i * L);
+        if (at >= p.experts) break;
+        f32x4 v = mine[at / 4];
+        if constexpr (DENSE)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) v[s] -= p.scale * (x[i][s] * share) * mean;
+        store_four(out + at, v, p.experts - at);
     }
 }
 
