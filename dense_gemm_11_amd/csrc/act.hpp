@@ -93,7 +93,8 @@ __device__ __forceinline__ void act_slope(float x, int act, float& value, float&
         float s, rest;
         sigmoids<PRECISE>(c * (x + k * x * x * x), s, rest);
         value = x * s;
-        slope = s + value * rest * (c * (1.0f + 3.0f * k * x * x));
+        // (the square kept finite: far out value * rest is 0)
+        slope = s + value * rest * (c * (1.0f + 3.0f * k * fminf(x * x, 3e38f)));
     } else if (act == EPI_ACT_GELU) {
         const float phi = normal_cdf<PRECISE>(x), q = -0.5f * x * x;
         const float e = PRECISE ? expf(q) : __builtin_amdgcn_exp2f(q * 1.44269504088896341f);

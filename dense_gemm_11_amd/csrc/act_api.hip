@@ -192,6 +192,10 @@ gemm_status_t gemm_run_grouped_act_grad(gemm_handle_t h, int64_t M, int64_t N,
             (H && (!in_place_or_apart(dD, sd, H, sh, lddd == ldh && es == eo) ||
                    ranges_overlap(Z, sz, H, sh) || ranges_overlap(dZ, so, H, sh))))
             return GEMM_ERR_INVALID_VALUE;
+        const int64_t sb = dbias ? G * width * 4 : 0;
+        if (dbias && (ranges_overlap(dbias, sb, Z, sz) || ranges_overlap(dbias, sb, dD, sd) ||
+                      ranges_overlap(dbias, sb, dZ, so) || (H && ranges_overlap(dbias, sb, H, sh))))
+            return GEMM_ERR_INVALID_VALUE;
     }
     if (dbias && M > 0 &&
         (!ws || !aligned_to(ws, 256) || ws_bytes < gemm_act_grad_workspace_bytes(M, width, (int)G)))
@@ -219,6 +223,7 @@ gemm_status_t gemm_run_grouped_act_grad(gemm_handle_t h, int64_t M, int64_t N,
     const int64_t tile_rows = groups ? grad_tiles(M, G) : ceil_div(M, ACT_GRAD_ROWS);
     if (dbias && M > 0) {
         a.sums = static_cast<float*>(ws);
+        a.tile_rows = (int)grad_tiles(M, G);
         a.firsts = reinterpret_cast<int32_t*>(a.sums + grad_tiles(M, G) * width);
     }
     a.tiles_n = (int)ceil_div(N, 64 * (16 / es));

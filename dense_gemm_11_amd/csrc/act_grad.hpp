@@ -31,6 +31,7 @@ struct ActGradArgs : RaggedArgs {
     float* dbias;
     int64_t ldz, ld_dd, ld_dz, ldh;
     int width;
+    int tile_rows;     // of sums
 };
 
 template <typename T, typename OutT, bool GATE>
@@ -100,6 +101,8 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs p)
     __syncthreads();
     if (wave > 0) return;
     if (tm == 0 && tn == 0 && lane == 0) p.firsts[t.group] = t.first;
+    // (offsets that do not ascend can make more tiles than the workspace has rows)
+    if ((unsigned)(t.first + tm) >= (unsigned)p.tile_rows) return;
     float* out = p.sums + (int64_t)(t.first + tm) * p.width + col;
 #pragma unroll
     for (int h = 0; h < HALVES; ++h)
@@ -122,8 +125,10 @@ __global__ __launch_bounds__(64 * WAVES) void act_bias_kernel(ActGradArgs p)
     for (int g = blockIdx.y; g < p.groups; g += gridDim.y) {
         int start = 0, size = p.M;
         if (p.offsets) group_span(p, g, start, size);
-        const int tiles = (int)(((unsigned)size + ACT_GRAD_ROWS - 1) / ACT_GRAD_ROWS);
-        const int first = tiles > 0 ? p.firsts[g] : 0;
+        int tiles = (int)(((unsigned)size + ACT_GRAD_ROWS - 1) / ACT_GRAD_ROWS);
+        int first = tiles > 0 ? p.firsts[g] : 0;
+        // (nor has then every group a first tile)
+        if (first < 0 || first > p.tile_rows - tiles) first = tiles = 0;
         float s = 0.0f;
         if (col < p.width) {
             const float* in = p.sums + (int64_t)first * p.width + col;

@@ -39,4 +39,21 @@ inline bool ranges_overlap(const void* a, int64_t abytes, const void* b, int64_t
     return a0 < b0 + (uintptr_t)bbytes && b0 < a0 + (uintptr_t)abytes;
 }
 
+// Memory that a call reads or writes (p NULL or no bytes: none).
+struct MemoryRange {
+    const void* p;
+    int64_t bytes;
+};
+// Whether one of the first `written` of n ranges overlaps another one.
+template <int N>
+bool written_overlap(const MemoryRange (&r)[N], int written)
+{
+    for (int i = 0; i < written; ++i)
+        for (int j = i + 1; j < N; ++j)
+            if (r[i].p && r[j].p && r[i].bytes > 0 && r[j].bytes > 0 &&
+                ranges_overlap(r[i].p, r[i].bytes, r[j].p, r[j].bytes))
+                return true;
+    return false;
+}
+
 }  // namespace dg

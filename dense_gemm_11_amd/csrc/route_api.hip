@@ -94,6 +94,12 @@ gemm_status_t gemm_route(gemm_handle_t h, int64_t tokens, const void* logits, in
         !ints_ok(order) || !ints_ok(position) || !ints_ok(r.bias))
         return GEMM_ERR_NOT_SUPPORTED;
 
+    const int64_t es = bf16 ? 2 : 4, chosen = tokens * r.top * 4;
+    if (written_overlap({{ids, chosen}, {weights, chosen}, {offsets, ((int64_t)r.experts + 1) * 4}, {order, chosen},
+                         {position, chosen}, {plan && tokens > 16 ? ws : nullptr, (int64_t)gemm_route_workspace_bytes(tokens, r.experts)},
+                         {logits, ((tokens - 1) * ld + r.experts) * es}, {r.bias, (int64_t)r.experts * 4}}, 6))
+        return GEMM_ERR_INVALID_VALUE;
+
     RouteArgs a{};
     a.logits = logits;
     a.bias = r.bias;
@@ -186,8 +192,9 @@ gemm_status_t gemm_route_grad(gemm_handle_t h, int64_t tokens, const void* logit
     if (tokens == 0) return GEMM_OK;
     if (!logits || !ids || !dweights || !dlogits) return GEMM_ERR_INVALID_VALUE;
     if (tokens > MAX_TOKENS || ld > INT_MAX || ldd > INT_MAX) return GEMM_ERR_NOT_SUPPORTED;
-    if (ranges_overlap(logits, ((tokens - 1) * ld + r.experts) * es, dlogits,
-                       ((tokens - 1) * ldd + r.experts) * es))
+    if (written_overlap({{dlogits, ((tokens - 1) * ldd + r.experts) * es},
+                         {logits, ((tokens - 1) * ld + r.experts) * es}, {ids, tokens * r.top * 4},
+                         {dweights, tokens * r.top * 4}}, 1))
         return GEMM_ERR_INVALID_VALUE;
     if (!aligned_to(logits, es) || !aligned_to(dlogits, es) || !ints_ok(ids) || !ints_ok(dweights))
         return GEMM_ERR_NOT_SUPPORTED;

@@ -106,7 +106,8 @@ gemm_status_t gemm_gather_rows(gemm_handle_t h, int64_t tokens, int64_t cols, in
     if (tokens == 0 || cols == 0 || rows == 0) return GEMM_OK;
     if (!X || !order || !D) return GEMM_ERR_INVALID_VALUE;
     if (!rows_fit(tokens, cols, top, rows) || ldx > INT_MAX || ldd > INT_MAX) return GEMM_ERR_NOT_SUPPORTED;
-    if (ranges_overlap(X, span(tokens, ldx, cols, es), D, span(rows, ldd, cols, eo)))
+    if (written_overlap({{D, span(rows, ldd, cols, eo)}, {X, span(tokens, ldx, cols, es)}, {order, rows * 4},
+                         {weights, tokens * top * 4}}, 1))
         return GEMM_ERR_INVALID_VALUE;
     if (!matrix_ok(X, es) || !matrix_ok(D, eo) || !aligned_to(order, 4) || !aligned_to(weights, 4))
         return GEMM_ERR_NOT_SUPPORTED;
@@ -145,7 +146,8 @@ gemm_status_t gemm_combine_rows(gemm_handle_t h, int64_t tokens, int64_t cols, i
         (beta != 0.0f && ldc > INT_MAX))
         return GEMM_ERR_NOT_SUPPORTED;
     const int64_t span_d = span(tokens, ldd, cols, eo);
-    if ((rows > 0 && ranges_overlap(Y, span(rows, ldy, cols, es), D, span_d)) ||
+    if (written_overlap({{D, span_d}, {Y, span(rows, ldy, cols, es)}, {position, tokens * top * 4},
+                         {weights, tokens * top * 4}}, 1) ||
         (beta != 0.0f && (C == D ? ldc != ldd : ranges_overlap(C, span(tokens, ldc, cols, eo), D, span_d))))
         return GEMM_ERR_INVALID_VALUE;
     if (!matrix_ok(Y, es) || !matrix_ok(D, eo) || (beta != 0.0f && !matrix_ok(C, eo)) ||
@@ -197,6 +199,12 @@ gemm_status_t gemm_combine_rows_grad(gemm_handle_t h, int64_t tokens, int64_t co
     if (rows > 0 && cols > 0 &&
         ((Y == dY ? ldy != lddy : ranges_overlap(Y, span(rows, ldy, cols, es), dY, span_dy)) ||
          ranges_overlap(dD, span(tokens, lddd, cols, eo), dY, span_dy)))
+        return GEMM_ERR_INVALID_VALUE;
+    const int64_t assigned = tokens * top * 4;
+    if (written_overlap({{dweights, assigned}, {cols > 0 ? dY : nullptr, span_dy}, {position, assigned},
+                         {weights, assigned}, {cols > 0 ? Y : nullptr, span(rows, ldy, cols, es)},
+                         {cols > 0 ? dD : nullptr, span(tokens, lddd, cols, eo)}}, 1) ||
+        written_overlap({{cols > 0 ? dY : nullptr, span_dy}, {position, assigned}, {weights, assigned}}, 1))
         return GEMM_ERR_INVALID_VALUE;
     if (!matrix_ok(Y, es) || !matrix_ok(dY, es) || !matrix_ok(dD, eo) || !aligned_to(position, 4) ||
         !aligned_to(weights, 4) || !aligned_to(dweights, 4))

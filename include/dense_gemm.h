@@ -533,7 +533,8 @@ gemm_status_t gemm_run_grouped_act(gemm_handle_t h, gemm_op_t transB, int64_t M,
  * aligned (GEMM_ERR_INVALID_VALUE otherwise), which needs no clearing; calls that
  * may overlap in time need one each.  dZ may be Z, and H may be dD, where they
  * have one type and leading dimension; any other overlap of what is written is
- * rejected.  Rows in no group are not written.  Results are bitwise reproducible. */
+ * rejected.  Rows in no group are not written.  (With offsets that decrease the dbias
+ * of groups that share rows is undefined.)  Results are bitwise reproducible. */
 size_t gemm_act_grad_workspace_bytes(int64_t M, int64_t width, int groups);
 
 gemm_status_t gemm_run_grouped_act_grad(gemm_handle_t h, int64_t M, int64_t N,
@@ -581,7 +582,8 @@ gemm_status_t gemm_run_grouped_act_grad(gemm_handle_t h, int64_t M, int64_t N,
  * GEMM_ERR_INVALID_VALUE: a NULL that is needed, negative sizes, ld < experts,
  * experts or top < 1, top > experts or than the kept groups hold, groups that do not
  * divide experts, top_groups outside [1, groups], group_top other than 1 and 2, a
- * scale that is not finite, part of a plan, too small a workspace.
+ * scale that is not finite, part of a plan, too small a workspace, an output (or
+ * the workspace, where it is needed) that overlaps another one or an input.
  * GEMM_ERR_NOT_SUPPORTED: experts > 1024, top > 32, groups > 64, tokens above 2^26 -
  * 64, ld above 2^31 - 1, pointers that are not element-aligned. */
 typedef enum { GEMM_SCORES_SOFTMAX = 0, GEMM_SCORES_SIGMOID = 1 } gemm_scores_t;
@@ -610,7 +612,7 @@ gemm_status_t gemm_route(gemm_handle_t h, int64_t tokens, const void* logits, in
  *     sigmoid, renormalised  dx_j = c q_j (1 - s_j) (g_j - sum_l g_l q_l)
  * and 0 for the others.  Of `routing` experts, top, scores, renormalize and scale
  * are read.  dlogits (rows ldd >= experts apart) has the logits' type and may not
- * overlap them; every one of its tokens x experts elements is written.  ids outside
+ * overlap an input; every one of its tokens x experts elements is written.  ids outside
  * [0, experts) have no part; an expert named twice gets the sum. */
 gemm_status_t gemm_route_grad(gemm_handle_t h, int64_t tokens, const void* logits, int64_t ld,
                               gemm_dtype_t dtype, const gemm_routing_t* routing, const int32_t* ids,

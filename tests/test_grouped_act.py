@@ -314,6 +314,47 @@ def test_grouped_act_grad(h, case, dtype, gated, in_place):
                        (torch.float32, "dbias " + name))
 
 
+@gpu
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_values_and_slopes_far_out(h, dtype):
+    """Finite Z whose square or cube is not: act(x) is x or 0 and act' 1 or 0,
+    exactly, from |x| = 2^7 on (the tails are below 2^-180)."""
+    require_gpu()
+    ti, to = TYPES[dtype]
+    x = torch.tensor([2.0 ** e for e in (7, 20, 42, 60, 64, 100, 126, 127)])
+    x = torch.cat([x, -x]).to(to)[:, None]
+    up = (x > 0).to(ti).cuda()
+    for name in ("relu", "gelu", "silu", "gelu_tanh"):
+        announce("far out", dtype, name)
+        D, Z = (torch.empty(16, 1, dtype=to, device="cuda") for _ in range(2))
+        g().run_grouped_act(h, x.to(ti).cuda(), torch.ones(1, 1, dtype=ti, device="cuda"), D, None,
+                            activation=name, Z=Z)
+        assert torch.equal(Z.cpu(), x) and torch.equal(D.cpu(), x.clamp_min(0.0)), name
+        dZ, H = (torch.empty(16, 1, dtype=ti, device="cuda") for _ in range(2))
+        g().run_grouped_act_grad(h, Z, torch.ones_like(D), dZ, None, activation=name, H=H)
+        assert torch.equal(dZ, up) and torch.equal(H.cpu().to(to), x.clamp_min(0.0)), name
+
+
+@gpu
+def test_act_grad_stays_inside_with_offsets_that_descend(h):
+    """Groups that share rows make more tiles than the workspace has rows: their
+    sums are anything, but nothing beyond the rows, the sums and the workspace is
+    read or written."""
+    require_gpu()
+    M, N = 1000, 72
+    Z, dD = (draw((M + 8, N), i, torch.float32).cuda() for i in (1, 2))
+    for off in ([0, M, 0, M, 0, M, 3], [M, 0, 1 << 30, -5, 40, 7, M], [0] + [M, 0] * 40):
+        announce("offsets that descend", off[:6])
+        G = len(off) - 1
+        need = g().gemm_act_grad_workspace_bytes(M, N, G)
+        ws = torch.full((need + 65536,), 255, dtype=torch.uint8, device="cuda")
+        dZ, dbias = torch.full((M + 8, N), 7.0, device="cuda"), torch.full((G + 4, N), 7.0, device="cuda")
+        g().run_grouped_act_grad(h, Z[:M], dD[:M], dZ[:M], torch.tensor(off, dtype=torch.int32, device="cuda"),
+                                 activation="silu", dbias=dbias[:G], workspace=ws[:need])
+        torch.cuda.synchronize()
+        assert (ws[need:] == 255).all() and (dZ[M:] == 7.0).all() and (dbias[G:] == 7.0).all()
+
+
 @pytest.mark.parametrize("name", ACTS)
 def test_slopes_against_differences(name):
     """The slopes above against central differences in 64 bits: with steps of 1e-5
@@ -398,10 +439,11 @@ def test_act_grad_refusals(h):
     for kw in (dict(M=-1), dict(N=-1), dict(activation=9), dict(dtype=5), dict(ldz=15), dict(lddd=7),
                dict(lddz=15), dict(ldh=7), dict(Z=None), dict(dD=None), dict(dZ=None), dict(ws=None),
                dict(ws=FAKE + 64), dict(ws_bytes=64), dict(dZ=z + 8), dict(dZ=z, lddz=17),
-               dict(dZ=z, dtype=1), dict(dZ=dd), dict(H=z), dict(H=dz), dict(H=dd, ldh=9)):
+               dict(dZ=z, dtype=1), dict(dZ=dd), dict(H=z), dict(H=dz), dict(H=dd, ldh=9),
+               dict(dbias=z + 312), dict(dbias=dd - 124), dict(dbias=dz), dict(dbias=hh)):
         assert grad(h, **kw) == bad, kw
     assert grad(h, groups=(2, None, None)) == bad and grad(h, groups=(-2, FAKE, None)) == bad
-    for kw in (dict(Z=z + 1), dict(dD=dd + 1), dict(dZ=dz + 1), dict(H=hh + 1), dict(dbias=FAKE + 2),
+    for kw in (dict(Z=z + 1), dict(dD=dd + 1), dict(dZ=dz + 1), dict(H=hh + 1), dict(dbias=FAKE + (4 << 30) + 2),
                dict(N=1 << 30, ldz=1 << 31, lddd=1 << 30, lddz=1 << 31, ldh=1 << 30),
                dict(lddd=1 << 31, M=1)):
         assert grad(h, **kw) == no, kw

@@ -371,8 +371,9 @@ def call(h, routing=None, **kw):
     r = dict(experts=16, top=2, scores=0, groups=1, top_groups=1, group_top=1, bias=None, renormalize=0,
              scale=1.0)
     r.update(routing or {})
-    a = dict(tokens=100, logits=FAKE, ld=16, dtype=0, ids=FAKE, weights=FAKE, offsets=FAKE, order=FAKE,
-             position=FAKE, ws=FAKE, ws_bytes=1 << 20)
+    ids, weights, offsets, order, position, ws = (FAKE + (i << 36) for i in range(1, 7))
+    a = dict(tokens=100, logits=FAKE, ld=16, dtype=0, ids=ids, weights=weights, offsets=offsets, order=order,
+             position=position, ws=ws, ws_bytes=1 << 20)
     a.update(kw)
     rt = None if routing == "none" else m.GemmRouting(**r)
     return m.gemm_route(h, a["tokens"], a["logits"], a["ld"], a["dtype"], rt, a["ids"], a["weights"],
@@ -398,6 +399,18 @@ def test_route_refuses_invalid_values(h):
               dict(groups=4, group_top=3), dict(groups=4, group_top=0),
               dict(groups=8, top_groups=1, top=3), dict(scale=float("nan")), dict(scale=float("inf"))):
         assert call(h, r) == bad, r
+
+
+def test_route_refuses_outputs_that_overlap(h):
+    """100 tokens of 16 experts, 2 each: ids, weights, order and position of 800 bytes."""
+    bad = g().GEMM_ERR_INVALID_VALUE
+    ids, weights, offsets, order, position, ws = (FAKE + (i << 36) for i in range(1, 7))
+    for kw in (dict(ids=FAKE + 6396), dict(weights=ids + 796), dict(offsets=ids - 64), dict(order=offsets),
+               dict(position=order + 796), dict(position=ids), dict(ws=FAKE), dict(ws=order + 512),
+               dict(order=FAKE)):
+        assert call(h, **kw) == bad, kw
+    assert call(h, dict(bias=weights + 796)) == bad and call(h, dict(bias=offsets + 64)) == bad
+    assert call(h, ids=FAKE, offsets=None, order=None, position=None) == bad
 
 
 def test_route_refuses_what_it_does_not_support(h):
@@ -437,7 +450,8 @@ def test_route_grad_refusals(h):
         return m.gemm_route_grad(h, a["tokens"], a["logits"], a["ld"], a["dtype"], m.GemmRouting(**q),
                                  a["ids"], a["dw"], a["out"], a["ldd"], None)
     for kw in (dict(tokens=-1), dict(ld=15), dict(ldd=15), dict(dtype=-1), dict(logits=None), dict(ids=None),
-               dict(dw=None), dict(out=None), dict(out=FAKE + 64)):
+               dict(dw=None), dict(out=None), dict(out=FAKE + 64), dict(ids=FAKE + (1 << 20)),
+               dict(dw=FAKE + (1 << 20) + 6396)):
         assert grad(**kw) == m.GEMM_ERR_INVALID_VALUE, kw
     assert grad(dict(top=17)) == m.GEMM_ERR_INVALID_VALUE
     for kw in (dict(out=FAKE + (1 << 20) + 2), dict(dw=FAKE + 2), dict(tokens=1 << 26, ld=16)):

@@ -215,7 +215,8 @@ def test_gather_refusals(h):
                                                        "weights", "D", "ldd", "dtype")], None)
     assert call(None) == m.GEMM_ERR_INVALID_VALUE
     for kw in (dict(tokens=-1), dict(cols=-1), dict(rows=-1), dict(top=0), dict(ldx=7), dict(ldd=7),
-               dict(X=None), dict(order=None), dict(D=None), dict(D=FAKE + 32), dict(dtype=3)):
+               dict(X=None), dict(order=None), dict(D=None), dict(D=FAKE + 32), dict(dtype=3),
+               dict(order=FAR + 632), dict(weights=FAR - 76)):
         assert call(**kw) == m.GEMM_ERR_INVALID_VALUE, kw
     for kw in (dict(tokens=1 << 24), dict(rows=1 << 24, D=FAKE + (1 << 40)), dict(top=1 << 30),
                dict(cols=1 << 27, ldx=1 << 27, ldd=1 << 27, D=FAKE + (1 << 40)), dict(X=FAKE + 2),
@@ -235,7 +236,8 @@ def test_combine_refusals(h):
                                                        "weights", "beta", "C", "ldc", "D", "ldd", "dtype")], None)
     for kw in (dict(tokens=-1), dict(top=-1), dict(ldy=7), dict(ldd=7), dict(Y=None), dict(position=None),
                dict(D=None), dict(D=FAKE + 32), dict(beta=1.0), dict(beta=1.0, C=FAR, ldc=7),
-               dict(beta=1.0, C=FAR, ldc=9), dict(beta=1.0, C=FAR + 32), dict(dtype=-1)):
+               dict(beta=1.0, C=FAR, ldc=9), dict(beta=1.0, C=FAR + 32), dict(dtype=-1),
+               dict(position=FAR + 316), dict(weights=FAR)):
         assert call(**kw) == m.GEMM_ERR_INVALID_VALUE, kw
     for kw in (dict(tokens=1 << 24, D=FAKE + (1 << 40)), dict(Y=FAKE + 1), dict(position=FAKE + 1),
                dict(beta=1.0, C=FAR + (1 << 20) + 2), dict(weights=FAKE + 2)):
@@ -248,16 +250,17 @@ def test_combine_grad_refusals(h):
 
     def call(**kw):
         a = dict(tokens=10, cols=8, top=2, Y=FAKE, ldy=8, rows=20, position=FAKE, weights=FAKE, dD=FAKE,
-                 lddd=8, dY=FAR, lddy=8, dw=FAKE, dtype=0)
+                 lddd=8, dY=FAR, lddy=8, dw=FAR + (1 << 20), dtype=0)
         a.update(kw)
         return m.gemm_combine_rows_grad(h, *[a[k] for k in ("tokens", "cols", "top", "Y", "ldy", "rows",
                                                             "position", "weights", "dD", "lddd", "dY", "lddy",
                                                             "dw", "dtype")], None)
     for kw in (dict(rows=-1), dict(lddd=7), dict(lddy=7), dict(Y=None), dict(weights=None), dict(dw=None),
                dict(dD=None), dict(dY=None), dict(dY=FAKE + 32), dict(dY=FAKE, lddy=9), dict(dD=FAR),
-               dict(dtype=7)):
+               dict(dtype=7), dict(dw=FAKE), dict(dw=FAR + 636), dict(position=FAR), dict(weights=FAR + 4),
+               dict(weights=FAR + (1 << 20) + 76)):
         assert call(**kw) == m.GEMM_ERR_INVALID_VALUE, kw
-    for kw in (dict(tokens=1 << 24, dY=FAKE + (1 << 40)), dict(dD=FAKE + 2), dict(dw=FAKE + 2)):
+    for kw in (dict(tokens=1 << 24, dY=FAKE + (1 << 40)), dict(dD=FAKE + 2), dict(dw=FAR + (1 << 20) + 2)):
         assert call(**kw) == m.GEMM_ERR_NOT_SUPPORTED, kw
     assert call(tokens=0, dD=None) == m.GEMM_OK
 
@@ -269,7 +272,7 @@ def test_failed_launches_are_reported(monkeypatch):
     assert m.gemm_gather_rows(hh, 10, 8, 2, FAKE, 8, 20, FAKE, None, FAR, 8, 0, None) == m.GEMM_ERR_HIP
     assert m.gemm_combine_rows(hh, 10, 8, 2, FAKE, 8, 20, FAKE, None, 0.0, None, 8, FAR, 8, 0,
                                None) == m.GEMM_ERR_HIP
-    assert m.gemm_combine_rows_grad(hh, 10, 8, 2, FAKE, 8, 20, FAKE, FAKE, FAKE, 8, FAR, 8, FAKE, 0,
+    assert m.gemm_combine_rows_grad(hh, 10, 8, 2, FAKE, 8, 20, FAKE, FAKE, FAKE, 8, FAR, 8, FAR + 4096, 0,
                                     None) == m.GEMM_ERR_HIP
     m.gemm_destroy(hh)
 
