@@ -780,9 +780,27 @@ __device__ __forceinline__ void dma_gemm_body(Args p)
     const bool guard_last = RAG == RAG_NONE ? k_ragged || edge : (k_ragged && !REBASE) || odd_end;
     const int nk_dma = ALIGNED ? ((last && guard_last) ? nk - 1 : nk) : 0;
 
+    // A k-contiguous B that one row of tiles reads comes from memory as fast as it
+    // can, and rows a power of two apart keep few of its channels busy while all
+    // workgroups read at the same k: the XCDs begin an eighth of K apart there and go
+    // round (64 groups of 4096x4096, 64, 128 and 256 rows each: 0.428 -> 0.368 ms,
+    // 0.496 -> 0.437 and 0.655 -> 0.622).  Elsewhere it costs 2 %: the tiles of one
+    // column read B together.  The turn is such that a round of steps never wraps.
+    constexpr bool TURNS = ACTED && B_KC;
+    static_assert(!TURNS || (Cfg::LATE && P == ((PA && PB) ? 2 * NP : AHEAD)), "a round's copies");
+    int turn = 0;
+    if constexpr (TURNS)
+        if (p.tiles_m == 1 && nk_dma == nk && (!PAIRED || nk % 2 == 0))
+            turn = nk - (nk - (int)((uint64_t)(blockIdx.x & 7) * nk >> 3)) / P * P;
+    // K-step of step kt
+    auto k_of = [&](int kt) __attribute__((always_inline)) {
+        if constexpr (TURNS) return kt + turn >= nk ? kt + turn - nk : kt + turn;
+        return k_lo + kt;
+    };
+
     // step kt of the staged operands into a stage array
     auto load = [&](int kt, char* base) __attribute__((always_inline)) {
-        const int k0 = (k_lo + kt) * BK;
+        const int k0 = k_of(kt) * BK;
         if (kt < nk_dma) {
             if constexpr (REBASE) {
                 oa.dma(OpA::panel_rsrc(panel_a + (int64_t)k0 * p.lda, end_a), 0, base, wave);
@@ -800,7 +818,7 @@ __device__ __forceinline__ void dma_gemm_body(Args p)
     // steps 2q and 2q+1 of the paired operands into a pair buffer (one DMA
     // copy when both are DMA steps, else each existing step register-staged)
     auto load_pair = [&](int q, char* base) __attribute__((always_inline)) {
-        const int k0 = (k_lo + 2 * q) * BK;
+        const int k0 = k_of(2 * q) * BK;
         if (2 * q + 1 < nk_dma) {
             if constexpr (PA) oa.dma(rsrc_a, OpA::step_bytes(k0, p.lda), base, wave);
             if constexpr (PB) ob.dma(rsrc_b, OpB::step_bytes(k0, p.ldb), base + A_PR, wave);
@@ -1024,16 +1042,38 @@ __device__ __forceinline__ void dma_gemm_body(Args p)
     };
 
     int kt = 0;
+    // (ACTED) A wave whose rows or columns all lie past the group's copies with the
+    // others and computes nothing: where two waves share a SIMD, the other has the
+    // matrix core to itself (64 groups of 128 rows in tiles of 256, 4096x4096 gated
+    // bf16: 0.491 -> 0.466 ms, with B in the caches 0.363 -> 0.279).
+    if constexpr (ACTED) {
+        const int wv = __builtin_amdgcn_readfirstlane(wave);
+        if (wv / Cfg::WN * Cfg::WTM >= rlim_a || wv % Cfg::WN * (Cfg::WTN / (GATE ? 2 : 1)) >= rlim_b) {
+            auto idle = [&](auto cur_c) __attribute__((always_inline)) {
+                constexpr int CUR = decltype(cur_c)::value;
+                if (kt >= nk) return;
+                if (kt + LOOK < nk) wait_vm_lgkm0<(CUR & 1) ? WAIT_O : WAIT_E>();
+                else wait_vm_lgkm0<0>();
+                barrier_only();
+                if (kt + AHEAD < nk) load(kt + AHEAD, stage((CUR + FILL) % S));
+                if constexpr (PAIRED && (CUR & 1) != 0)
+                    if (kt + 2 * NP - 1 < nk) load_pair((kt + 2 * NP - 1) / 2, pr((CUR >> 1) % NP));
+                ++kt;
+            };
+            while (kt < nk) static_for<P>([&](auto c) __attribute__((always_inline)) { idle(c); });
+        }
+    }
     // steady state: every step of the round issues its copies as DMA (the
     // last step of a round copies up to step kt + P - 1 + LAST_AHEAD)
     constexpr int LAST_AHEAD = PAIRED && AHEAD < 2 * NP ? 2 * NP : AHEAD;
     for (; kt + P - 1 + LAST_AHEAD < nk_dma; kt += P) {
-        steady(I0{}, kt);
-        steady(I1{}, kt + 1);
-        if constexpr (P > 2) steady(I2{}, kt + 2);
-        if constexpr (P > 3) steady(I3{}, kt + 3);
-        if constexpr (P > 4) steady(I4{}, kt + 4);
-        if constexpr (P > 5) steady(I5{}, kt + 5);
+        const int at = TURNS ? k_of(kt + P) - P : kt;
+        steady(I0{}, at);
+        steady(I1{}, at + 1);
+        if constexpr (P > 2) steady(I2{}, at + 2);
+        if constexpr (P > 3) steady(I3{}, at + 3);
+        if constexpr (P > 4) steady(I4{}, at + 4);
+        if constexpr (P > 5) steady(I5{}, at + 5);
     }
     // tail: remaining steps with run-time checks (guarded copies allowed)
     for (; kt < nk; kt += P) {
@@ -1397,6 +1437,7 @@ __device__ __forceinline__ void dma_gemm_body(Args p)
             bias_u[j] = GATE ? act_bias<OutT>(p, p.N + col, p.N - col) : f32x4{};
         }
         __syncthreads();  // every wave is done reading operands from the stage arrays
+        if (tm * BM + wv / Cfg::WN * Cfg::WTM >= p.M) return;
         static_for<MF * NFH>([&](auto x_c) __attribute__((always_inline)) {
             constexpr int i = decltype(x_c)::value / NFH, j = decltype(x_c)::value % NFH;
 #pragma unroll
