@@ -175,7 +175,9 @@ __global__ __launch_bounds__(256) void combine_rows_kernel(RowsArgs p, int lanes
     else sum_up(std::false_type{});
 }
 
-// A workgroup per token, JB of its rows at a time.
+// A workgroup per token, JB of its rows at a time.  dD, read again for each JB of
+// them, is loaded in the ordinary way: 4096 tokens of 4096 bf16, 8 rows each 119 ->
+// 110 us (5.2 TB/s), 5 rows 79 -> 70, and of 2 no slower (8192 tokens 65 -> 64).
 template <typename T, typename OutT, int JB>
 __global__ __launch_bounds__(256) void combine_rows_grad_kernel(RowsArgs p)
 {
@@ -199,7 +201,7 @@ __global__ __launch_bounds__(256) void combine_rows_grad_kernel(RowsArgs p)
         auto piece = [&](auto full, int col, int n) __attribute__((always_inline)) {
             constexpr bool FULL = decltype(full)::value;
             float d[VEC], y[JB][VEC];
-            load_row_vec<FULL>(d, dD + col, n);
+            load_row_vec<FULL, false>(d, dD + col, n);
             if (p.rows > 0) {
 #pragma unroll
                 for (int j = 0; j < JB; ++j)
