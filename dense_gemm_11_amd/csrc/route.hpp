@@ -23,9 +23,9 @@
 // neighbours among the chosen (or the last of them and the next) are closer than
 // what is cut off, or scores closer than their fp32 errors, the token's candidates,
 // one to a lane, are compared for certain (route_rank).  A token for which that is
-// not enough (three so close, sums of groups, a softmax with a bias) is chosen for
-// again in 64 bits by a wave of its own once its workgroup is done with the others
-// (route_exact).
+// not enough (three so close, sums of groups, softmax scores with a bias that 32
+// bits cannot tell apart) is chosen for again in 64 bits by a wave of its own once
+// its workgroup is done with the others (route_exact), about 5 us more for a launch.
 #pragma once
 
 #include "common.hpp"
@@ -78,6 +78,19 @@ __device__ __forceinline__ double dpp(double x)
                             __builtin_amdgcn_mov_dpp(__double2loint(x), CTRL, 0xf, 0xf, true));
 }
 
+// x of one lane.
+template <int LANE>
+__device__ __forceinline__ float lane_of(float x)
+{
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), LANE));
+}
+template <int LANE>
+__device__ __forceinline__ double lane_of(double x)
+{
+    return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(x), LANE),
+                            __builtin_amdgcn_readlane(__double2loint(x), LANE));
+}
+
 __device__ __forceinline__ float max_of(float a, float b) { return fmaxf(a, b); }
 __device__ __forceinline__ double max_of(double a, double b) { return fmax(a, b); }
 
@@ -90,10 +103,7 @@ __device__ __forceinline__ K lanes_reduce(K x, F op)
     x = op(x, dpp<0x4E>(x));   // quad_perm 2, 3, 0, 1
     x = op(x, dpp<0x141>(x));  // row_half_mirror
     x = op(x, dpp<0x140>(x));  // row_mirror
-    if constexpr (L == 64) {
-        x = op(x, __shfl_xor(x, 16));
-        x = op(x, __shfl_xor(x, 32));
-    }
+    if constexpr (L == 64) x = op(op(lane_of<0>(x), lane_of<16>(x)), op(lane_of<32>(x), lane_of<48>(x)));
     return x;
 }
 template <int L, typename K>
@@ -291,28 +301,31 @@ __device__ __forceinline__ float chosen_score(const RouteArgs& p, float x, float
 // How far a token's choice is certain.
 enum : int { ROUTE_SURE = 0, ROUTE_RANK = 1, ROUTE_AGAIN = 2 };
 
+// (see route_quick)
+__device__ __forceinline__ float near_softmax(float share) { return 1.0f + 60.0f * share; }
+
 // Chooses a token's experts: the j-th of them, and the one after the last, to lane
 // j of its L lanes (-1: none), and returns how certain that is, in every lane.
+// share: one over a softmax's sum, the largest p, where there is a bias.
 // BIAS: by scores with a bias, which it forms in fp32.  In units u of 2^-24 a
 // sigmoid is off by 4 at most and the sum c with the bias by |c| more, so two
 // choices may be in the wrong order up to 8 + 2 |c| apart.  A softmax is off by
 // |x - m| e^(x - m) <= 0.37 for its argument and 4 p for its exponential and
 // products, and its sum by 49 of itself at most (of which 38 are additions), which
 // shifts two choices against each other by 49 of the largest p: 0.8 + 57 p + 2 |c|.
-// `close` times 1 + |c| is more than that, and twice it more than what sums of two
-// choices are off by.
+// Sums of two choices are off by the choices' errors and by |c| + |c'| more (which
+// may be large where the sum is not), two of them by twice the above + 8 |c|;
+// without a bias, of exponentials or sigmoids up to 1, by 2 (2 4.4 + 2) < 26.
+// `near` is a little more than the part that does not depend on c.
 template <typename X, int L, int V, bool BIAS>
 __device__ __forceinline__ int route_quick(const RouteArgs& p, const TokenPart<X, L, V>& in, float most,
-                                           int& expert)
+                                           int& expert, float& share)
 {
     constexpr int BITS = sizeof(X) == 2 && !BIAS ? 16 : __builtin_ctz(L * V);
     constexpr uint32_t PLACES = (1u << BITS) - 1u;
     constexpr bool WHOLE = BITS == 16;  // nothing of the value is cut off
     const int lane = threadIdx.x & 63, sub = lane & (L - 1);
-    float close = 0x1p-20f;
-    auto apart = [&](float a, float b, float times) __attribute__((always_inline)) {
-        return a - b > times * close * (1.0f + fmaxf(fabsf(a), fabsf(b)));
-    };
+    float near = BIAS ? 10.0f : 13.0f;
     bool again = false;
     uint32_t c[V];
     if constexpr (BIAS) {
@@ -328,8 +341,8 @@ __device__ __forceinline__ int route_quick(const RouteArgs& p, const TokenPart<X
                 s[i] = in.x[i] > -__builtin_inff() ? quick_exp_below(in.x[i], most) : 0.0f;
                 sum += s[i];
             }
-            sum = 1.0f / lanes_sum<L>(sum);  // the largest p
-            close = 0x1p-24f * (2.0f + 64.0f * sum);
+            share = sum = 1.0f / lanes_sum<L>(sum);
+            near = near_softmax(share);
 #pragma unroll
             for (int i = 0; i < V; ++i) s[i] *= sum;
         }
@@ -353,6 +366,7 @@ __device__ __forceinline__ int route_quick(const RouteArgs& p, const TokenPart<X
         group_two(p.lanes_per_group, a, b);
         const bool sums = p.group_top > 1;
         uint32_t score = a;
+        float size = 0.0f;  // of the largest choice in a sum
         if (sums && a >= LEAST) {
             // (without a bias: of the two logits' scores, a softmax's up to its sum)
             float f = key_value(a), g = key_value(b);
@@ -361,6 +375,7 @@ __device__ __forceinline__ int route_quick(const RouteArgs& p, const TokenPart<X
                 g = p.sigmoid ? quick_sigmoid(g) : quick_exp_below(g, most);
             }
             score = order_key(b >= LEAST ? f + g : f);
+            if constexpr (BIAS) size = fmaxf(fabsf(f), b >= LEAST ? fabsf(g) : 0.0f);
         }
         bool kept = false;
         uint32_t m = 0;
@@ -373,7 +388,9 @@ __device__ __forceinline__ int route_quick(const RouteArgs& p, const TokenPart<X
         again = __popcll(lanes_mask<L>(__ballot(kept), lane)) > p.top_groups * p.lanes_per_group;
         if (BIAS || sums) {
             const uint32_t next = lanes_most<L>(kept ? 0u : score);
-            again |= next >= LEAST && !apart(key_value(m), key_value(next), 2.0f);
+            const float hi = key_value(m), lo = key_value(next);
+            if constexpr (BIAS) size = sums ? lanes_max<L>(size) : fmaxf(fabsf(hi), fabsf(lo));
+            again |= next >= LEAST && !(hi - lo > 0x1p-24f * (2.0f * near + 9.0f * size));
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) c[i] = kept ? c[i] : 0u;
@@ -383,7 +400,7 @@ __device__ __forceinline__ int route_quick(const RouteArgs& p, const TokenPart<X
     const uint32_t place = PLACES - V * sub;
 #pragma unroll
     for (int i = 0; i < V; ++i) c[i] = (c[i] & ~PLACES) + (place - i);
-    uint32_t m = 0, mine = 0, last = 0;  // this choice, lane j's, the last that counts
+    uint32_t m = 0, mine = 0;  // this choice, lane j's
     bool rank = false;
     auto next = [&]() __attribute__((always_inline)) {
         uint32_t d = m - 1u - c[0];
@@ -391,36 +408,40 @@ __device__ __forceinline__ int route_quick(const RouteArgs& p, const TokenPart<X
         for (int i = 1; i < V; ++i) d = least_of(d, m - 1u - c[i]);
         m = m - 1u - lanes_pick<L>(d, [](uint32_t a, uint32_t b) { return least_of(a, b); });
     };
-    // whether hi, at the least, is above m at the most
-    auto sure = [&](uint32_t hi) __attribute__((always_inline)) {
-        if constexpr (BIAS) return apart(key_value(hi & ~PLACES), key_value(m | PLACES), 1.0f);
-        else return (hi & ~PLACES) > (m | PLACES);
+    // whether hi, at the least, is above lo at the most
+    auto sure = [&](uint32_t hi, uint32_t lo) __attribute__((always_inline)) {
+        if constexpr (BIAS) {
+            const float a = key_value(hi & ~PLACES), b = key_value(lo | PLACES);
+            return a - b > 0x1p-24f * (near + 3.0f * fmaxf(fabsf(a), fabsf(b)));
+        } else return (hi & ~PLACES) > (lo | PLACES);
     };
     for (int j = 0; j < p.top; ++j) {
-        last = m;
         next();
         mine = sub == j ? m : mine;
-        if constexpr (!WHOLE) rank |= j > 0 && m >= LEAST && !sure(last);
     }
     if constexpr (!WHOLE) {
-        last = m;
+        const uint32_t last = m;
         next();
         mine = sub == p.top ? m : mine;
-        rank |= m >= LEAST && !sure(last);
+        // each lane's choice against the one before, of the lane before
+        const uint32_t before = L == 16 ? dpp<0x111>(mine) : dpp<0x138>(mine);  // row_shr, wave_shr: 1
+        const bool meet = sub > 0 && sub <= p.top && mine >= LEAST && !sure(before, mine);
+        rank = lanes_mask<L>(__ballot(meet), lane) != 0;
         if (__any(rank)) {
             next();  // has to be below the last for certain
-            again |= rank && m >= LEAST && !sure(last);
+            again |= rank && m >= LEAST && !sure(last, m);
         }
     }
-    if (BIAS && !p.sigmoid) again |= rank;
     expert = mine < LEAST ? -1 : TokenPart<X, L, V>::expert_at(p, p.lanes_per_group, PLACES - (mine & PLACES));
     return again ? ROUTE_AGAIN : rank ? ROUTE_RANK : ROUTE_SURE;
 }
 
 // Puts the candidates of lanes 0 .. top (one more than are chosen) in their order,
-// of logits or of sigmoids with a bias in 64 bits; c: the lane's.
+// of logits or of sigmoids with a bias in 64 bits, or of softmax scores with a bias
+// in all of their 32; c: the lane's.  `tight` where another one is as near as `off`.
 template <int L>
-__device__ __forceinline__ int route_rank(const RouteArgs& p, int expert, double c, int32_t* picked)
+__device__ __forceinline__ int route_rank(const RouteArgs& p, int expert, double c, double off,
+                                          int32_t* picked, bool& tight)
 {
     const int lane = threadIdx.x & 63, sub = lane & (L - 1);
     const bool in = sub <= p.top && expert >= 0;
@@ -429,6 +450,7 @@ __device__ __forceinline__ int route_rank(const RouteArgs& p, int expert, double
     int before = 0;  // candidates ahead of the lane's
     auto meet = [&](double c2, int e2) __attribute__((always_inline)) {
         before += c2 > c || (c2 == c && e2 < e);
+        tight |= fabs(c2 - c) <= off && e2 != e;
     };
     if constexpr (L == 16) {
         static_for<15>([&](auto q_c) __attribute__((always_inline)) {
@@ -634,14 +656,29 @@ __global__ __launch_bounds__(1024) void route_kernel(RouteArgs p)
         float most, total;
         in.sums(p, most, total);
         int expert;
-        const int certain = route_quick<X, L, V, BIAS>(p, in, most, expert);
+        float share = 0.0f;
+        int certain = route_quick<X, L, V, BIAS>(p, in, most, expert, share);
         if (__any(certain == ROUTE_RANK)) {
-            double c = 0.0;
+            double c = 0.0, off = -1.0;
             if (live && expert >= 0) {
-                c = to_f32(static_cast<const X*>(p.logits)[(int64_t)(t0 + i) * p.ld + expert]);
-                if constexpr (BIAS) c = 1.0 / (1.0 + exp(-c)) + p.bias[expert];
+                const float x = to_f32(static_cast<const X*>(p.logits)[(int64_t)(t0 + i) * p.ld + expert]);
+                if constexpr (BIAS) {
+                    const float b = p.bias[expert];
+                    if (p.sigmoid) {
+                        c = 1.0 / (1.0 + exp(-(double)x)) + b;
+                    } else {
+                        const float v = quick_exp_below(x, most) * share + b;
+                        c = v;
+                        off = 0x1p-24f * (near_softmax(share) + 3.0f * fabsf(v));
+                    }
+                } else {
+                    c = x;
+                }
             }
-            const int ranked = route_rank<L>(p, expert, c, picked[slot]);
+            bool tight = false;
+            const int ranked = route_rank<L>(p, expert, c, off, picked[slot], tight);
+            if (BIAS && certain == ROUTE_RANK && lanes_mask<L>(__ballot(tight), lane) != 0)
+                certain = ROUTE_AGAIN;
             expert = certain == ROUTE_RANK ? ranked : expert;
         }
         // (the first logits were asked for before the workgroup meets)

@@ -223,6 +223,20 @@ def test_route_separates_scores_that_fp32_cannot():
 
 
 @gpu
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_route_sums_of_choices_far_larger_than_themselves(kind):
+    """Groups of one bias near 1000 and one near -1000: fp32 rounds their choices to
+    2^-15, the sums decide by less."""
+    require_gpu()
+    announce("route large biases", kind)
+    x = draw(3000, 16, "f32", 3, False)
+    x[:, [0, 1, 5, 8, 9, 13]] /= 64  # sums of several groups next to each other
+    bias = torch.tensor([1000.0, -1000.0, -4000.0, -4000.0] * 4) + torch.tensor([0.125, -0.125, 0, 0] * 4)
+    opt = dict(kind=kind, bias=bias.cuda(), groups=4, top_groups=2, group_top=2)
+    check(x, run(x.cuda(), 4, **opt), 4, **opt)
+
+
+@gpu
 def test_route_without_plan_without_tokens_and_on_a_stream():
     require_gpu()
     announce("route without plan")
