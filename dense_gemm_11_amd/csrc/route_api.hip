@@ -122,8 +122,9 @@ gemm_status_t gemm_route(gemm_handle_t h, int64_t tokens, const void* logits, in
     // 16 lanes to a token where they have room (for a candidate more than are chosen,
     // too; 32 scores and biases to a lane spill): few lanes to a token take fewer
     // instructions, but a single token, or a token to each SIMD and no more, is
-    // sooner done in 64 (one of 64 experts 3.9 us, 17 of them 4.6 in 16 lanes each
-    // and 16 of them 5.6 in 64; 256 tokens of 256 experts 9.6 us in 64).
+    // sooner done in 64 (one of 256 experts in groups with a bias 5.7 us, in 16 lanes
+    // 6.8; 17 of 64 experts 6.2, in 16 3.9; 1024 of 256 experts 9.9, in 16 10.5, and
+    // 2048 of them 10.5, in 16 9.6).
     int padded = 1;
     while (padded < groups) padded *= 2;
     auto per_lane = [&](int lanes) {  // log2 of the experts to a lane (in 64 lanes: 5 at most)
@@ -133,11 +134,11 @@ gemm_status_t gemm_route(gemm_handle_t h, int64_t tokens, const void* logits, in
     };
     const bool fits16 = padded <= 16 && r.top < 16 && per_lane(16) <= (r.bias ? 4 : 5);
     // One workgroup makes the plan with the choice (a launch less: 2.5 us for the
-    // host) until its passes take longer than that: 96 tokens of 64 experts 7.6 us
-    // either way, of 256 experts 12.8 against 9.1, 64 of those 8.1 against 8.9, 32 of
-    // 256 with a bias and groups 8.6 against 10.1 and 64 of them 12.6 against 10.4.
-    const bool one = fits16 ? tokens <= ROUTE_ONE && tokens << per_lane(16) <= (r.bias ? 512 : 1024)
-                            : tokens <= 16;
+    // host) until its passes take longer than that: 96 tokens of 64 experts 6.5 us
+    // against 7.1, 64 of 256 experts 8.0 against 7.7 and 96 of them 12.7 against 8.6, 32
+    // of 256 in groups with a bias 6.8 against 8.4 and 64 of them 11.3 against 9.8.
+    const bool one = tokens <= 16 ||  // (which is what needs no workspace)
+                     (fits16 && tokens <= ROUTE_ONE && tokens << per_lane(16) <= (r.bias ? 512 : 1024));
     const bool lanes64 = !fits16 || tokens <= 4 || (!one && tokens <= 4 * ROUTE_SUPER);
     a.lanes_per_group = (lanes64 ? 64 : 16) / padded;
     const int v = per_lane(lanes64 ? 64 : 16);
