@@ -172,6 +172,29 @@ def test_grouped_act(h, dtype, trans, gated, tile):
 
 
 @gpu
+@pytest.mark.parametrize("tile", [t for t in TILES if t[0] >= 64])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_every_number_of_steps(h, dtype, gated, tile):
+    """Whole steps of K, one to 21 of 32 (a tile may begin anywhere in K), by groups
+    of one row of tiles and of several."""
+    require_gpu()
+    ti, to = TYPES[dtype]
+    sizes, N = [40, 0, 64, 5, 260, 1], 600
+    M, G, W = sum(sizes), len(sizes), N * (2 if gated else 1)
+    assert g().gemm_set_group_tile_nth(h, *tile) == g().GEMM_OK
+    off = torch.tensor(bounds_of(sizes, 0), dtype=torch.int32, device="cuda")
+    for steps in range(1, 22):
+        K = 32 * steps
+        announce("steps", dtype, gated, tile, K)
+        A, B = draw((M, K), 1, ti), (draw((G, W, K), 2, ti).float() / math.sqrt(K)).to(ti)
+        D = torch.empty(M, N, dtype=to, device="cuda")
+        g().run_grouped_act(h, A.cuda(), B.cuda(), D, off, activation="silu", gated=gated, transB="T")
+        (d, td), _, _ = reference(A, B, sizes, 0, "T", 1.0, None, None, gated, "silu", None, to)
+        within(D, d, td, (to, f"D of K {K}"))
+
+
+@gpu
 @pytest.mark.parametrize("name", ACTS)
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("dtype", list(TYPES))
