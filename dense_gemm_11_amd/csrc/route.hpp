@@ -486,6 +486,8 @@ __device__ __forceinline__ void route_exact(const RouteArgs& p, int group_lanes,
     };
     K c[V];
     if constexpr (BIAS) {
+        float b[V];
+        load_part(b, p.bias + (in.count > 0 ? in.e0 : 0), in.count, 0.0f);
         double sum = 0.0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -496,7 +498,7 @@ __device__ __forceinline__ void route_exact(const RouteArgs& p, int group_lanes,
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             if (!p.sigmoid) c[i] /= sum;
-            c[i] += i < in.count ? (double)p.bias[in.e0 + i] : 0.0;
+            c[i] += b[i];
             c[i] = in.x[i] > -__builtin_inff() && c[i] > key_low<K>() ? c[i] : key_low<K>();
         }
     } else {
