@@ -157,6 +157,8 @@ CASES = [
     (4097, 33, 5, dict(renorm=True)),
     (20000, 30, 2, dict(groups=15, top_groups=7, group_top=2, bias=True)),
     (33000, 12, 3, {}),
+    (6000, 512, 10, dict(bias=True)),
+    (8193, 64, 15, dict(kind="sigmoid", bias=True, groups=4, top_groups=2, group_top=2)),
 ]
 
 
