@@ -74,7 +74,7 @@ def _compile_bind() -> str:
 
     rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
     obj = os.path.join(BUILD, "bind.o")
-    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w",
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
            "-D__HIP_PLATFORM_AMD__=1", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            "-I", INCLUDE, "-isystem", os.path.join(rocm, "include"),
            "-isystem", sysconfig.get_paths()["include"]]

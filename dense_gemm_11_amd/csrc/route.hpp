@@ -26,7 +26,7 @@
 // one to a lane, are compared for certain (route_rank).  A token for which that is
 // not enough (three so close, sums of groups, softmax scores with a bias that 32
 // bits cannot tell apart) is chosen for again in 64 bits by a wave of its own once
-// its workgroup is done with the others (route_exact), about 5 us more for a launch.
+// its workgroup is done with the others (route_exact), 3 to 4 us more for a launch.
 #pragma once
 
 #include "common.hpp"
