@@ -64,17 +64,27 @@ __device__ __forceinline__ float normal_cdf(float x)
 // 2 sqrt(2 / pi): gelu by tanh is x s(TANH_C (x + 0.044715 x^3)).
 constexpr float TANH_C = 1.59576912160573080f, TANH_K = 0.044715f;
 
+// What s is taken of: x for silu (and not the cubic by a factor of 0, which makes a
+// NaN of an infinite x), and its slope, with the square kept finite.
+__device__ __forceinline__ float sigmoid_argument(float x, int act)
+{
+    return act == EPI_ACT_SILU ? x : TANH_C * (x + TANH_K * x * x * x);
+}
+__device__ __forceinline__ float argument_slope(float x, int act)
+{
+    return act == EPI_ACT_SILU ? 1.0f : TANH_C * (1.0f + 3.0f * TANH_K * fminf(x * x, 3e38f));
+}
+
 // act(x); act is uniform across a launch.
 template <bool PRECISE>
 __device__ __forceinline__ f32x4 act_value4(f32x4 x, int act)
 {
     f32x4 r = x;
     if (act == EPI_ACT_SILU || act == EPI_ACT_GELU_TANH) {
-        const float k = act == EPI_ACT_SILU ? 0.0f : TANH_K, c = act == EPI_ACT_SILU ? 1.0f : TANH_C;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float s, rest;
-            sigmoids<PRECISE>(c * (x[i] + k * x[i] * x[i] * x[i]), s, rest);
+            sigmoids<PRECISE>(sigmoid_argument(x[i], act), s, rest);
             r[i] = x[i] * s;
         }
     } else if (act == EPI_ACT_GELU) {
@@ -94,12 +104,10 @@ __device__ __forceinline__ void act_slope(float x, int act, float& value, float&
     value = x;
     slope = 1.0f;
     if (act == EPI_ACT_SILU || act == EPI_ACT_GELU_TANH) {
-        const float k = act == EPI_ACT_SILU ? 0.0f : TANH_K, c = act == EPI_ACT_SILU ? 1.0f : TANH_C;
         float s, rest;
-        sigmoids<PRECISE>(c * (x + k * x * x * x), s, rest);
+        sigmoids<PRECISE>(sigmoid_argument(x, act), s, rest);
         value = x * s;
-        // (the square kept finite: far out value * rest is 0)
-        slope = s + value * rest * (c * (1.0f + 3.0f * k * fminf(x * x, 3e38f)));
+        slope = s + value * rest * argument_slope(x, act);  // (far out value * rest is 0)
     } else if (act == EPI_ACT_GELU) {
         const float phi = normal_cdf<PRECISE>(x), q = -0.5f * x * x;
         const float e = PRECISE ? expf(q) : __builtin_amdgcn_exp2f(q * 1.44269504088896341f);

@@ -358,6 +358,42 @@ def test_values_and_slopes_far_out(h, dtype):
         assert torch.equal(dZ, up) and torch.equal(H.cpu().to(to), x.clamp_min(0.0)), name
 
 
+def infinite_products(h, dtype, name, gated):
+    """A product of zeros with inf, -inf and NaN as its bias, and its gradient: (D, Z,
+    dZ, H) and, by the formulas in 64 bits, what they are."""
+    ti, to = TYPES[dtype]
+    inf, nan = float("inf"), float("nan")
+    z = torch.tensor([inf, -inf, nan, 0.0] * 3 + [inf])
+    n = len(z)
+    u = torch.tensor([2.0] * 4 + [-2.0] * 4 + [1.0] * 5)
+    bias = (torch.cat([z, u]) if gated else z).to(to)
+    M, W = 37, len(bias)
+    D, Z = torch.empty(M, n, dtype=to, device="cuda"), torch.empty(M, W, dtype=to, device="cuda")
+    A, B = torch.zeros(M, 40, dtype=ti, device="cuda"), torch.ones(W, 40, dtype=ti, device="cuda")
+    g().run_grouped_act(h, A, B, D, None, activation=name, gated=gated, bias=bias.cuda(), Z=Z, transB="T")
+    dZ, H = (torch.empty(M, k, dtype=ti, device="cuda") for k in (W, n))
+    g().run_grouped_act_grad(h, Z, torch.ones_like(D), dZ, None, activation=name, gated=gated, H=H)
+    v, s = act(z.double(), name), slope(z.double(), name)
+    u = u.double() if gated else torch.ones_like(v)
+    want = (v * u, bias.double(), torch.cat([s * u, v]) if gated else s, v * u)
+    return [x.double().cpu() for x in (D, Z, dZ, H)], [w.expand(M, -1) for w in want]
+
+
+@gpu
+@pytest.mark.parametrize("tile", [(0, 0), (16, 0), (128, 0)])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("name", ["none", "gelu", "silu", "gelu_tanh"])
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_infinities_and_nan(h, dtype, name, gated, tile):
+    """What the formulas give: act(inf) is inf, act(-inf) NaN (inf times 0), and so
+    are the slopes at either, but for no activation."""
+    require_gpu()
+    announce("infinities", dtype, name, gated, tile)
+    assert g().gemm_set_group_tile_nth(h, *tile) == g().GEMM_OK
+    for what, got, want in zip(("D", "Z", "dZ", "H"), *infinite_products(h, dtype, name, gated)):
+        torch.testing.assert_close(got, want, rtol=0, atol=0, equal_nan=True, msg=lambda m: f"{what}: {m}")
+
+
 @gpu
 def test_act_grad_stays_inside_with_offsets_that_descend(h):
     """Groups that share rows make more tiles than the workspace has rows: their
