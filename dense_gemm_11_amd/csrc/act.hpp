@@ -92,7 +92,7 @@ __device__ __forceinline__ f32x4 act_value4(f32x4 x, int act)
         for (int i = 0; i < 4; ++i) r[i] = x[i] * normal_cdf<PRECISE>(x[i]);
     } else if (act == EPI_ACT_RELU) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = x[i] > 0.0f ? x[i] : 0.0f;
+        for (int i = 0; i < 4; ++i) r[i] = x[i] <= 0.0f ? 0.0f : x[i];  // (a NaN stays)
     }
     return r;
 }
@@ -115,7 +115,7 @@ __device__ __forceinline__ void act_slope(float x, int act, float& value, float&
         slope = phi + x * (e * 0.39894228040143268f);
     } else if (act == EPI_ACT_RELU) {
         slope = x > 0.0f ? 1.0f : 0.0f;
-        value = x > 0.0f ? x : 0.0f;
+        value = x <= 0.0f ? 0.0f : x;
     }
 }
 

@@ -498,6 +498,7 @@ gemm_status_t gemm_last_group_launch(gemm_handle_t h, gemm_group_launch_t* out);
  *                to is rejected.
  * An infinite or NaN Z gives what these formulas give: GELU, SILU and GELU_TANH of
  * +inf are +inf, of -inf (infinity times 0) NaN, and so are their slopes at either.
+ * Every activation of a NaN is NaN, RELU's too (gemm_run_epilogue's gives 0).
  * K == 0 or alpha == 0: Z = bias, and A and B are not read.  Rows in no group are
  * not written.  Otherwise as gemm_run_grouped, with N up to 2^30 - 257, and gated
  * B's panel of both halves below 4 GiB; D, Z, R and bias must be element-aligned

@@ -395,6 +395,17 @@ def test_infinities_and_nan(h, dtype, name, gated, tile):
 
 
 @gpu
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_relu_of_infinities_and_nan(h, dtype, gated):
+    """max(x, 0) of a NaN is NaN, of -inf 0; relu' is 1 above 0 and else 0."""
+    require_gpu()
+    announce("relu of nan", dtype, gated)
+    for what, got, want in zip(("D", "Z", "dZ", "H"), *infinite_products(h, dtype, "relu", gated)):
+        torch.testing.assert_close(got, want, rtol=0, atol=0, equal_nan=True, msg=lambda m: f"{what}: {m}")
+
+
+@gpu
 def test_act_grad_stays_inside_with_offsets_that_descend(h):
     """Groups that share rows make more tiles than the workspace has rows: their
     sums are anything, but nothing beyond the rows, the sums and the workspace is
