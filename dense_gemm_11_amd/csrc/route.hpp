@@ -375,7 +375,9 @@ __device__ __forceinline__ int route_quick(const RouteArgs& p, const TokenPart<X
                 f = p.sigmoid ? quick_sigmoid(f) : quick_exp_below(f, most);
                 g = p.sigmoid ? quick_sigmoid(g) : quick_exp_below(g, most);
             }
-            score = order_key(b >= LEAST ? f + g : f);
+            // (two live choices stay a live sum, however low: below the lowest number
+            // sums are as good as equal)
+            score = order_key(b >= LEAST ? fmaxf(f + g, -0x1.fffffep127f) : f);
             if constexpr (BIAS) size = fmaxf(fabsf(f), b >= LEAST ? fabsf(g) : 0.0f);
         }
         bool kept = false;

@@ -239,6 +239,26 @@ def test_route_sums_of_choices_far_larger_than_themselves(kind):
 
 
 @gpu
+@pytest.mark.parametrize("T", [1, 90, 3000])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_route_groups_whose_sums_pass_fp32(dtype, kind, T):
+    """Biases that mask whole groups by the type's lowest numbers: two of them sum
+    below -FLT_MAX, which in 64 bits is a number like any other, so these groups are
+    kept where too few others are."""
+    require_gpu()
+    announce("route sums past fp32", dtype, kind, T)
+    x = draw(T, 32, dtype, 7, False)
+    low = torch.finfo(torch.float32).min
+    x[::3, 4:8] = -float("inf")                      # a group of none at all
+    for masks in ([low] * 7, [-3e38, low, -2.5e38, low, -2.9e38, low, -1.9e38], [low, -2.0, low, low, low, 0.0, low]):
+        bias = torch.cat([torch.zeros(4), torch.tensor(masks).repeat_interleave(4)])
+        for top_groups, top in ((1, 2), (3, 10), (6, 15)):
+            opt = dict(kind=kind, bias=bias.cuda(), groups=8, top_groups=top_groups, group_top=2)
+            check(x, run(x.cuda(), top, **opt), top, **opt)
+
+
+@gpu
 def test_route_without_plan_without_tokens_and_on_a_stream():
     require_gpu()
     announce("route without plan")
