@@ -406,6 +406,33 @@ def test_relu_of_infinities_and_nan(h, dtype, gated):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", ["bf16", "bf16_out"])
+def test_gelu_keeps_its_relative_accuracy_in_the_tail(h, dtype):
+    """gelu and its slope from -12.5 on: D with bf16 outputs, H and dZ of bf16
+    operands.  Phi's tail is off by 2^-17 of itself by its formula, by a^2 2^-22 <
+    2^-15 for the roundings of the argument of e^(-a^2) with a = |x| / sqrt 2 up to
+    8.9, and a few units of 2^-23: 2^-14 in all, beside the output's half step.  The
+    slope is a difference of Phi and |x| times the density, off by as much of each
+    of them.  (x itself is a bf16 number.)"""
+    require_gpu()
+    announce("gelu tail", dtype)
+    ti, to = TYPES[dtype]
+    x = torch.cat([torch.linspace(-12.5, -2, 3001), torch.linspace(-2, 0, 500)]).bfloat16()[:, None]
+    D, Z = (torch.empty(len(x), 1, dtype=to, device="cuda") for _ in range(2))
+    one = torch.ones(1, 1, dtype=ti, device="cuda")
+    g().run_grouped_act(h, x.cuda(), one, D, None, activation="gelu", Z=Z)
+    assert torch.equal(Z.cpu(), x.to(to))
+    dZ, H = (torch.empty(len(x), 1, dtype=ti, device="cuda") for _ in range(2))
+    g().run_grouped_act_grad(h, Z, torch.ones_like(D), dZ, None, activation="gelu", H=H)
+    x = x.double()
+    val, phi = act(x, "gelu"), 0.5 * torch.erfc(-x / math.sqrt(2.0))
+    within(D, val, 2.0 ** -14 * val.abs(), (to, "D"))
+    within(H, val, 2.0 ** -14 * val.abs(), (ti, "H"))
+    s = slope(x, "gelu")
+    within(dZ, s, 2.0 ** -14 * (phi + (s - phi).abs()), (ti, "dZ"))
+
+
+@gpu
 def test_act_grad_stays_inside_with_offsets_that_descend(h):
     """Groups that share rows make more tiles than the workspace has rows: their
     sums are anything, but nothing beyond the rows, the sums and the workspace is
