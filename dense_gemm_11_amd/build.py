@@ -2,13 +2,16 @@
 
 Each source in csrc/ is compiled to an object under _build/ (in parallel),
 then the objects are linked into one shared library.  csrc/bind.cpp, the native
-part of the Python binding, becomes the extension module _bind beside it.  Every HIP compile uses
+part of the Python binding, becomes the extension module _bind beside it, where
+torch is installed (without it there are no tensors to check, and the raw calls
+are all there is).  Every HIP compile uses
 -Xclang -target-feature -Xclang -packed-fp32-ops, which keeps the compiler
 from emitting packed FP32 instructions.
 """
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -103,13 +106,16 @@ def build(extra_flags=(), jobs: int = 0) -> str:
     os.makedirs(BUILD, exist_ok=True)
     jobs = jobs or min(len(SOURCES), os.cpu_count() or 4)
     with concurrent.futures.ThreadPoolExecutor(jobs) as ex:
-        bind = ex.submit(_compile_bind)
+        bind = ex.submit(_compile_bind) if importlib.util.find_spec("torch") else None
         objs = list(ex.map(lambda s: _compile(s, extra_flags), SOURCES))
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
-    _link_bind(bind.result())
+    if bind:
+        _link_bind(bind.result())
+    elif os.path.exists(BIND):
+        os.remove(BIND)  # of an earlier build, for another library
     return LIB
 
 
