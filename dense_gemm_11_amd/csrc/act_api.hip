@@ -188,21 +188,19 @@ gemm_status_t gemm_run_grouped_act_grad(gemm_handle_t h, int64_t M, int64_t N,
     if (M > MAX_EXTENT || ldz > INT_MAX || lddd > INT_MAX || lddz > INT_MAX || (H && ldh > INT_MAX) ||
         G > MAX_GROUPS)
         return GEMM_ERR_NOT_SUPPORTED;
-    if (M > 0) {
-        // dZ may be Z and H may be dD, of one type; else everything lies apart
-        const int64_t sz = span(M, ldz, width, eo), sd = span(M, lddd, N, eo), so = span(M, lddz, width, es);
-        const int64_t sh = H ? span(M, ldh, N, es) : 0;
-        if (!in_place_or_apart(Z, sz, dZ, so, ldz == lddz && es == eo) || ranges_overlap(dD, sd, dZ, so) ||
-            (H && (!in_place_or_apart(dD, sd, H, sh, lddd == ldh && es == eo) ||
-                   ranges_overlap(Z, sz, H, sh) || ranges_overlap(dZ, so, H, sh))))
-            return GEMM_ERR_INVALID_VALUE;
-        const int64_t sb = dbias ? G * width * 4 : 0;
-        if (dbias && (ranges_overlap(dbias, sb, Z, sz) || ranges_overlap(dbias, sb, dD, sd) ||
-                      ranges_overlap(dbias, sb, dZ, so) || (H && ranges_overlap(dbias, sb, H, sh))))
-            return GEMM_ERR_INVALID_VALUE;
-    }
-    if (dbias && M > 0 &&
-        (!ws || !aligned_to(ws, 256) || ws_bytes < gemm_act_grad_workspace_bytes(M, width, (int)G)))
+    const size_t needed = dbias && M > 0 ? gemm_act_grad_workspace_bytes(M, width, (int)G) : 0;
+    if (needed && (!ws || !aligned_to(ws, 256) || ws_bytes < needed)) return GEMM_ERR_INVALID_VALUE;
+    // dZ may be Z and H may be dD, of one type; else what is written lies apart
+    const int64_t sz = M > 0 ? span(M, ldz, width, eo) : 0, sd = M > 0 ? span(M, lddd, N, eo) : 0;
+    const int64_t so = M > 0 ? span(M, lddz, width, es) : 0, sh = M > 0 && H ? span(M, ldh, N, es) : 0;
+    const MemoryRange off{groups ? groups->offsets : nullptr, (G + 1) * 4};
+    if (M > 0 && (!in_place_or_apart(Z, sz, dZ, so, ldz == lddz && es == eo) ||
+                  (H && !in_place_or_apart(dD, sd, H, sh, lddd == ldh && es == eo)) ||
+                  written_overlap({{dZ, so}, {H, sh}, {dD, sd}, off}, 1) ||
+                  written_overlap({{H, sh}, {Z, sz}, off}, 1)))
+        return GEMM_ERR_INVALID_VALUE;
+    if (written_overlap({{dbias, G * width * 4}, {needed ? ws : nullptr, (int64_t)needed}, {dZ, so}, {H, sh},
+                         {Z, sz}, {dD, sd}, off}, 2))
         return GEMM_ERR_INVALID_VALUE;
     if (!aligned_to(Z, eo) || !aligned_to(dD, eo) || !aligned_to(dZ, es) || !aligned_to(H, es) ||
         !aligned_to(dbias, 4) || (groups && !aligned_to(groups->offsets, 4)))

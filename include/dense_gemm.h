@@ -534,7 +534,8 @@ gemm_status_t gemm_run_grouped_act(gemm_handle_t h, gemm_op_t transB, int64_t M,
  * of gemm_act_grad_workspace_bytes(M, width of Z, groups) bytes, 256-byte
  * aligned (GEMM_ERR_INVALID_VALUE otherwise), which needs no clearing; calls that
  * may overlap in time need one each.  dZ may be Z, and H may be dD, where they
- * have one type and leading dimension; any other overlap of what is written is
+ * have one type and leading dimension; any other overlap of what is written (dbias
+ * and those bytes of the workspace among it) with another tensor or the offsets is
  * rejected.  Rows in no group are not written.  (With offsets that decrease the dbias
  * of groups that share rows is undefined.)  Results are bitwise reproducible. */
 size_t gemm_act_grad_workspace_bytes(int64_t M, int64_t width, int groups);

@@ -548,6 +548,43 @@ def test_act_grad_refusals(h):
     assert grad(h, M=0, Z=None, dbias=None) == m.GEMM_OK
 
 
+def test_act_grad_refuses_a_workspace_and_offsets_that_overlap(monkeypatch):
+    """50 rows, Z of 16 columns, 2 groups: what is written, the workspace's used part and
+    dbias among it, lies apart from all else.  (The handle fails the launch of what
+    passes.)"""
+    monkeypatch.setenv("GEMM_DEBUG_FAIL_LAUNCH", "1")
+    m = g()
+    bad, passed = m.GEMM_ERR_INVALID_VALUE, m.GEMM_ERR_HIP
+    z, dd, dz, hh, db, ws = [FAKE + (i << 30) for i in range(6)]
+    far = FAKE + (8 << 30)
+    need = m.gemm_act_grad_workspace_bytes(50, 16, 2)
+    assert 256 < need < 512 and need % 4 == 0
+
+    def grad_of(**kw):
+        return grad(handle, M=50, **kw)
+
+    handle = m.gemm_create()
+    try:
+        # Z, dZ: 1600 bytes of bf16; dD, H: 800; dbias: 128; offsets: 12
+        for at in (z, z + 1536, z - 256, dd, dz, dz + 1536, hh, db - 256, db):
+            assert grad_of(ws=at) == bad, hex(at)
+        for at in (db, db + 124, db - 8, dz + 1596, hh + 796, dz - 8, ws, ws + need - 4):
+            assert grad_of(groups=(2, at, None)) == bad, hex(at)
+        # side by side; a larger workspace counts by what is used of it
+        assert grad_of(ws=far, dbias=far + need) == passed
+        assert grad_of(ws=far, dZ=far - 1600, groups=(2, far + need, None)) == passed
+        assert grad_of(ws=far, dZ=far + need) == passed
+        assert grad_of(groups=(2, db + 128, None)) == passed
+        # without dbias the workspace is not used; without offsets none are read
+        assert grad_of(ws=dz, dbias=None) == passed
+        assert grad_of(groups=()) == passed
+        # in place (the offsets, by default where Z is, elsewhere)
+        assert grad_of(dZ=z, H=dd, groups=(2, far, None)) == passed
+        assert grad_of(dZ=z, H=dd) == bad
+    finally:
+        m.gemm_destroy(handle)
+
+
 def test_act_failed_launches_are_reported(monkeypatch):
     monkeypatch.setenv("GEMM_DEBUG_FAIL_LAUNCH", "1")
     handle = g().gemm_create()
