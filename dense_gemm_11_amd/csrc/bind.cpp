@@ -154,17 +154,19 @@ int64_t columns(PyObject* o, const char* name)
 }
 int as_int(int64_t v) { return v > INT32_MAX ? -1 : (int)v; }
 
+// A workspace, whose bytes count from its first one.
 struct Workspace {
-    void* p = nullptr;
-    size_t bytes = 0;
-    Workspace(PyObject* o, const Device& device)
+    const at::Tensor* t;
+    explicit Workspace(PyObject* o) : t(maybe(o, "workspace"))
     {
-        if (const at::Tensor* t = maybe(o, "workspace")) {
-            device.holds(*t, "the workspace");
-            p = t->data_ptr();
-            bytes = t->nbytes();
-        }
+        if (t && !t->is_contiguous()) wrong_value("the workspace must be contiguous");
     }
+    void* on(const Device& device) const
+    {
+        if (t) device.holds(*t, "the workspace");
+        return t ? t->data_ptr() : nullptr;
+    }
+    size_t bytes() const { return t ? t->nbytes() : 0; }
 };
 
 // GROUPS: offsets of `groups` groups (None: no groups) and their scales.
@@ -195,18 +197,18 @@ int route(PyObject* const* a)
     const gemm_dtype_t dtype = logits_type(x);
     const Matrix m = matrix(x, "logits");
     const int64_t top = columns(a[3], "ids"), T = m.rows, E = m.cols;
+    const Workspace ws(a[8]);
     const Device device(x);
     if ((a[5] == Py_None) != (a[6] == Py_None) || (a[6] == Py_None) != (a[7] == Py_None))
         wrong_value("offsets, order and position come together");
     const gemm_routing_t r{as_int(E), as_int(top), (gemm_scores_t)small(a[9]), small(a[11]), small(a[12]),
                            small(a[13]), packed_as<float>(a[10], E, -1, device, "bias"), truth(a[14]),
                            number(a[15])};
-    const Workspace ws(a[8], device);
     return gemm_route(HANDLE, T, m.p, m.ld, dtype, &r, packed_as<int32_t>(a[3], T, top, device, "ids"),
                       packed_as<float>(a[4], T, top, device, "weights"),
                       packed_as<int32_t>(a[5], E + 1, -1, device, "offsets"),
                       packed_as<int32_t>(a[6], T * top, -1, device, "order"),
-                      packed_as<int32_t>(a[7], T, top, device, "position"), ws.p, ws.bytes, STREAM);
+                      packed_as<int32_t>(a[7], T, top, device, "position"), ws.on(device), ws.bytes(), STREAM);
 }
 
 // logits, ids, dweights, dlogits, scores, renormalize, scale
@@ -336,6 +338,7 @@ int grouped_act_grad(PyObject* const* a)
     const gemm_dtype_t dtype = two_types(ti, Z.scalar_type());
     const Matrix mz = matrix(Z, "Z"), md = matrix(dD, "dD");
     const bool gated = truth(a[7]);
+    const Workspace ws(a[10]);
     if (md.rows != mz.rows || mz.cols != (gated ? 2 : 1) * md.cols) wrong_value("inconsistent shapes of Z and dD");
     const Device device(Z);
     device.holds(dD, "dD");
@@ -348,11 +351,10 @@ int grouped_act_grad(PyObject* const* a)
         G = offsets.size(0) - 1;
     }
     const Groups groups(a[5], Py_None, G, device);
-    const Workspace ws(a[10], device);
     return gemm_run_grouped_act_grad(HANDLE, mz.rows, md.cols, (gemm_activation_t)small(a[6]), gated, mz.p,
                                      mz.ld, md.p, md.ld, mdz.p, mdz.ld, mh.p, mh.ld,
                                      packed_as<float>(a[9], G, mz.cols, device, "dbias"), dtype, groups.get(),
-                                     ws.p, ws.bytes, STREAM);
+                                     ws.on(device), ws.bytes(), STREAM);
 }
 
 template <int (*F)(PyObject* const*), int ARGS>

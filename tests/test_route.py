@@ -511,3 +511,17 @@ def test_binding_refuses_wrong_tensors(h):
         m.run_route_grad(h, x.double(), ids, w, x)
     with pytest.raises(ValueError):
         m.run_route_grad(h, x, ids, w, x[:, :4])
+
+
+def test_workspaces_that_are_not_contiguous_are_refused(h):
+    """(Their numel is not what lies behind their first byte; seen before the
+    tensors' device is, which here is the host.)"""
+    m = g()
+    x, ids, w = torch.zeros(40, 8), torch.zeros(40, 2, dtype=torch.int32), torch.zeros(40, 2)
+    plan = (torch.zeros(9, dtype=torch.int32), torch.zeros(80, dtype=torch.int32), torch.zeros_like(ids))
+    for ws in (torch.zeros(256, dtype=torch.uint8).expand(256, 256), torch.zeros(1, dtype=torch.uint8).expand(1 << 20),
+               torch.zeros(64, 512, dtype=torch.uint8)[:, :256]):
+        with pytest.raises(ValueError, match="contiguous"):
+            m.run_route(h, x, ids, w, *plan, workspace=ws)
+        with pytest.raises(ValueError, match="contiguous"):
+            m.run_grouped_act_grad(h, x, x.clone(), x.clone(), dbias=torch.zeros(1, 8), workspace=ws)
