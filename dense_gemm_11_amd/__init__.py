@@ -762,6 +762,8 @@ def run_lora(h, A, B, D, offsets, down, up, workspace, ids=None, scales=None, C=
             raise ValueError("inconsistent low-rank adapter shapes")
     if Kb != K or Md != M or Nd != N or Kd != K or adapters_up != adapters or Nu != N or Ru != R:
         raise ValueError("inconsistent low-rank adapter shapes")
+    if not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
     device = _device_of(D, A, B, C, down, up, workspace)
     if offsets.dim() != 1 or offsets.shape[0] < 1:
         raise ValueError("offsets must hold segments + 1 entries")

@@ -272,3 +272,17 @@ def test_host_tensors_are_refused():
                          torch.zeros(4096, dtype=torch.uint8))
     finally:
         g().gemm_destroy(h)
+
+
+def test_lora_refuses_a_workspace_that_is_not_contiguous():
+    """(Its numel is not what lies behind its first byte; seen before the tensors'
+    device is, which here is the host.)"""
+    h = g().gemm_create()
+    A, B, D = torch.zeros(4, 6), torch.zeros(6, 5), torch.zeros(4, 5)
+    off = torch.zeros(3, dtype=torch.int32)
+    try:
+        for ws in (torch.zeros(1, dtype=torch.uint8).expand(4096), torch.zeros(64, 128, dtype=torch.uint8)[:, :64]):
+            with pytest.raises(ValueError, match="contiguous"):
+                g().run_lora(h, A, B, D, off, torch.zeros(2, 3, 6), torch.zeros(2, 5, 3), ws)
+    finally:
+        g().gemm_destroy(h)
