@@ -259,6 +259,29 @@ def test_route_groups_whose_sums_pass_fp32(dtype, kind, T):
 
 
 @gpu
+@pytest.mark.parametrize("T,E,top", [(16, 1024, 32), (16, 64, 4), (1, 256, 8), (9, 33, 15), (5, 1024, 1)])
+@pytest.mark.parametrize("opt", [dict(), dict(kind="sigmoid", renorm=True, bias=True)], ids=["plain", "bias"])
+def test_route_up_to_16_tokens_needs_no_workspace(T, E, top, opt):
+    require_gpu()
+    announce("route without workspace", T, E, top, opt)
+    opt = dict(opt)
+    x = draw(T, E, "f32", 11, False)
+    if opt.pop("bias", False):
+        opt["bias"] = torch.randn(E, generator=torch.Generator().manual_seed(12)).cuda() * 0.2
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ids, w = torch.full((T, top), 99, **i32), torch.full((T, top), 9.0, device="cuda")
+    plan = [torch.full((E + 1,), 99, **i32), torch.full((T * top,), 99, **i32), torch.full((T, top), 99, **i32)]
+    handle = g().gemm_create()
+    try:
+        g().run_route(handle, x.cuda(), ids, w, *plan, scores=opt.get("kind", "softmax"), bias=opt.get("bias"),
+                      renormalize=opt.get("renorm", False))
+        torch.cuda.synchronize()
+    finally:
+        g().gemm_destroy(handle)
+    check(x, [v.cpu().numpy() for v in (ids, w, *plan)], top, **opt)
+
+
+@gpu
 def test_route_without_plan_without_tokens_and_on_a_stream():
     require_gpu()
     announce("route without plan")
@@ -465,6 +488,24 @@ def test_route_fails_its_launch_on_request(monkeypatch):
     assert call(handle) == g().GEMM_ERR_HIP
     assert call(handle, tokens=0, offsets=None, order=None, position=None) == g().GEMM_OK
     g().gemm_destroy(handle)
+
+
+def test_route_workspace_is_asked_for_beyond_16_tokens_only(monkeypatch):
+    """By what the host refuses: the handle fails the launch of what passes."""
+    monkeypatch.setenv("GEMM_DEBUG_FAIL_LAUNCH", "1")
+    handle = g().gemm_create()
+    none = dict(offsets=None, order=None, position=None)
+    try:
+        for experts, top in ((16, 2), (1024, 32), (1, 1)):
+            r = dict(experts=experts, top=top)
+            for tokens in (1, 2, 15, 16):
+                assert call(handle, r, tokens=tokens, ld=experts, ws=None, ws_bytes=0) == g().GEMM_ERR_HIP
+            for tokens in (17, 100, 5000):
+                assert call(handle, r, tokens=tokens, ld=experts, ws=None,
+                            ws_bytes=0) == g().GEMM_ERR_INVALID_VALUE
+                assert call(handle, r, tokens=tokens, ld=experts, ws=None, ws_bytes=0, **none) == g().GEMM_ERR_HIP
+    finally:
+        g().gemm_destroy(handle)
 
 
 def test_route_workspace_grows_with_the_tokens():
