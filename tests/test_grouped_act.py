@@ -234,6 +234,48 @@ def test_activations_over_their_range(h, dtype):
         within(D, val, own_error(to) * x.double().abs()[:, None], (to, name))
 
 
+# tiles of each height (TILES names up to two of them), by the operands' type
+HEIGHTS = {"bf16": {256: 1, 192: 1, 128: 2, 64: 2, 32: 2, 16: 2}, "f32": {128: 1, 64: 1, 32: 2, 16: 2}}
+
+
+def forced_tile(dtype, tile):
+    """(rows, nth) of the tile that gemm_set_group_tile_nth(*tile) makes a call take: of
+    the tallest height not above, the nth or else its last."""
+    table = HEIGHTS["f32" if dtype == "f32" else "bf16"]
+    rows = max(r for r in table if r <= tile[0])
+    return rows, min(tile[1], table[rows] - 1)
+
+
+@gpu
+@pytest.mark.parametrize("tile", TILES[1:])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("trans", ["N", "T"])
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_the_forced_tile_is_the_one_that_runs(h, dtype, trans, gated, tile):
+    """As the tests above force them: heights, numbers and columns of what ran, and that
+    every one of a type's tiles is among them."""
+    require_gpu()
+    announce("forced tile", dtype, trans, gated, tile)
+    ti, to = TYPES[dtype]
+    rows, nth = forced_tile(dtype, tile)
+    assert g().gemm_set_group_tile_nth(h, *tile) == g().GEMM_OK
+    seen = set()
+    for M, N, K in ((300, 600, 160), (5, 34, 33)):
+        W = N * (2 if gated else 1)
+        A, B = draw((M, K), 1, ti).cuda(), draw((1, K, W) if trans == "N" else (1, W, K), 2, ti).cuda()
+        D = torch.empty(M, N, dtype=to, device="cuda")
+        off = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+        for offsets in (off, None):
+            g().run_grouped_act(h, A, B, D, offsets, activation="silu", gated=gated, transB=trans)
+            x = g().gemm_last_group_launch(h)
+            assert (x.rows, x.nth, x.launches) == (rows, nth, 1) and g().gemm_last_group_tile(h) == rows
+            seen.add(x.columns)
+    assert len(seen) == 1
+    reached = {forced_tile(dtype, t) for t in TILES[1:]}
+    table = HEIGHTS["f32" if dtype == "f32" else "bf16"]
+    assert reached == {(r, i) for r in table for i in range(table[r])}
+
+
 @gpu
 def test_act_empty_calls_and_empty_groups(h):
     require_gpu()
