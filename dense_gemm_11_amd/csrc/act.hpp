@@ -13,8 +13,8 @@
 //
 // The products bound it as they do without all this: 384 rows of 64 experts of
 // 4096 x 2 1792 bf16 read their matrices at 5.7 TB/s (286 us), 16384 rows of 8 of
-// 4096 x 2 14336 take 3.22 ms (1.2 PFLOP/s; even groups 3.11, silu 1 % of it), two of
-// 2048 x 2 1024 a launch and a trip to memory (6.1 us).
+// 4096 x 2 14336 take 3.17 ms (1.2 PFLOP/s; even groups 3.09, silu 1 % of it, gelu 2),
+// two of 2048 x 2 1024 a launch and a trip to memory (6.0 us).
 #pragma once
 
 #include "common.hpp"

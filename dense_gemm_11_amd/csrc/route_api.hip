@@ -140,6 +140,8 @@ gemm_status_t gemm_route(gemm_handle_t h, int64_t tokens, const void* logits, in
     // host) until its passes take longer than that: 96 tokens of 64 experts 6.5 us
     // against 7.1, 64 of 256 experts 8.0 against 7.7 and 96 of them 12.7 against 8.6, 32
     // of 256 in groups with a bias 6.8 against 8.4 and 64 of them 11.3 against 9.8.
+    // (64 of 256 experts gain by it in eager calls alone: a replayed graph's host
+    // time is none, and there they lose 0.3 us.)
     const bool one = tokens <= 16 ||  // (which is what needs no workspace)
                      (fits16 && tokens <= ROUTE_ONE && tokens << per_lane(16) <= (r.bias ? 512 : 1024));
     const bool lanes64 = !fits16 || tokens <= 4 || (!one && tokens <= 4 * ROUTE_SUPER);

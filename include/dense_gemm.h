@@ -499,6 +499,12 @@ gemm_status_t gemm_last_group_launch(gemm_handle_t h, gemm_group_launch_t* out);
  * An infinite or NaN Z gives what these formulas give: GELU, SILU and GELU_TANH of
  * +inf are +inf, of -inf (infinity times 0) NaN, and so are their slopes at either.
  * Every activation of a NaN is NaN, RELU's too (gemm_run_epilogue's gives 0).
+ * Beside Z's own rounding act(Z) is off by at most 2^-20 |Z| with fp32 D and 2^-19
+ * |Z| with bf16 D, whose exponentials and reciprocals are the hardware's; there
+ * GELU's tail (Z from -2 to -12.5) is off by at most 2^-14 of itself.
+ * With transB T the K-step that a row's sum begins with may depend on where its
+ * group's tiles come among all of them, so a group's last bits may differ between
+ * calls whose other groups have other sizes; the same call repeats exactly.
  * K == 0 or alpha == 0: Z = bias, and A and B are not read.  Rows in no group are
  * not written.  Otherwise as gemm_run_grouped, with N up to 2^30 - 257, and gated
  * B's panel of both halves below 4 GiB; D, Z, R and bias must be element-aligned
@@ -537,7 +543,10 @@ gemm_status_t gemm_run_grouped_act(gemm_handle_t h, gemm_op_t transB, int64_t M,
  * have one type and leading dimension; any other overlap of what is written (dbias
  * and those bytes of the workspace among it) with another tensor or the offsets is
  * rejected.  Rows in no group are not written.  (With offsets that decrease the dbias
- * of groups that share rows is undefined.)  Results are bitwise reproducible. */
+ * of groups that share rows is undefined.)  Results are bitwise reproducible.
+ * act and act' are formed as the product's with fp32 D where the operands are fp32,
+ * off by at most 2^-19 (|Z| + 1), and as with bf16 D, off by 2^-18 (|Z| + 1), where
+ * they are bf16, whatever type Z and dD have: so are the terms of an fp32 dbias. */
 size_t gemm_act_grad_workspace_bytes(int64_t M, int64_t width, int groups);
 
 gemm_status_t gemm_run_grouped_act_grad(gemm_handle_t h, int64_t M, int64_t N,
@@ -563,7 +572,10 @@ gemm_status_t gemm_run_grouped_act_grad(gemm_handle_t h, int64_t M, int64_t N,
  * bits; without a bias the logits themselves are compared, in whose order the
  * scores are.
  * The weights are scale * s, or with renormalize scale * s / (sum of the chosen s),
- * in fp32 and formed so that no underflow of s spoils the ratio.
+ * in fp32 and formed so that no underflow of s spoils the ratio.  They are off by at
+ * most 64 + 2 d units of 2^-24 of themselves, with d the largest distance of a chosen
+ * logit from the token's largest, a sigmoid's also from 0 (the exponentials and
+ * reciprocals are the hardware's).
  *
  * An expert whose logit, or c, is NaN or -inf is not chosen; where fewer than
  * `top` are left (none in a row of -inf that pads a batch), ids is -1 and the
@@ -616,7 +628,10 @@ gemm_status_t gemm_route(gemm_handle_t h, int64_t tokens, const void* logits, in
  * and 0 for the others.  Of `routing` experts, top, scores, renormalize and scale
  * are read.  dlogits (rows ldd >= experts apart) has the logits' type and may not
  * overlap an input; every one of its tokens x experts elements is written.  ids outside
- * [0, experts) have no part; an expert named twice gets the sum. */
+ * [0, experts) have no part; an expert named twice gets the sum.  Before its rounding
+ * to the logits' type an element is off by at most 96 + 2 d units of 2^-24 of the
+ * magnitudes that it is a difference of, d the logits' spread (-inf apart), for
+ * the sigmoid with 0 among them. */
 gemm_status_t gemm_route_grad(gemm_handle_t h, int64_t tokens, const void* logits, int64_t ld,
                               gemm_dtype_t dtype, const gemm_routing_t* routing, const int32_t* ids,
                               const float* dweights, void* dlogits, int64_t ldd, hipStream_t stream);
@@ -636,8 +651,8 @@ gemm_status_t gemm_route_grad(gemm_handle_t h, int64_t tokens, const void* logit
  *                            that no position names are left as they were.  dY may be
  *                            Y (one leading dimension).  C's gradient is beta dD.
  * A position outside [0, rows) has no part and a dweights of 0, whatever the rows
- * hold; a row that several positions name is summed from each, and its dY is
- * undefined.  The gradient of gather is combine without weights (and gather of dD
+ * hold; a row that several positions name is summed from each, and its dY (and
+ * where dY is Y, its dweights) is undefined.  The gradient of gather is combine without weights (and gather of dD
  * with weights is the dY above).
  * GEMM_ERR_INVALID_VALUE: negative sizes, top < 1, leading dimensions below cols,
  * a NULL that is needed, outputs that overlap operands otherwise than said.
